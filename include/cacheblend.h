@@ -350,6 +350,92 @@ cb_status cb_hkvd_select_noalloc(const void* v_new, const void* v_old, const int
                                  int32_t k, int32_t n_rows, int32_t hkv, int32_t head_dim,
                                  int32_t* sel_tok, int32_t* sel_row, void* stream);
 
+/* ---- Serving a batch over a paged cache held in 4 bits --------------------------------------
+ * ("rag的kvcache问题" §独立编码: chunk caches are computed on their own and kept; §阶段 2
+ * (Decode): a decode step reads the whole cache, so its bytes set the step's time. The pages give no
+ * cache format, paging or quantisation: the definitions below are this library's.)
+ *
+ * A cache is uint8 [n_pages, hkv, page_bytes], page_bytes = cb_kv4_page_bytes(plan, page_size)
+ * = page_size / 16 * 18 D. A page holds page_size tokens (a multiple of 16, at most
+ * CB_KV4_MAX_PAGE); slot = page * page_size + token in the page. Every 32 dims of a K or V row of one
+ * kv head share a scale: scale = bf16(max|x| / 7), code = round-half-even(x / scale) in -7 .. 7, and
+ * the row stands for scale * code (a group with a NaN or an infinity stands for NaN). For every 16
+ * tokens of a page and kv head there is one record of 18 D bytes: with NG = D / 32,
+ *   K codes at 0:     u32 [token 16][c 4][group NG], dims 32 group + 8 c + e; the dim e = 2 i in bits
+ *                     4 i, e = 2 i + 1 in bits 16 + 4 i, as code + 8;
+ *   V codes at 8 D:   u32 [half 2][r 8][c 4][group NG], tokens 8 half + 2 c (low 16 bits) and + 1
+ *                     (high), dims 32 group + 4 r + i in bits 4 i of its 16, as code + 8;
+ *   scales at 16 D:   bf16 [token 16][K, V][group NG]. */
+#define CB_KV4_MAX_PAGE 1024
+
+/* Bytes of one page of one kv head (a multiple of 16), 0 for a page_size that is not supported. */
+int32_t cb_kv4_page_bytes(const cb_plan* plan, int32_t page_size);
+
+/* Page tables, slot map, packed offsets and positions of one step, built on the device from the
+ * requests' lengths: request s has ctx_lens[s] tokens in the cache and appends new_lens[s] (a prompt's
+ * length, 1 for a decode step, 0 to sit out). With P = page_size and ceil division it holds
+ * ceil(ctx / P) pages and takes the next ceil((ctx + new) / P) - ceil(ctx / P) of
+ * free_pages[free_from ..], request by request; their ids go to its row of table [n_seqs,
+ * table_width], entries of pages that it held stay, and so does the rest of the row. Out:
+ *   cu_seqlens [n_seqs + 1]  exclusive sum of new_lens, at most n_rows (for cb_prompt_attention)
+ *   kv_lens    [n_seqs]      ctx + new (for cb_kv4_decode_attention)
+ *   positions  [n_rows]      position of each packed new token, 0 behind the last one
+ *   slots      [n_rows]      its slot (for cb_kv4_store), -1 behind the last one
+ *   free_to    [1]           free_from + the pages taken
+ * free_from: device int32, NULL = 0. kv_lens must be another buffer than the lengths, free_to another
+ * than free_from. n_seqs is at most CB_PAGE_TABLES_MAX_SEQS. Recorded as CB_ERR_DEVICE_CHECK: a
+ * negative length (taken as 0); a request past table_width * P tokens (its kv_lens is cut there, the
+ * tokens behind get slot -1); a free list that runs out or holds an id below 0 or whose slots would
+ * pass 2^31 - 1 (table entry and slots -1); a token that falls in a held page whose table entry is no
+ * page (slot -1); more new tokens than n_rows (those behind are left out). No scratch: calls on one
+ * plan may overlap. */
+#define CB_PAGE_TABLES_MAX_SEQS 16384
+cb_status cb_page_tables(cb_plan* plan, const int32_t* ctx_lens, const int32_t* new_lens, int32_t n_seqs,
+                         int32_t page_size, const int32_t* free_pages, int32_t n_free, const int32_t* free_from,
+                         int32_t* table, int32_t table_width, int32_t* cu_seqlens, int32_t* kv_lens,
+                         int32_t* positions, int32_t* slots, int32_t n_rows, int32_t* free_to, void* stream);
+
+/* Quantise rows k, v [n, hkv, D] (as attention reads them: keys RoPE-encoded) into the cache at
+ * slots[i]. A negative slot skips its row (padding); one past the cache is skipped and recorded.
+ * Slots of one call must differ (the content of a slot named twice is a mix of its rows). */
+cb_status cb_kv4_store(cb_plan* plan, const void* k, const void* v, const int32_t* slots, int32_t n, void* cache,
+                       int32_t n_pages, int32_t page_size, void* stream);
+
+/* Read rows back: k[i], v[i] [n, hkv, D] = bf16(scale * code) of slots[i], e.g. a stored chunk's
+ * k_old / v_old for cb_blend_layer. A negative slot leaves its rows as they are; one past the cache
+ * too, and is recorded. */
+cb_status cb_kv4_load(cb_plan* plan, const void* cache, int32_t n_pages, int32_t page_size, const int32_t* slots,
+                      int32_t n, void* k, void* v, void* stream);
+
+/* Decode attention of a batch over the 4-bit cache: one new token per request, its own key and
+ * value stored already,
+ *   out[s, h] = sum_{j < kv_lens[s]} softmax_j(scale * q[s, h] . k_j[g]) v_j[g],  g = h / (hq/hkv),
+ * k_j, v_j the rows at slot table[s][j / P] * P + j % P. q, out: [n_seqs, hq, D]; scale <= 0 selects
+ * 1/sqrt(D). A request with kv_lens 0 (a padded batch) gets zeros and its table row is not read; slots
+ * behind a request's length may hold any bytes. Requests may share pages. fp32 scores, softmax and
+ * accumulation; the softmax weights times V's scales are rounded to bf16 before the product.
+ * Recorded as CB_ERR_DEVICE_CHECK: a negative length (as 0), one past table_width * P (cut there), a
+ * table entry outside [0, n_pages) (its keys are left out). Partial results meet in the plan's
+ * scratch: calls of this function on one plan must not overlap on the GPU; order them on one stream,
+ * or give each stream its own plan. */
+cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,
+                                  const int32_t* table, int32_t table_width, const int32_t* kv_lens, int32_t n_seqs,
+                                  float scale, void* out, void* stream);
+
+/* Causal grouped-query attention of whole prompts (or chunks, "rag的kvcache问题" §独立编码), packed one
+ * after the other: sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of q, out [n_rows, hq, D]
+ * and k, v [n_rows, hkv, D], and
+ *   out[t, h] = sum_{j <= t, same sequence} softmax_j(scale * q[t, h] . k[j, g]) v[j, g],  g = h / (hq/hkv),
+ * with q and k RoPE-encoded at their positions. cu_seqlens: device int32 [n_seqs + 1], ascending,
+ * within [0, n_rows]; empty sequences are allowed, and rows in no sequence keep their out. Values of
+ * keys that a row does not see (later ones, other sequences') do not reach it, whatever they are.
+ * scale <= 0 selects 1/sqrt(D). fp32 accumulation and softmax, bf16 P, bf16 output; tcgen05 (TMEM
+ * accumulators) fed by TMA. out must be none of the inputs. Offsets that fall or leave [0, n_rows] are
+ * recorded as CB_ERR_DEVICE_CHECK (clipped, a falling pair read as empty). No scratch: calls on one
+ * plan may overlap. A bounded wait that gives up records CB_ERR_TIMEOUT. */
+cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                              int32_t n_seqs, int32_t n_rows, float scale, void* out, void* stream);
+
 /* Which of the two attention kernels a cb_hkvd_attention call (or a blend
  * layer's attention) of mq query rows runs on the plan's device: 1 for the
  * paired-tile kernel (two 128-row query tiles per CTA whose softmax and

@@ -30,6 +30,9 @@ Parity status per function:
   diagnostics.attention_deviation      pinned (definition, r = 100% gives exactly 0)
   diagnostics.attention_sparsity       pinned (closed form for equal scores, library softmax matrix)
   projection.qkv_projection            pinned (element loops, one-hot rows, RoPE at the row position)
+  serving.quantise / store / load      pinned (hand-worked codes and bytes, round trips, error bound)
+  serving.page_tables                  pinned (hand-worked steps)
+  serving.packed_attention             pinned (each sequence alone)
 """
 
-from . import attention, blend, deviation, diagnostics, fuse, positions, projection, rope, topk  # noqa: F401
+from . import attention, blend, deviation, diagnostics, fuse, positions, projection, rope, serving, topk  # noqa: F401

@@ -18,7 +18,8 @@ from ._lib import CacheBlendError, check
 __all__ = ["Plan", "CacheBlendError", "cb_rope_rerotate", "cb_kv_deviation", "cb_kv_deviation_kv", "cb_hkvd_topk",
            "cb_fuse_scatter", "cb_hkvd_attention", "cb_decode_attention", "cb_attention_sparsity",
            "cb_output_deviation", "cb_qkv_projection", "cb_qkv_projection_indexed", "cb_blend_layer", "cb_blend_stage",
-           "cb_blend_request", "cb_hkvd_select_noalloc", "cb_attention_uses_paired_tiles",
+           "cb_blend_request", "cb_hkvd_select_noalloc", "cb_kv4_page_bytes", "cb_page_tables", "cb_kv4_store",
+           "cb_kv4_load", "cb_kv4_decode_attention", "cb_prompt_attention", "cb_attention_uses_paired_tiles",
            "cb_test_attention_wait_timeout", "cb_test_decode_wait_timeout", "cb_test_projection_wait_timeout",
            "cb_check", "cb_version",
            "LayerBuffers"]
@@ -59,6 +60,7 @@ class Plan:
         self.n_ctx = n_chunks * chunk_len
         self.n_tokens = self.n_ctx + n_suffix
         self.hq, self.hkv, self.head_dim = hq, hkv, head_dim
+        self.device = torch.cuda.current_device() if torch.cuda.is_available() else 0
         self._h = ctypes.c_void_p()
         check(lib.cb_plan_create(ctypes.byref(self.cfg), ctypes.byref(self._h)))
 
@@ -207,6 +209,112 @@ def cb_hkvd_select_noalloc(v_new, v_old, cand, m, k, n_rows, sel_tok, sel_row, s
         _ptr(v_new, torch.bfloat16, "v_new"), _ptr(v_old, torch.bfloat16, "v_old"),
         _ptr(cand, torch.int32, "cand"), m, k, n_rows, v_new.shape[1], v_new.shape[2],
         _ptr(sel_tok, torch.int32, "sel_tok"), _ptr(sel_row, torch.int32, "sel_row"), _stream(stream)))
+
+
+def cb_kv4_page_bytes(plan, page_size) -> int:
+    """Bytes of one page of one kv head: a 4-bit cache is uint8 [n_pages, hkv, page_bytes] (see cacheblend.h)."""
+    n = _lib.load().cb_kv4_page_bytes(plan.handle, page_size)
+    if n == 0:
+        raise CacheBlendError(1, _lib.load().cb_last_error_string().decode())
+    return n
+
+
+def _shape(t, name, *want):
+    """want: sizes, None for any."""
+    if t is not None and (t.dim() != len(want) or any(w is not None and w != n for n, w in zip(t.shape, want))):
+        raise ValueError(f"{name} must have shape {tuple('*' if w is None else w for w in want)}, got {tuple(t.shape)}")
+
+
+def _same_device(plan, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != plan.device:
+            raise ValueError(f"{name} is on {t.device}, the plan on cuda:{plan.device}")
+
+
+def _kv4_cache(plan, cache, page_size):
+    _shape(cache, "cache", None, plan.hkv, cb_kv4_page_bytes(plan, page_size))
+    return _ptr(cache, torch.uint8, "cache"), cache.shape[0]
+
+
+def cb_page_tables(plan, ctx_lens, new_lens, page_size, free_pages, table, cu_seqlens, kv_lens, positions, slots,
+                   free_to, free_from=None, stream=None):
+    """Page table rows, packed offsets, positions and slots of one step from the requests' lengths
+    (see cacheblend.h): ctx_lens, new_lens, kv_lens [n], table [n, width], cu_seqlens [n + 1],
+    positions and slots [n_rows], free_from and free_to [1]; all int32 on the device."""
+    n, rows = ctx_lens.numel(), slots.numel()
+    for name, t, size in (("ctx_lens", ctx_lens, n), ("new_lens", new_lens, n), ("kv_lens", kv_lens, n),
+                          ("cu_seqlens", cu_seqlens, n + 1), ("positions", positions, rows), ("slots", slots, rows),
+                          ("free_pages", free_pages, None), ("free_from", free_from, 1), ("free_to", free_to, 1)):
+        _shape(t, name, size)
+    _shape(table, "table", n, None)
+    _same_device(plan, ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages, table=table,
+                 cu_seqlens=cu_seqlens, kv_lens=kv_lens, positions=positions, slots=slots, free_to=free_to,
+                 free_from=free_from)
+    i32 = torch.int32
+    check(_lib.load().cb_page_tables(
+        plan.handle, _ptr(ctx_lens, i32, "ctx_lens"), _ptr(new_lens, i32, "new_lens"), n, page_size,
+        _ptr(free_pages, i32, "free_pages"), free_pages.numel(), _ptr(free_from, i32, "free_from"),
+        _ptr(table, i32, "table"), table.shape[1], _ptr(cu_seqlens, i32, "cu_seqlens"), _ptr(kv_lens, i32, "kv_lens"),
+        _ptr(positions, i32, "positions"), _ptr(slots, i32, "slots"), rows, _ptr(free_to, i32, "free_to"),
+        _stream(stream)))
+
+
+def _kv4_rows(plan, k, v, slots):
+    _shape(k, "k", None, plan.hkv, plan.head_dim)
+    _shape(v, "v", k.shape[0], plan.hkv, plan.head_dim)
+    _shape(slots, "slots", k.shape[0])
+    return (_ptr(k, torch.bfloat16, "k"), _ptr(v, torch.bfloat16, "v"), _ptr(slots, torch.int32, "slots"),
+            k.shape[0])
+
+
+def cb_kv4_store(plan, k, v, slots, cache, page_size, stream=None):
+    """Rows k, v [n, hkv, D] quantised to 4 bits into cache at slots [n] (negative: skipped)."""
+    pk, pv, ps, n = _kv4_rows(plan, k, v, slots)
+    pc, n_pages = _kv4_cache(plan, cache, page_size)
+    _same_device(plan, k=k, v=v, slots=slots, cache=cache)
+    check(_lib.load().cb_kv4_store(plan.handle, pk, pv, ps, n, pc, n_pages, page_size, _stream(stream)))
+
+
+def cb_kv4_load(plan, cache, page_size, slots, k, v, stream=None):
+    """k, v [n, hkv, D] = the rows that cache holds at slots [n] (negative: left as they are)."""
+    pk, pv, ps, n = _kv4_rows(plan, k, v, slots)
+    pc, n_pages = _kv4_cache(plan, cache, page_size)
+    _same_device(plan, k=k, v=v, slots=slots, cache=cache)
+    check(_lib.load().cb_kv4_load(plan.handle, pc, n_pages, page_size, ps, n, pk, pv, _stream(stream)))
+
+
+def cb_kv4_decode_attention(plan, q, cache, page_size, table, kv_lens, out, scale=0.0, stream=None):
+    """One decode step of a batch: q, out [n, Hq, D] over the pages table [n, width] of the 4-bit cache,
+    kv_lens [n] keys each (0: zeros)."""
+    n = kv_lens.numel()
+    _shape(kv_lens, "kv_lens", n)
+    _shape(q, "q", n, plan.hq, plan.head_dim)
+    _shape(out, "out", n, plan.hq, plan.head_dim)
+    _shape(table, "table", n, None)
+    pc, n_pages = _kv4_cache(plan, cache, page_size)
+    _same_device(plan, q=q, cache=cache, table=table, kv_lens=kv_lens, out=out)
+    check(_lib.load().cb_kv4_decode_attention(
+        plan.handle, _ptr(q, torch.bfloat16, "q"), pc, n_pages, page_size, _ptr(table, torch.int32, "table"),
+        table.shape[1], _ptr(kv_lens, torch.int32, "kv_lens"), n, float(scale), _ptr(out, torch.bfloat16, "out"),
+        _stream(stream)))
+
+
+def cb_prompt_attention(plan, q, k, v, cu_seqlens, out, scale=0.0, stream=None):
+    """Causal attention of packed prompts: q, out [n_rows, Hq, D], k, v [n_rows, Hkv, D], sequence s in
+    rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 on the device); rows in none keep their out."""
+    n = q.shape[0]
+    _shape(q, "q", n, plan.hq, plan.head_dim)
+    _shape(out, "out", n, plan.hq, plan.head_dim)
+    _shape(k, "k", n, plan.hkv, plan.head_dim)
+    _shape(v, "v", n, plan.hkv, plan.head_dim)
+    _shape(cu_seqlens, "cu_seqlens", None)
+    if cu_seqlens.numel() == 0:
+        raise ValueError("cu_seqlens must hold at least the first offset")
+    _same_device(plan, q=q, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
+    check(_lib.load().cb_prompt_attention(
+        plan.handle, _ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"), _ptr(v, torch.bfloat16, "v"),
+        _ptr(cu_seqlens, torch.int32, "cu_seqlens"), cu_seqlens.numel() - 1, n, float(scale),
+        _ptr(out, torch.bfloat16, "out"), _stream(stream)))
 
 
 def cb_attention_uses_paired_tiles(plan, mq) -> bool:

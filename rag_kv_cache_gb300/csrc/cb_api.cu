@@ -15,6 +15,8 @@
 #include "common.cuh"
 #include "kernels.h"
 
+static_assert(CB_PAGE_TABLES_MAX_SEQS == cb::kPageTablesMaxSeqs, "page table limit");
+
 // Streams that run consecutive layers' attention in cb_blend_request (the caller's stream and
 // CB_ATTN_STREAMS - 1 of the plan's): a layer's attention overlaps the tails of the layers before it.
 #ifndef CB_ATTN_STREAMS
@@ -35,6 +37,7 @@ struct cb_plan {
                                         // ([0] unused: that one is the caller's stream)
   cudaEvent_t ev_fork, ev_ready, ev_join;
   cb::DecodeScratch decode;  // cb_decode_attention's split partials and ticket counters
+  cb::Kv4Scratch kv4;        // cb_kv4_decode_attention's partials and ticket counters
 };
 
 namespace {
@@ -85,6 +88,25 @@ cb_status need_ptr(const void* p, const char* name) {
 
 cb_status check_plan(const cb_plan* plan) {
   if (plan == nullptr) return fail(CB_ERR_INVALID_ARG, "plan is NULL");
+  return CB_OK;
+}
+
+// The serving calls check that the plan's device is the current one: its scratch and error word live there.
+cb_status check_device(const cb_plan* plan) {
+  int dev = -1;
+  CB_TRY(cuda_status(cudaGetDevice(&dev), "cudaGetDevice"));
+  if (dev != plan->device)
+    return fail(CB_ERR_INVALID_ARG, "the plan belongs to device %d, the current device is %d", plan->device, dev);
+  return CB_OK;
+}
+
+// Shape of a 4-bit cache: pages of whole 16-token records, slots that fit an int32.
+cb_status check_kv4_cache(int32_t n_pages, int32_t page_size) {
+  if (n_pages < 0) return fail(CB_ERR_INVALID_ARG, "n_pages < 0");
+  if (page_size <= 0 || page_size % 16 != 0 || page_size > CB_KV4_MAX_PAGE)
+    return fail(CB_ERR_INVALID_ARG, "page_size %d: a multiple of 16 up to %d is required", page_size, CB_KV4_MAX_PAGE);
+  if ((int64_t)n_pages * page_size > 0x7fffffffll)
+    return fail(CB_ERR_INVALID_ARG, "n_pages * page_size above 2^31 - 1");
   return CB_OK;
 }
 
@@ -157,6 +179,13 @@ cb_status cb_plan_create(const cb_config* cfg, cb_plan** out) {
   if (e == cudaSuccess) e = cudaMalloc(&p->decode.tickets, sizeof(int32_t) * c.hkv);
   if (e == cudaSuccess) e = cudaMemset(p->decode.tickets, 0, sizeof(int32_t) * c.hkv);
 
+  p->kv4.sms = p->decode.sms;
+  const size_t kv4_units = (size_t)p->kv4.sms * 2 * cb::kKv4MaxGroup;
+  if (e == cudaSuccess) e = cudaMalloc(&p->kv4.part_o, sizeof(float) * kv4_units * c.head_dim);
+  if (e == cudaSuccess) e = cudaMalloc(&p->kv4.part_ml, sizeof(float2) * kv4_units);
+  if (e == cudaSuccess) e = cudaMalloc(&p->kv4.tickets, sizeof(int32_t) * p->kv4.sms);
+  if (e == cudaSuccess) e = cudaMemset(p->kv4.tickets, 0, sizeof(int32_t) * p->kv4.sms);
+
   if (e == cudaSuccess) {
     const int32_t init[2] = {0, -1};
     e = cudaMemcpy(p->err, init, sizeof(init), cudaMemcpyHostToDevice);
@@ -193,6 +222,9 @@ cb_status cb_plan_destroy(cb_plan* plan) {
   cudaFree(plan->decode.part_o);
   cudaFree(plan->decode.part_ml);
   cudaFree(plan->decode.tickets);
+  cudaFree(plan->kv4.part_o);
+  cudaFree(plan->kv4.part_ml);
+  cudaFree(plan->kv4.tickets);
   if (plan->aux_stream) cudaStreamDestroy(plan->aux_stream);
   for (int a = 1; a < kAttnStreams; ++a)
     if (plan->aux_attn[a]) cudaStreamDestroy(plan->aux_attn[a]);
@@ -500,6 +532,122 @@ cb_status cb_decode_attention(cb_plan* plan, const void* q, const void* k, const
   return cuda_status(cb::launch_decode_tc(q, k, v, n_keys, c.hq, c.hkv, c.head_dim, scale, out, plan->decode,
                                           plan->err, static_cast<cudaStream_t>(stream)),
                      "cb_decode_attention");
+}
+
+int32_t cb_kv4_page_bytes(const cb_plan* plan, int32_t page_size) {
+  if (check_plan(plan) != CB_OK || check_kv4_cache(0, page_size) != CB_OK) return 0;
+  return page_size / 16 * 18 * plan->cfg.head_dim;
+}
+
+cb_status cb_page_tables(cb_plan* plan, const int32_t* ctx_lens, const int32_t* new_lens, int32_t n_seqs,
+                         int32_t page_size, const int32_t* free_pages, int32_t n_free, const int32_t* free_from,
+                         int32_t* table, int32_t table_width, int32_t* cu_seqlens, int32_t* kv_lens,
+                         int32_t* positions, int32_t* slots, int32_t n_rows, int32_t* free_to, void* stream) {
+  CB_NVTX_RANGE();
+  CB_TRY(check_plan(plan));
+  CB_TRY(check_kv4_cache(0, page_size));
+  if (n_seqs < 0 || n_free < 0 || table_width < 0 || n_rows < 0) return fail(CB_ERR_INVALID_ARG, "negative size");
+  if (n_seqs > CB_PAGE_TABLES_MAX_SEQS)
+    return fail(CB_ERR_UNSUPPORTED, "n_seqs %d above %d", n_seqs, CB_PAGE_TABLES_MAX_SEQS);
+  if ((int64_t)n_seqs * table_width > (1 << 30) || (int64_t)table_width * page_size > 0x7fffffffll)
+    return fail(CB_ERR_INVALID_ARG, "page table too large: n_seqs * table_width above 2^30 or a row above 2^31 - 1 slots");
+  if (n_seqs > 0) {
+    CB_TRY(need_ptr(ctx_lens, "ctx_lens"));
+    CB_TRY(need_ptr(new_lens, "new_lens"));
+    CB_TRY(need_ptr(kv_lens, "kv_lens"));
+    if (table_width > 0) CB_TRY(need_ptr(table, "table"));
+  }
+  if (n_free > 0) CB_TRY(need_ptr(free_pages, "free_pages"));
+  if (n_rows > 0) {
+    CB_TRY(need_ptr(positions, "positions"));
+    CB_TRY(need_ptr(slots, "slots"));
+  }
+  CB_TRY(need_ptr(cu_seqlens, "cu_seqlens"));
+  CB_TRY(need_ptr(free_to, "free_to"));
+  // every block reads all lengths and the start of the free list, so no block may write over them
+  if (n_seqs > 0 && (kv_lens == ctx_lens || kv_lens == new_lens))
+    return fail(CB_ERR_INVALID_ARG, "kv_lens must not be ctx_lens or new_lens");
+  if (free_to == free_from) return fail(CB_ERR_INVALID_ARG, "free_to must not be free_from");
+  CB_TRY(check_device(plan));
+  return cuda_status(cb::launch_page_tables(ctx_lens, new_lens, n_seqs, page_size, free_pages, n_free, free_from, table,
+                                            table_width, cu_seqlens, kv_lens, positions, slots, n_rows, free_to,
+                                            plan->err, static_cast<cudaStream_t>(stream)),
+                     "cb_page_tables");
+}
+
+static cb_status kv4_rows(const char* fn, bool store, cb_plan* plan, void* k, void* v, const int32_t* slots, int32_t n,
+                          void* cache, int32_t n_pages, int32_t page_size, void* stream) {
+  CB_TRY(check_plan(plan));
+  CB_TRY(check_kv4_cache(n_pages, page_size));
+  if (n < 0) return fail(CB_ERR_INVALID_ARG, "n < 0");
+  if (n == 0) return CB_OK;
+  CB_TRY(need_tensor(k, "k"));
+  CB_TRY(need_tensor(v, "v"));
+  CB_TRY(need_ptr(slots, "slots"));
+  if (n_pages > 0) CB_TRY(need_tensor(cache, "cache"));
+  CB_TRY(check_device(plan));
+  return cuda_status(cb::launch_kv4_rows(store, k, v, slots, n, cache, n_pages, page_size, plan->cfg.hkv,
+                                         plan->cfg.head_dim, plan->err, static_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+cb_status cb_kv4_store(cb_plan* plan, const void* k, const void* v, const int32_t* slots, int32_t n, void* cache,
+                       int32_t n_pages, int32_t page_size, void* stream) {
+  CB_NVTX_RANGE();
+  return kv4_rows("cb_kv4_store", true, plan, const_cast<void*>(k), const_cast<void*>(v), slots, n, cache, n_pages,
+                  page_size, stream);
+}
+
+cb_status cb_kv4_load(cb_plan* plan, const void* cache, int32_t n_pages, int32_t page_size, const int32_t* slots,
+                      int32_t n, void* k, void* v, void* stream) {
+  CB_NVTX_RANGE();
+  return kv4_rows("cb_kv4_load", false, plan, k, v, slots, n, const_cast<void*>(cache), n_pages, page_size, stream);
+}
+
+cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,
+                                  const int32_t* table, int32_t table_width, const int32_t* kv_lens, int32_t n_seqs,
+                                  float scale, void* out, void* stream) {
+  CB_NVTX_RANGE();
+  CB_TRY(check_plan(plan));
+  CB_TRY(check_kv4_cache(n_pages, page_size));
+  const auto& c = plan->cfg;
+  if (n_seqs < 0 || table_width < 0) return fail(CB_ERR_INVALID_ARG, "negative size");
+  if ((int64_t)n_seqs * c.hkv > 0x7fffffffll || (int64_t)table_width * page_size > 0x7fffffffll)
+    return fail(CB_ERR_INVALID_ARG, "n_seqs * hkv or table_width * page_size above 2^31 - 1");
+  if (n_seqs == 0) return CB_OK;
+  CB_TRY(need_tensor(q, "q"));
+  if (n_pages > 0) CB_TRY(need_tensor(cache, "cache"));
+  if (table_width > 0) CB_TRY(need_ptr(table, "table"));
+  CB_TRY(need_ptr(kv_lens, "kv_lens"));
+  CB_TRY(need_tensor(out, "out"));
+  CB_TRY(check_device(plan));
+  if (!(scale > 0.0f)) scale = 1.0f / std::sqrt((float)c.head_dim);
+  return cuda_status(cb::launch_kv4_decode(q, cache, n_pages, page_size, table, table_width, kv_lens, n_seqs, c.hq,
+                                           c.hkv, c.head_dim, scale, out, plan->kv4, plan->err,
+                                           static_cast<cudaStream_t>(stream)),
+                     "cb_kv4_decode_attention");
+}
+
+cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                              int32_t n_seqs, int32_t n_rows, float scale, void* out, void* stream) {
+  CB_NVTX_RANGE();
+  CB_TRY(check_plan(plan));
+  const auto& c = plan->cfg;
+  if (n_seqs < 0 || n_rows < 0) return fail(CB_ERR_INVALID_ARG, "negative size");
+  if (n_seqs == 0 || n_rows == 0) return CB_OK;
+  if (cb::prompt_items(n_seqs, n_rows, c.hq, c.hkv) > (1 << 30))
+    return fail(CB_ERR_INVALID_ARG, "n_rows and n_seqs make more than 2^30 work items");
+  CB_TRY(need_tensor(q, "q"));
+  CB_TRY(need_tensor(k, "k"));
+  CB_TRY(need_tensor(v, "v"));
+  CB_TRY(need_ptr(cu_seqlens, "cu_seqlens"));
+  CB_TRY(need_tensor(out, "out"));
+  if (out == q || out == k || out == v) return fail(CB_ERR_INVALID_ARG, "out must not be q, k or v");
+  CB_TRY(check_device(plan));
+  if (!(scale > 0.0f)) scale = 1.0f / std::sqrt((float)c.head_dim);
+  return cuda_status(cb::launch_prompt_attention(q, k, v, cu_seqlens, n_seqs, n_rows, c.hq, c.hkv, c.head_dim, scale,
+                                                 out, plan->decode.sms, plan->err, static_cast<cudaStream_t>(stream)),
+                     "cb_prompt_attention");
 }
 
 struct LayerShape {

@@ -151,6 +151,38 @@ cudaError_t launch_decode_timeout_probe(const void* q, const void* k, const void
                                         int32_t hkv, float scale, void* out, const DecodeScratch& ws, int32_t* err,
                                         cudaStream_t s);
 
+// Page tables, slot map, packed offsets and positions of one serving step (page_tables.cu).
+constexpr int32_t kPageTablesMaxSeqs = 16384;  // both prefix sums live in shared memory
+cudaError_t launch_page_tables(const int32_t* ctx, const int32_t* added, int32_t n_seqs, int32_t page_size,
+                               const int32_t* free_pages, int32_t n_free, const int32_t* free_from, int32_t* table,
+                               int32_t width, int32_t* cu, int32_t* kv_lens, int32_t* positions, int32_t* slots,
+                               int32_t n_rows, int32_t* free_to, int32_t* err, cudaStream_t s);
+
+// Rows k, v [n, hkv, D] into (store) or out of the 4-bit cache at slots[i]; negative slots are skipped.
+cudaError_t launch_kv4_rows(bool store, void* k, void* v, const int32_t* slots, int32_t n, void* cache,
+                            int32_t n_pages, int32_t page_size, int32_t hkv, int32_t head_dim, int32_t* err,
+                            cudaStream_t s);
+
+// Scratch of the decode attention over the 4-bit cache (owned by the plan): two partial results per
+// CTA of one wave and a ticket counter per CTA, zero between calls (the kernel leaves it zero).
+constexpr int32_t kKv4MaxGroup = 16;  // query heads per kv head
+struct Kv4Scratch {
+  float* part_o;     // [sms][2][kKv4MaxGroup][D]
+  float2* part_ml;   // [sms][2][kKv4MaxGroup]
+  int32_t* tickets;  // [sms]
+  int32_t sms;
+};
+cudaError_t launch_kv4_decode(const void* q, const void* cache, int32_t n_pages, int32_t page_size,
+                              const int32_t* table, int32_t width, const int32_t* lens, int32_t n_seqs, int32_t hq,
+                              int32_t hkv, int32_t head_dim, float scale, void* out, const Kv4Scratch& ws,
+                              int32_t* err, cudaStream_t s);
+
+// Causal attention of packed prompts; prompt_items is the most work items a launch can have.
+int64_t prompt_items(int32_t n_seqs, int32_t n_rows, int32_t hq, int32_t hkv);
+cudaError_t launch_prompt_attention(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,
+                                    int32_t n_rows, int32_t hq, int32_t hkv, int32_t head_dim, float scale, void* out,
+                                    int32_t sms, int32_t* err, cudaStream_t s);
+
 // QKV projection of listed rows: q / k / v rows of token t_i = tokens[i] (null: i) from
 // x[x_index[i]] W^T (x_index null: x[i], read in place; else the rows are first copied to
 // x_gathered [m, d_model]), q and k RoPE-encoded at position t_i when `encode`.

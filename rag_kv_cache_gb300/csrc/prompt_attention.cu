@@ -1,0 +1,741 @@
+// Causal grouped-query attention over whole prompts, packed one after the other:
+//
+//   out[t, h] = sum_{j <= t} softmax_j(scale * q[t, h] . k[j, g]) v[j, g],  g = h / G,
+//
+// for tokens t and j of the same sequence; sequence s is rows cu[s] .. cu[s + 1] - 1 of q, k, v, out.
+//
+// Bound by the tensor cores from a few hundred tokens per sequence on (4 hq D flops per visible pair),
+// by HBM below that. The tile loop is the paired-tile kernel's (attention_pp.cu): a work item is one
+// kv head and two query tiles of 128 rows (tile i: TQ = 128 / G tokens times the G heads), whose
+// softmax and tensor-core work alternate, so that each softmax hides behind the other tile's MMAs.
+//
+// What differs, and why:
+//   Persistent CTAs. A chunk of 2,048 tokens has items of 1 to 16 key tiles, about 9 rounds of 1.4 us
+//   on average, and starting a CTA (TMEM, barriers, first loads) costs about 3 us, a quarter of that.
+//   One CTA per SM takes items in turn; the rings of K and V run on across items, and the next
+//   item's first tiles load while the last softmax of the current one runs.
+//   No tile list. The lengths are known on the device only, and the items of one launch should go out
+//   longest first. The order (level, sequence) with level = index of the item in its sequence, from
+//   the largest down, is that order; the producer warp finds the r-th item in it directly: the
+//   sequences with more than `level` items do not change between two distinct item counts, so a run
+//   of levels is skipped at once (two warp reductions over the lengths per distinct count passed).
+//   CTAs take ranks in alternating direction (0 .. n - 1, then 2 n - 1 .. n), which evens out
+//   the sum of a descending cost.
+//   Rows of other sequences. A key tile that reaches past its sequence's end holds the next one's
+//   rows, and one on the diagonal holds keys that some of the rows must not see; their weight is 0, but
+//   0 * V is NaN where V is infinite or NaN. In those tiles (the ones with a key that some row of the
+//   item does not see) the waiter warp looks for such values and sets them to 0 in shared memory; an
+//   item where it found any adds them back to the rows that do see them, in the epilogue. The search
+//   runs while the tile waits for its softmax.
+//   Output. Rows behind a sequence's end belong to others, so the epilogue stores each row from its
+//   thread's registers, 32 bytes (a whole sector) per instruction, instead of a tile by TMA; no
+//   shared memory is needed for it, and the query tiles' buffers are free for the next item.
+//
+// Roles, TMEM columns, register split and bounded waits are those of attention_pp.cu; "round" counts
+// the key tiles of all the CTA's items, and ring stage and parity follow from it. Item descriptions
+// pass from the producer to the other warps through a ring of four. After a wait that gave up
+// (abort flag) every warp still walks through the rounds of the current item, without work, and the
+// producer ends the list, so no named barrier is left short.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "attn_common.cuh"
+#include "attn_tile.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+#include "tmem_ops.cuh"
+
+namespace cb {
+namespace {
+
+constexpr int kBM = 128;      // rows per query tile
+constexpr int kTiles = 2;     // query tiles per item
+constexpr int kBN = kTileKeys;  // keys per key tile
+constexpr int kStages = 2;    // depth of the K and of the V ring
+constexpr int kItems = 4;     // depth of the item ring
+constexpr int kThreads = 384;
+constexpr int kSoftmaxThreads = 128;
+constexpr int kWarpProducerK = 8;
+constexpr int kWarpMma = 9;
+constexpr int kWarpProducerV = 10;
+constexpr int kWarpWaiter = 11;
+constexpr int kBarExit = 1;   // all 384 threads, before the tensor memory is freed
+constexpr int kBarIssue = 2;  // issuer + waiter (64 threads): the first scores of an item
+constexpr int kBarTile0 = 3;  // WG0 + issuer + waiter (192 threads), once per key tile
+constexpr int kBarTile1 = 4;  // WG1 + issuer (160 threads), once per key tile
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSoftmaxRegs = 224;  // per thread of WG0 / WG1 after setmaxnreg.inc
+constexpr int kOtherRegs = 56;     // per thread of WG2 after setmaxnreg.dec
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only when the max grows by > 2^8
+constexpr float kTileSumLimit = 65536.0f;  // a later tile whose P sum exceeds 2^16 moves the reference
+constexpr unsigned long long kItemLimitNs = 5 * kTimeoutNs;  // the producer's own waits end well before
+
+__host__ __device__ constexpr uint32_t col_s(int i) { return (uint32_t)(i * kBN); }
+__host__ __device__ constexpr uint32_t col_o(int i, int d) { return 256u + (uint32_t)(i * d); }
+
+struct Item {
+  int row0;   // first row of the sequence
+  int len;    // its rows
+  int t0;     // first token (in the sequence) of query tile 0
+  int g;      // kv head
+  int n_kv;   // key tiles, 0: no more items
+  int fixed;  // set by the waiter: a V tile held values that are not finite
+};
+
+struct Bars {
+  uint64_t q_full[kTiles];
+  uint64_t k_full[kStages];
+  uint64_t v_full[kStages];
+  uint64_t s_full[kTiles][kStages];  // S_i of a round complete (commit); [1][s] also: K stage s free
+  uint64_t o_done[kTiles][kStages];  // P_i V of a round complete (commit); [1][s] also: V stage s free
+  uint64_t item[kItems];
+  uint64_t drain;
+};
+
+struct PromptParams {
+  const uint8_t* v;
+  const int32_t* cu;
+  uint8_t* out;
+  int n_seqs;
+  int n_rows;
+  int hq;
+  int hkv;
+  int group;
+  int tq;    // query tokens per tile = 128 / group
+  int wide;  // out is 32-byte aligned
+  float scale_log2;
+  int32_t* err;
+};
+
+__device__ __forceinline__ void named_sync(int id, int count) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// First row of each sequence, inside [0, n_rows].
+__device__ __forceinline__ int row_at(const PromptParams& p, int s) {
+  const int r = __ldg(p.cu + s);
+  return r < 0 ? 0 : min(r, p.n_rows);
+}
+
+// The launch's items by rank (longest first), for a converged warp. Ranks asked for must not fall.
+struct Ranks {
+  int hi, lo;  // levels hi .. lo hold the same `count` sequences each
+  int count;
+  int first;  // rank of the run's first item
+
+  __device__ __forceinline__ int items_of(const PromptParams& p, int s) const {
+    if (s >= p.n_seqs) return 0;
+    const int n = row_at(p, s + 1) - row_at(p, s), per = kTiles * p.tq;
+    return n > 0 ? (n + per - 1) / per : 0;
+  }
+  // The run below level `top` (sequences of at least `top` items): its count and lowest level.
+  __device__ __forceinline__ void enter(const PromptParams& p, int top, int lane) {
+    hi = top - 1;
+    int n = 0, next = 0;
+    for (int s = lane; s < p.n_seqs; s += 32) {
+      const int m = items_of(p, s);
+      if (m > hi)
+        ++n;
+      else
+        next = max(next, m);
+    }
+    count = __reduce_add_sync(0xffffffffu, n);
+    lo = __reduce_max_sync(0xffffffffu, next);
+  }
+  __device__ __forceinline__ void start(const PromptParams& p, int lane) {
+    int top = 0;
+    for (int s = lane; s < p.n_seqs; s += 32) top = max(top, items_of(p, s));
+    top = __reduce_max_sync(0xffffffffu, top);
+    first = 0;
+    if (top > 0)
+      enter(p, top, lane);
+    else
+      hi = -1, lo = 0, count = 0;
+  }
+  // Item of rank r: false past the last one.
+  __device__ __forceinline__ bool find(const PromptParams& p, int r, int lane, int& seq, int& level) {
+    while (hi >= 0 && r >= first + count * (hi - lo + 1)) {
+      first += count * (hi - lo + 1);
+      if (lo == 0) {
+        hi = -1;
+        break;
+      }
+      enter(p, lo, lane);
+    }
+    if (hi < 0) return false;
+    const uint32_t rel = r - first, up = rel / (uint32_t)count;  // 32 bits: a 64-bit division would be a call
+    level = hi - (int)up;
+    int nth = (int)(rel - up * count);
+    for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {  // `count` sequences have more than hi >= level items
+      const uint32_t has = __ballot_sync(0xffffffffu, items_of(p, s0 + lane) > hi);
+      const int n = __popc(has);
+      if (nth < n) {
+        uint32_t rest = has;
+        for (int i = 0; i < nth; ++i) rest &= rest - 1;
+        seq = s0 + __ffs(rest) - 1;
+        return true;
+      }
+      nth -= n;
+    }
+    return false;
+  }
+};
+
+// A V tile of `bytes` bytes in shared memory: values that are not finite become 0. True (in every
+// lane) if there were any. Called by a converged warp.
+__device__ __forceinline__ bool zero_not_finite(uint32_t tile, uint32_t bytes, int lane) {
+  bool found = false;
+#pragma unroll 4
+  for (uint32_t at = lane * 16; at < bytes; at += 512) {
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(tile + at)
+                 : "memory");
+    // an exponent of all ones, plus one unit of it, carries into the sign bit of its half
+    uint32_t bad = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad |= (w[e] & 0x7f807f80u) + 0x00800080u;
+    if (bad & 0x80008000u) {
+      found = true;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+        if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3])
+                   : "memory");
+    }
+  }
+  found = __any_sync(0xffffffffu, found);
+  if (found) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it next
+  return found;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const PromptParams p) {
+  constexpr int kBoxes = D / 64;
+  constexpr uint32_t kQBytes = kBM * D * 2;  // one query tile
+  constexpr uint32_t kKVBytes = kBN * D * 2;
+  constexpr uint32_t kQBox = kBM * 128;   // bytes of one 64-column box of a query tile
+  constexpr uint32_t kKVBox = kBN * 128;  // bytes of one 64-column box of a K or V tile
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars bars;
+  __shared__ Item items[kItems];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ int s_first_ok;
+  __shared__ int s_round_ok[2];
+
+  pdl_launch_dependents();
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sQ = base;                        // query tile i at sQ + i kQBytes
+  const uint32_t sK0 = base + kTiles * kQBytes;    // K stage s at sK0 + s kKVBytes
+  const uint32_t sV0 = sK0 + kStages * kKVBytes;   // V stage s at sV0 + s kKVBytes
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (warp == kWarpProducerK && lane == 0) {
+    for (int i = 0; i < kTiles; ++i) mbar_init(smem_u32(&bars.q_full[i]), 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&bars.k_full[s]), 1);
+      mbar_init(smem_u32(&bars.v_full[s]), 1);
+      for (int i = 0; i < kTiles; ++i) {
+        mbar_init(smem_u32(&bars.s_full[i][s]), 1);
+        mbar_init(smem_u32(&bars.o_done[i][s]), 1);
+      }
+    }
+    for (int i = 0; i < kItems; ++i) mbar_init(smem_u32(&bars.item[i]), 1);
+    mbar_init(smem_u32(&bars.drain), 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  volatile int* abort_flag = &s_abort;
+  // The it-th item of this CTA; n_kv = 0 at the end (and, never expected, if it does not come).
+  auto item_at = [&](int it) -> Item {
+    const uint32_t bar = smem_u32(&bars.item[it % kItems]);
+    bool there = mbar_test(bar, (it / kItems) & 1);
+    if (!there) {
+      const uint64_t t0 = global_timer();
+      for (uint32_t n = 1; !(there = mbar_try_wait_sleep(bar, (it / kItems) & 1)); ++n)
+        if ((n & 7u) == 0 && global_timer() - t0 > kItemLimitNs) break;
+    }
+    there = __all_sync(0xffffffffu, there);
+    if (there) return items[it % kItems];
+    *abort_flag = 1;
+    record_error(p.err, kErrTimeout, 40);
+    return Item{0, 0, 0, 0, 0, 0};
+  };
+
+  if (warp >= kTiles * (kSoftmaxThreads / 32)) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    pdl_wait();  // q, k, v and the offsets come from the kernels before this one
+    if (warp == kWarpProducerK) {
+      if (blockIdx.x == 0)  // offsets that fall or leave the rows are recorded (and read as empty or clipped)
+        for (int s = lane; s < p.n_seqs; s += 32) {
+          const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1);
+          if (a < 0 || b > p.n_rows) record_error(p.err, kErrIndex, s);
+          if (b < a) record_error(p.err, kErrOrder, s);
+        }
+      Ranks ranks;
+      ranks.start(p, lane);
+      int rounds = 0;  // rounds of the items before
+      int nk = 0;      // K tiles requested, by round
+      int nq[kTiles] = {0, 0};  // query tiles requested
+      const uint32_t grid = gridDim.x;
+      for (int it = 0;; ++it) {
+        const uint32_t idx = (uint32_t)it * grid + ((it & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
+        Item x{0, 0, 0, 0, 0, 0};
+        int seq, level;
+        const bool give_up = __any_sync(0xffffffffu, *abort_flag != 0);
+        if (!give_up && ranks.find(p, (int)(idx / (uint32_t)p.hkv), lane, seq, level)) {
+          x.row0 = row_at(p, seq);
+          x.len = row_at(p, seq + 1) - x.row0;
+          x.t0 = level * kTiles * p.tq;
+          x.g = (int)(idx % (uint32_t)p.hkv);
+          x.n_kv = (min(x.t0 + kTiles * p.tq, x.len) - 1) / kBN + 1;
+        }
+        if (lane == 0) {
+          items[it % kItems] = x;
+          mbar_arrive(smem_u32(&bars.item[it % kItems]));
+          const int n = x.n_kv;
+          auto load_k = [&](int j) -> bool {
+            const int r = rounds + j, st = r % kStages;
+            // K of round r - 2 held this stage: free once S_1 of that round (issued after S_0) is complete
+            if (r >= kStages &&
+                !mbar_wait_inl(smem_u32(&bars.s_full[1][st]), ((r / kStages) - 1) & 1, abort_flag, p.err, 41))
+              return false;
+            const uint32_t kb = smem_u32(&bars.k_full[st]);
+            mbar_expect_tx(kb, kKVBytes);
+#pragma unroll
+            for (int b = 0; b < kBoxes; ++b)
+              tma_load_3d(sK0 + st * kKVBytes + b * kKVBox, &tm_k, kb, b * 64, x.g, x.row0 + j * kBN);
+            nk = r + 1;
+            return true;
+          };
+          bool ok = n > 0 && load_k(0);
+          // Query tile i: its buffer is free once S_i of the round before (the last of the item before)
+          // is complete. Rows past the sequence's end are other sequences' (or the fill value).
+          for (int i = 0; i < kTiles && ok; ++i) {
+            const int r = rounds - 1;
+            ok = r < 0 || mbar_wait_inl(smem_u32(&bars.s_full[i][r % kStages]), (r / kStages) & 1, abort_flag, p.err, 42);
+            if (!ok) break;
+            const uint32_t qb = smem_u32(&bars.q_full[i]);
+            mbar_expect_tx(qb, kQBytes);
+#pragma unroll
+            for (int b = 0; b < kBoxes; ++b)
+              tma_load_4d(sQ + i * kQBytes + b * kQBox, &tm_q, qb, b * 64, 0, x.g, x.row0 + x.t0 + i * p.tq);
+            ++nq[i];
+          }
+          for (int j = 1; j < n && ok; ++j) ok = load_k(j);
+        }
+        __syncwarp();
+        if (x.n_kv == 0) break;
+        rounds += x.n_kv;
+      }
+      // Before the CTA can exit, every copy issued must have landed (also after an abort).
+      if (lane == 0) {
+        for (int i = 0; i < kTiles; ++i)
+          if (nq[i] > 0) mbar_wait_inl(smem_u32(&bars.q_full[i]), (nq[i] - 1) & 1, abort_flag, p.err, 56, false);
+        for (int r = nk < kStages ? 0 : nk - kStages; r < nk; ++r)
+          mbar_wait_inl(smem_u32(&bars.k_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 57, false);
+      }
+    } else if (warp == kWarpProducerV) {
+      int rounds = 0, nv = 0;
+      bool ok = true;
+      for (int it = 0;; ++it) {
+        const Item x = item_at(it);
+        if (x.n_kv == 0) break;
+        if (lane == 0) {
+          for (int j = 0; j < x.n_kv && ok; ++j) {
+            const int r = rounds + j, st = r % kStages;
+            // V of round r - 2 held this stage: free once P_1 V of that round (after P_0 V) is complete
+            ok = r < kStages ||
+                 mbar_wait_inl(smem_u32(&bars.o_done[1][st]), ((r / kStages) - 1) & 1, abort_flag, p.err, 43);
+            if (!ok) break;
+            const uint32_t vb = smem_u32(&bars.v_full[st]);
+            mbar_expect_tx(vb, kKVBytes);
+#pragma unroll
+            for (int b = 0; b < kBoxes; ++b)
+              tma_load_3d(sV0 + st * kKVBytes + b * kKVBox, &tm_v, vb, b * 64, x.g, x.row0 + j * kBN);
+            nv = r + 1;
+          }
+        }
+        __syncwarp();
+        rounds += x.n_kv;
+      }
+      if (lane == 0)
+        for (int r = nv < kStages ? 0 : nv - kStages; r < nv; ++r)
+          mbar_wait_inl(smem_u32(&bars.v_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 58, false);
+    } else if (warp == kWarpWaiter) {
+      // The TMA inputs of an item's first scores (both query tiles and its first K tile), then per key
+      // tile those of its round (V and the next K), published to the issuer through shared memory
+      // before it meets the issuer (and WG0) on a named barrier. Every round is joined, also after a
+      // failure.
+      auto spin_all = [&](uint32_t bar, uint32_t parity, int site) -> bool {
+        return __all_sync(0xffffffffu, mbar_spin_inl(bar, parity, abort_flag, p.err, site));
+      };
+      int rounds = 0;
+      bool ok = true;
+      for (int it = 0;; ++it) {
+        const Item x = item_at(it);
+        if (x.n_kv == 0) break;
+        ok = ok && spin_all(smem_u32(&bars.q_full[0]), it & 1, 44) && spin_all(smem_u32(&bars.q_full[1]), it & 1, 45) &&
+             spin_all(smem_u32(&bars.k_full[rounds % kStages]), (rounds / kStages) & 1, 46);
+        if (lane == 0) s_first_ok = ok ? 1 : 0;
+        __syncwarp();  // bar.sync is warp-aligned: reach it converged
+        named_sync(kBarIssue, 64);
+        for (int j = 0; j < x.n_kv; ++j) {
+          const int r = rounds + j, st = r % kStages;
+          ok = ok && spin_all(smem_u32(&bars.v_full[st]), (r / kStages) & 1, 47);
+          // a tile with a key that the item's first row does not see
+          if (ok && (j + 1) * kBN > x.t0 + 1 && zero_not_finite(sV0 + st * kKVBytes, kKVBytes, lane) && lane == 0)
+            items[it % kItems].fixed = 1;
+          ok = ok && (j + 1 >= x.n_kv ||
+                      spin_all(smem_u32(&bars.k_full[(r + 1) % kStages]), ((r + 1) / kStages) & 1, 48));
+          if (lane == 0) s_round_ok[r & 1] = ok ? 1 : 0;
+          __syncwarp();
+          named_sync(kBarTile0, 192);
+        }
+        rounds += x.n_kv;
+      }
+    } else if (warp == kWarpMma) {
+      constexpr uint32_t idesc_s = idesc_bf16(kBM, kBN, false);
+      constexpr uint32_t idesc_o = idesc_bf16(kBM, D, true);
+      const uint64_t dk0 = sdesc(sK0, 16, 1024);
+      const uint64_t dv0 = sdesc(sV0, kKVBox, 1024);
+      // S_i = Q_i K^T of round r; elected lane only.
+      auto issue_s = [&](int i, int r) {
+        const int st = r % kStages;
+        const uint64_t dq = sdesc(sQ + i * kQBytes, 16, 1024);
+        const uint64_t dk = dk0 + (uint64_t)((st * kKVBytes) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int bx = ks / 4, kk = ks % 4;
+          mma_ss(tmem + col_s(i), dq + (uint64_t)((bx * kQBox + kk * 32) >> 4),
+                 dk + (uint64_t)((bx * kKVBox + kk * 32) >> 4), idesc_s, ks > 0 ? 1u : 0u);
+        }
+        tc_commit(smem_u32(&bars.s_full[i][st]));
+      };
+      // O_i (+)= P_i V of round r: P from TMEM (16 keys = 8 columns per MMA), V MN-major in shared memory.
+      auto issue_pv = [&](int i, int r, bool first) {
+        const int st = r % kStages;
+        const uint64_t dv = dv0 + (uint64_t)((st * kKVBytes) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kBN / 16; ++ks)
+          mma_ts(tmem + col_o(i, D), tmem + col_s(i) + ks * 8, dv + (uint64_t)((ks * 16 * 128) >> 4), idesc_o,
+                 (ks > 0 || !first) ? 1u : 0u);
+        tc_commit(smem_u32(&bars.o_done[i][st]));
+      };
+      int rounds = 0;
+      bool ok = true;
+      for (int it = 0;; ++it) {
+        const Item x = item_at(it);
+        if (x.n_kv == 0) break;
+        __syncwarp();
+        named_sync(kBarIssue, 64);
+        ok = ok && s_first_ok != 0;
+        if (ok) {
+          tc_fence_after();
+          if (elect_one()) {
+            issue_s(0, rounds);
+            issue_s(1, rounds);
+          }
+          __syncwarp();
+        }
+        for (int j = 0; j < x.n_kv; ++j) {
+          const int r = rounds + j;
+          __syncwarp();
+          named_sync(kBarTile0, 192);  // P_0 in TMEM; this round's V and the next K loaded (waiter)
+          ok = ok && s_round_ok[r & 1] != 0 && !*abort_flag;
+          if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+              issue_pv(0, r, j == 0);
+              if (j + 1 < x.n_kv) issue_s(0, r + 1);
+            }
+            __syncwarp();
+          }
+          __syncwarp();
+          named_sync(kBarTile1, 160);  // P_1 in TMEM
+          ok = ok && !*abort_flag;
+          if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+              issue_pv(1, r, j == 0);
+              if (j + 1 < x.n_kv) issue_s(1, r + 1);
+            }
+            __syncwarp();
+          }
+        }
+        rounds += x.n_kv;
+      }
+      // All tensor-core work issued by this CTA completes before TMEM is freed.
+      if (elect_one()) tc_commit(smem_u32(&bars.drain));
+      __syncwarp();
+      mbar_wait_inl(smem_u32(&bars.drain), 0, abort_flag, p.err, 49, false);
+    }
+    // The two register regions end separately (no common tail after the branch): every warp
+    // meets on named barrier 1 before warp 0 frees the tensor memory.
+    __syncwarp();
+    tc_fence_before();
+    named_sync(kBarExit, kThreads);
+    return;
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    pdl_wait();
+    const int ti = warp / 4;  // this warpgroup's query tile
+    const int row = threadIdx.x % kBM;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp % 4) * 32) << 16);
+    int rounds = 0;
+    bool ok = true;
+    for (int it = 0;; ++it) {
+      const Item x = item_at(it);
+      if (x.n_kv == 0) break;
+      // Position of this thread's row in the sequence; rows past its end repeat the last one and are
+      // never stored.
+      const int tok = x.t0 + ti * p.tq + row / p.group;
+      const int my_pos = min(tok, x.len - 1);
+      float m_ref = -INFINITY, l = 0.0f;  // reference max (log2 units) that O_ti and l are scaled to
+      auto wait_o = [&](int r, int site) -> bool {
+        const bool w =
+            mbar_spin_inl(smem_u32(&bars.o_done[ti][r % kStages]), (r / kStages) & 1, abort_flag, p.err, site);
+        return __all_sync(0xffffffffu, w);
+      };
+      // One key tile; false if a wait gave up (the abort flag is raised then).
+      auto tile = [&](int j) -> bool {
+        const int r = rounds + j;
+        if (!__all_sync(0xffffffffu, mbar_spin_inl(smem_u32(&bars.s_full[ti][r % kStages]), (r / kStages) & 1,
+                                                   abort_flag, p.err, 50 + ti)))
+          return false;
+        tc_fence_after();
+        uint32_t sv[kBN];  // this row's 128 scores
+        {
+          uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[0]);
+          uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[32]);
+          uint32_t(&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[64]);
+          uint32_t(&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sv[96]);
+          tmem_ld_x32_async(lane_base + col_s(ti), s0);
+          tmem_ld_x32_async(lane_base + col_s(ti) + 32, s1);
+          tmem_ld_x32_async(lane_base + col_s(ti) + 64, s2);
+          tmem_ld_x32_async(lane_base + col_s(ti) + 96, s3);
+          tmem_wait_ld(s0);
+          tmem_wait_ld(s1);
+          tmem_wait_ld(s2);
+          tmem_wait_ld(s3);
+        }
+        const int lim = my_pos - j * kBN;  // columns c <= lim are visible to this row
+        if (__any_sync(0xffffffffu, lim < kBN - 1)) {  // diagonal tiles only
+#pragma unroll
+          for (int c = 0; c < kBN; ++c)
+            if (c > lim) sv[c] = 0xff800000u;  // -inf
+        }
+        // As in attention_pp.cu: a row's first tile sets the reference to its max; later tiles run
+        // against the reference and take their max only where their P sum shows that it jumped.
+        const uint32_t taddr_p = lane_base + col_s(ti);
+        bool move_ref = !__all_sync(0xffffffffu, m_ref != -INFINITY);
+        float sum = 0.0f;
+        if (!move_ref) {
+          sum = softmax_p(sv, m_ref, p.scale_log2, taddr_p);
+          move_ref = !__all_sync(0xffffffffu, sum <= kTileSumLimit);  // rare: the max jumped
+        }
+        if (move_ref) {
+          // Four independent chains of three-input max.
+          float tm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < kBN; c += 8) {
+            tm[0] = max3(tm[0], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+            tm[1] = max3(tm[1], __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+            tm[2] = max3(tm[2], __uint_as_float(sv[c + 4]), __uint_as_float(sv[c + 5]));
+            tm[3] = max3(tm[3], __uint_as_float(sv[c + 6]), __uint_as_float(sv[c + 7]));
+          }
+          const float mt = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * p.scale_log2;
+          const bool up = mt > m_ref + kRescaleThreshold;  // always, at a row's first tile
+          if (__any_sync(0xffffffffu, up)) {
+            const float alpha = up ? ex2(m_ref - mt) : 1.0f;  // 0 for a row that had nothing visible
+            const bool scale_o = up && m_ref != -INFINITY;
+            if (up) {
+              l *= alpha;
+              m_ref = mt;
+            }
+            // O_ti holds the sum through the tile before: wait for that product, then scale it.
+            if (j > 0 && __any_sync(0xffffffffu, scale_o)) {
+              if (!wait_o(r - 1, 52 + ti)) return false;
+              tc_fence_after();
+              const float a = scale_o ? alpha : 1.0f;
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                tmem_ld_x32(lane_base + col_o(ti, D) + c0, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                tmem_st_x32(lane_base + col_o(ti, D) + c0, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          sum = softmax_p(sv, m_ref, p.scale_log2, taddr_p);  // these stores replace any earlier P
+        }
+        l += sum;
+        tmem_st_wait();
+        return true;
+      };
+      // Every softmax warp syncs once per key tile on its tile's named barrier, also after a failed
+      // wait (then without work), so every round of the issuer and the waiter completes.
+      for (int j = 0; j < x.n_kv; ++j) {
+        if (ok) ok = tile(j);
+        tc_fence_before();
+        __syncwarp();
+        if (ti == 0)
+          named_sync(kBarTile0, 192);
+        else
+          named_sync(kBarTile1, 160);
+      }
+      rounds += x.n_kv;
+      if (ok) ok = wait_o(rounds - 1, 54 + ti);
+      // Epilogue: out = O_ti / l, each thread its row.
+      if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
+        tc_fence_after();
+        const float inv = 1.0f / l;
+        const bool fixed = items[it % kItems].fixed != 0;
+        const bool store = tok < x.len;
+        uint8_t* dst = p.out + ((int64_t)(x.row0 + my_pos) * p.hq + x.g * p.group + row % p.group) * (D * 2);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld_x32(lane_base + col_o(ti, D) + c0, o);
+          if (fixed) {  // the values that were set to 0, of the keys that this row does see
+            for (int key = (x.t0 + 1) / kBN * kBN; key <= my_pos; ++key) {
+              const uint8_t* src = p.v + (((int64_t)(x.row0 + key) * p.hkv + x.g) * D + c0) * 2;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                float f[8];
+                unpack8(*reinterpret_cast<const uint4*>(src + q * 16), f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (!isfinite(f[e])) o[q * 8 + e] = __float_as_uint(__uint_as_float(o[q * 8 + e]) + f[e]);
+              }
+            }
+          }
+          uint4 pk[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[q * 8 + e]) * inv;
+            pk[q] = pack8(f);
+          }
+          if (store) {
+            if (p.wide) {
+#pragma unroll
+              for (int q = 0; q < 4; q += 2)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c0 * 2 + q * 16),
+                             "r"(pk[q].x), "r"(pk[q].y), "r"(pk[q].z), "r"(pk[q].w), "r"(pk[q + 1].x),
+                             "r"(pk[q + 1].y), "r"(pk[q + 1].z), "r"(pk[q + 1].w)
+                             : "memory");
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + c0 * 2 + q * 16) = pk[q];
+            }
+          }
+          __syncwarp();  // the next load of TMEM is warp-aligned
+        }
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+    named_sync(kBarExit, kThreads);
+    if (warp == 0) {
+      tc_fence_after();
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,
+                            int32_t n_rows, int32_t hq, int32_t hkv, float scale, void* out, int32_t sms,
+                            int32_t* err, cudaStream_t s) {
+  const int group = hq / hkv;
+  const int tq = kBM / group;
+  // The register split: the block is launched with numRegs per thread and setmaxnreg moves them
+  // between the warpgroups; a build with fewer than the split needs would wait forever in
+  // setmaxnreg.inc, so it is never launched.
+  static int regs = -1;
+  if (regs < 0) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, prompt_attention_kernel<D>);
+    if (e != cudaSuccess) return e;
+    regs = a.numRegs;
+  }
+  if (regs * kThreads < kTiles * kSoftmaxThreads * kSoftmaxRegs + kSoftmaxThreads * kOtherRegs)
+    return cudaErrorNotSupported;
+  CUtensorMap tq_map, tk_map, tv_map;
+  const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)group, (cuuint64_t)hkv, (cuuint64_t)n_rows};
+  const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)group * D * 2, (cuuint64_t)hq * D * 2};
+  const cuuint32_t qb[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)tq};
+  const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)hkv, (cuuint64_t)n_rows};
+  const cuuint64_t ks[2] = {(cuuint64_t)D * 2, (cuuint64_t)hkv * D * 2};
+  const cuuint32_t kbx[3] = {64, 1, (cuuint32_t)kBN};
+  if (!encode_map(&tq_map, q, 4, qd, qs, qb) || !encode_map(&tk_map, k, 3, kd, ks, kbx) ||
+      !encode_map(&tv_map, v, 3, kd, ks, kbx))
+    return cudaErrorInvalidValue;
+  PromptParams p;
+  p.v = static_cast<const uint8_t*>(v);
+  p.cu = cu;
+  p.out = static_cast<uint8_t*>(out);
+  p.n_seqs = n_seqs;
+  p.n_rows = n_rows;
+  p.hq = hq;
+  p.hkv = hkv;
+  p.group = group;
+  p.tq = tq;
+  p.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.err = err;
+  const size_t smem = 1024 + (size_t)(kTiles * kBM + 2 * kStages * kBN) * D * 2;
+  static std::atomic<uint64_t> configured{0};
+  const cudaError_t e = set_smem_limit_once(prompt_attention_kernel<D>, (int)smem, configured);
+  if (e != cudaSuccess) return e;
+  const int64_t most = prompt_items(n_seqs, n_rows, hq, hkv);
+  return launch_pdl(prompt_attention_kernel<D>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), smem, s,
+                    tq_map, tk_map, tv_map, p);
+}
+
+}  // namespace
+
+int64_t prompt_items(int32_t n_seqs, int32_t n_rows, int32_t hq, int32_t hkv) {
+  const int64_t per = kTiles * (kBM / (hq / hkv));  // tokens per item; each sequence may end inside one
+  return ((int64_t)n_rows / per + n_seqs) * hkv;
+}
+
+cudaError_t launch_prompt_attention(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,
+                                    int32_t n_rows, int32_t hq, int32_t hkv, int32_t head_dim, float scale, void* out,
+                                    int32_t sms, int32_t* err, cudaStream_t s) {
+  if (n_seqs <= 0 || n_rows <= 0) return cudaSuccess;
+  if (head_dim == 128)
+    return launch_prompt_t<128>(q, k, v, cu, n_seqs, n_rows, hq, hkv, scale, out, sms, err, s);
+  if (head_dim == 64) return launch_prompt_t<64>(q, k, v, cu, n_seqs, n_rows, hq, hkv, scale, out, sms, err, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace cb

@@ -1,0 +1,648 @@
+"""Serving calls (page tables, 4-bit cache rows, decode over 4-bit pages, packed prompts) against the
+oracle, with the sizes, masks and contents where they can go wrong, and a run of them together.
+
+Tolerances. Page tables, slots, codes and loaded rows are exact. Attention in 64 bits over the same
+rows, s = sum_j p_j |v_j|: the softmax weights (decode: times V's scale) are rounded to bf16 once,
+2^-8 relative each, so at most 2^-8 s; the output's rounding adds 2^-8 |out|. Scores are fp32 sums:
+of D products |q k| (prompt), or of groups of 32 products of |q| with 136 + code <= 143 and the offset
+136 |q| (decode), each of at most 40 roundings of 2^-23 (the matrix unit truncates); their error e
+changes a weight by a factor within exp(2 e).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving
+from oracle.attention import decode_attention
+from oracle.deviation import bf16_bits_to_f64
+from workloads.generator import f32_to_bf16_bits
+from workloads.torch_io import bf16_bits, bf16_tensor
+
+pytestmark = pytest.mark.gpu
+
+HEADS = [(4, 2, 64), (32, 8, 128), (16, 16, 128), (32, 16, 64), (16, 1, 64), (32, 2, 128), (8, 4, 128)]
+
+
+def _plan(cb, hq, hkv, d):
+    return cb.Plan(1, 1, 0, hq, hkv, d, 1e4)
+
+
+def _bits(rng, *shape, scale=1.0):
+    return f32_to_bf16_bits((scale * rng.standard_normal(shape)).astype(np.float32))
+
+
+def _f64(t):
+    return bf16_bits_to_f64(bf16_bits(t))
+
+
+def _i32(x):
+    return torch.as_tensor(np.ascontiguousarray(np.asarray(x, dtype=np.int32))).cuda()
+
+
+def _close(got, ref, vs, e, what):
+    err = np.abs(got - ref)
+    lim = (2.0**-8 + 2 * e) * vs + (2.0**-8) * np.abs(ref) + 1e-30
+    assert np.isfinite(got).all(), f"{what}: {int((~np.isfinite(got)).sum())} values are not finite"
+    assert (err <= lim).all(), f"{what}: err/limit {float((err / lim).max()):.3f}"
+
+
+# ---- page tables ----------------------------------------------------------------------------
+
+
+def _tables(cb, plan, ctx, new, page, free, table, rows, free_from=0):
+    n = len(ctx)
+    t = _i32(table)
+    out = dict(cu_seqlens=_i32(np.full(n + 1, -7)), kv_lens=_i32(np.full(n, -7)), positions=_i32(np.full(rows, -7)),
+               slots=_i32(np.full(rows, -7)), free_to=_i32([-7]))
+    args = (plan, _i32(ctx), _i32(new), page, _i32(free), t)
+    cb.cb_page_tables(*args, free_from=_i32([free_from]) if free_from else None, **out)
+    return [x.cpu().numpy().astype(np.int64) for x in (t, *out.values())]
+
+
+@pytest.mark.parametrize("n,most_ctx,most_new,page,pad", [
+    (1, 0, 1, 16, 0), (1, 16, 1, 16, 3), (3, 40, 40, 16, 0), (64, 8448, 1, 64, 0), (65, 300, 5, 48, 129),
+    (513, 100, 700, 256, 1), (700, 0, 40, 1024, 0), (4099, 200, 3, 32, 11), (16384, 50, 2, 16, 5)])
+def test_page_tables(cb, n, most_ctx, most_new, page, pad):
+    rng = np.random.default_rng(n + page)
+    plan = _plan(cb, 4, 2, 64)
+    ctx, new = rng.integers(0, most_ctx + 1, n), rng.integers(0, most_new + 1, n)
+    if n > 2:
+        ctx[1], new[1], new[n - 1] = 0, 0, 0  # a request that holds nothing and adds nothing
+    have = -(-ctx // page)
+    width = int((-(-(ctx + new) // page)).max()) + 1
+    ids = rng.permutation(int(have.sum() + (new + 1).sum()) + 5)
+    table = np.full((n, width), -1)
+    table[np.arange(width) < have[:, None]] = ids[:have.sum()]
+    free = ids[have.sum():]
+    got = _tables(cb, plan, ctx, new, page, free, table, int(new.sum()) + pad, free_from=2)
+    plan.check()
+    want = serving.page_tables(ctx.tolist(), new.tolist(), page, free, table, int(new.sum()) + pad, 2)
+    for name, g, w in zip(("table", "cu", "kv_lens", "positions", "slots", "free_to"), got, want):
+        assert np.array_equal(g.reshape(-1), np.asarray(w).reshape(-1)), name
+    plan.close()
+
+
+def test_page_tables_without_requests_or_rows(cb):
+    plan = _plan(cb, 4, 2, 64)
+    t, cu, kv, pos, slots, to = _tables(cb, plan, [], [], 16, [1, 2], np.zeros((0, 4)), 5, free_from=1)
+    assert cu.tolist() == [0] and slots.tolist() == [-1] * 5 and pos.tolist() == [0] * 5 and to.tolist() == [1]
+    t, cu, kv, pos, slots, to = _tables(cb, plan, [3], [0], 16, [], [[5]], 0)
+    assert cu.tolist() == [0, 0] and kv.tolist() == [3] and t.tolist() == [[5]] and to.tolist() == [0]
+    plan.check()
+    plan.close()
+
+
+@pytest.mark.parametrize("case", ["free list ends", "table too narrow", "rows too few", "negative length", "bad free page",
+                                  "bad held page", "negative start"])
+def test_page_tables_findings(cb, case):
+    plan = _plan(cb, 4, 2, 64)
+    ctx, new, free, table, rows, frm = [20, 3], [20, 30], [3, 4, 5, 6], [[8, 9, -1], [7, -1, -1]], 50, 0
+    if case == "free list ends":
+        free = [3, 4]
+    elif case == "table too narrow":
+        table = [[8, 9], [7, -1]]
+    elif case == "rows too few":
+        rows = 25
+    elif case == "negative length":
+        new = [20, -30]
+    elif case == "bad free page":
+        free = [3, 1 << 28, -2, 6]
+    elif case == "bad held page":
+        table[0][1] = -1
+    else:
+        frm = -5
+    t, cu, kv, pos, slots, to = _tables(cb, plan, ctx, new, 16, free, table, rows, free_from=frm)
+    with pytest.raises(cb.CacheBlendError) as e:
+        plan.check()
+    assert e.value.status == 5
+    clean = [0 if x < 0 else x for x in new]
+    ids = [x if 0 <= x < (1 << 26) else -1 for x in free]
+    wt, wcu, wkv, wpos, wslots, wto = serving.page_tables(ctx, clean, 16, ids, table, rows, max(frm, 0))
+    assert np.array_equal(cu, wcu) and np.array_equal(kv, wkv) and np.array_equal(pos, wpos) and to[0] == wto
+    assert np.array_equal(slots, wslots)
+    if case not in ("bad free page", "rows too few"):
+        assert np.array_equal(t, wt)
+    plan.check()
+    plan.close()
+
+
+# ---- rows of the 4-bit cache ----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("hkv,d", [(2, 64), (8, 128), (1, 64), (3, 128), (16, 128)])
+@pytest.mark.parametrize("n,page", [(1, 16), (7, 48), (130, 64), (333, 16)])
+def test_store_and_load(cb, hkv, d, n, page):
+    rng = np.random.default_rng(hkv * n + d)
+    plan = _plan(cb, hkv, hkv, d)
+    n_pages = -(-2 * n // page) + 2
+    slots = rng.permutation(n_pages * page)[:n]
+    if n > 3:
+        slots[2] = -1
+    k, v = _bits(rng, n, hkv, d), _bits(rng, n, hkv, d, scale=20.0)
+    kf, vf = bf16_bits_to_f64(k), bf16_bits_to_f64(v)
+    if n > 9:  # rows that a quantiser meets seldom: zeros, a single value, tiny, huge, not finite
+        for x in (k, v):
+            x[0] = 0
+            x[1] = 0
+            x[1, :, 5] = 0xC040  # -3
+            x[3, :, :] = f32_to_bf16_bits((rng.standard_normal((hkv, d)) * 1e-39).astype(np.float32))
+            x[4] = f32_to_bf16_bits((rng.standard_normal((hkv, d)) * 5e37).astype(np.float32))
+            x[5, 0, 33] = 0x7F80
+            x[6, 0, 1] = 0x7FC1
+        kf, vf = bf16_bits_to_f64(k), bf16_bits_to_f64(v)
+    before = rng.integers(0, 256, (n_pages, hkv, serving.page_bytes(page, d)), dtype=np.uint8)
+    cache = torch.as_tensor(before).cuda()
+    assert cache.shape[2] == cb.cb_kv4_page_bytes(plan, page)
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(slots), cache, page)
+    want = before.copy()
+    serving.store(want, page, slots, kf, vf)
+    got = cache.cpu().numpy()
+    ok, ov = (torch.full((n, hkv, d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cb.cb_kv4_load(plan, cache, page, _i32(slots), ok, ov)
+    plan.check()
+    if n <= 9:
+        assert np.array_equal(got, want)  # every byte, also those of other tokens and the unused ones
+    wk, wv = serving.load(want, page, np.maximum(slots, 0), d)
+    for g, w in ((_f64(ok), wk), (_f64(ov), wv)):
+        w = np.where((slots >= 0)[:, None, None], serving._to_bf16(w), 7.0)
+        assert np.array_equal(np.isnan(g), np.isnan(w))
+        assert np.array_equal(g[~np.isnan(w)], w[~np.isnan(w)])
+    # NaN scales may differ in their payload: all other bytes are the oracle's
+    differ = got != want
+    assert differ.sum() <= 4 * n * hkv and (n > 9 or not differ.any())
+    plan.close()
+
+
+def test_store_skips_and_records_slots_past_the_cache(cb):
+    rng = np.random.default_rng(5)
+    plan = _plan(cb, 4, 2, 64)
+    cache = torch.zeros((2, 2, serving.page_bytes(16, 64)), dtype=torch.uint8, device="cuda")
+    k = bf16_tensor(_bits(rng, 4, 2, 64))
+    cb.cb_kv4_store(plan, k, k, _i32([-1, 32, 1 << 30, -(1 << 31)]), cache, 16)
+    with pytest.raises(cb.CacheBlendError) as e:
+        plan.check()
+    assert e.value.status == 5 and not cache.any()
+    out = k.clone()
+    cb.cb_kv4_load(plan, cache, 16, _i32([-1, 32, 1 << 30, -5]), out, k.clone())
+    with pytest.raises(cb.CacheBlendError):
+        plan.check()
+    assert torch.equal(out.view(torch.int16), k.view(torch.int16))
+    plan.close()
+
+
+def test_rows_far_into_a_large_cache(cb):
+    # byte offsets past 2^32: pages at the end of a 6 GB cache
+    rng = np.random.default_rng(6)
+    plan = _plan(cb, 8, 8, 128)
+    page = 64
+    n_pages = 6 * (1 << 30) // (8 * serving.page_bytes(page, 128))
+    cache = torch.empty((n_pages, 8, serving.page_bytes(page, 128)), dtype=torch.uint8, device="cuda")
+    pages = np.array([n_pages - 1, 3, n_pages - 2])
+    n = 3 * page
+    slots = (pages[:, None] * page + np.arange(page)).reshape(-1)
+    k, v = _bits(rng, n, 8, 128), _bits(rng, n, 8, 128)
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(slots), cache, page)
+    ok, ov = (torch.empty((n, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cb.cb_kv4_load(plan, cache, page, _i32(slots), ok, ov)
+    qk, qv = (serving.dequantise(*serving.quantise(bf16_bits_to_f64(x))) for x in (k, v))
+    assert np.array_equal(_f64(ok), serving._to_bf16(qk)) and np.array_equal(_f64(ov), serving._to_bf16(qv))
+    q = _bits(rng, 1, 8, 128)
+    out = torch.empty((1, 8, 128), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(pages[None]), _i32([n - 3]), out)
+    plan.check()
+    ref, vs = decode_attention(bf16_bits_to_f64(q)[0], qk[:n - 3], qv[:n - 3], return_vscale=True)
+    _close(_f64(out)[0], ref, vs, 1e-3, "decode at large offsets")
+    plan.close()
+
+
+# ---- decode over 4-bit pages ----------------------------------------------------------------
+
+
+def _cache(cb, plan, rng, lens, page, spare=2, kscale=1.0, koffset=0.5):
+    """A pool with the requests' rows stored to shuffled pages, every other byte random: (cache, table,
+    K, V rows as the cache holds them per request)."""
+    hkv, d = plan.hkv, plan.head_dim
+    need = [-(-n // page) for n in lens]
+    n_pages = sum(need) + spare
+    ids = rng.permutation(n_pages)
+    table = np.full((len(lens), max(need + [1])), -1)
+    slots, at = [], 0
+    for s, n in enumerate(lens):
+        table[s, :need[s]] = ids[at:at + need[s]]
+        at += need[s]
+        pos = np.arange(n)
+        slots.append(table[s][pos // page] * page + pos % page if n else np.zeros(0, int))
+    total = sum(lens)
+    kf = kscale * rng.standard_normal((total, hkv, d)) + koffset * rng.standard_normal((1, hkv, d))
+    k, v = f32_to_bf16_bits(kf.astype(np.float32)), _bits(rng, total, hkv, d)
+    cache = torch.as_tensor(rng.integers(0, 256, (n_pages, hkv, serving.page_bytes(page, d)), dtype=np.uint8)).cuda()
+    if total:
+        cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(np.concatenate(slots)), cache, page)
+    qk, qv = (serving.dequantise(*serving.quantise(bf16_bits_to_f64(x))) for x in (k, v))
+    cut = np.cumsum([0] + list(lens))
+    return cache, table, [qk[a:b] for a, b in zip(cut, cut[1:])], [qv[a:b] for a, b in zip(cut, cut[1:])]
+
+
+def _score_error(q, rows_scale, d, scale):
+    """Bound of the fp32 error of a decode score (docstring of this file)."""
+    return scale * (d / 32) * 40 * 2.0**-23 * 32 * 143 * np.abs(q).max() * rows_scale
+
+
+def _check_decode(plan, q, out, ks, vs_rows, what, scale=None):
+    d = plan.head_dim
+    for s in range(len(ks)):
+        if len(ks[s]) == 0:
+            assert not _f64(out[s]).any(), f"{what}: request {s} without keys"
+            continue
+        ref, vs = decode_attention(bf16_bits_to_f64(q)[s], ks[s], vs_rows[s], scale=scale, return_vscale=True)
+        e = _score_error(bf16_bits_to_f64(q)[s], np.abs(ks[s]).max() / 7, d, scale or d**-0.5)
+        _close(_f64(out[s]), ref, vs, min(e, 0.01), f"{what}, request {s} of {len(ks[s])} keys")
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+@pytest.mark.parametrize("lens,page", [([1], 16), ([0], 16), ([15, 16, 17], 16), ([33, 0, 1, 100, 48], 48),
+                                       ([700, 3, 0, 0, 257], 64), ([2500], 256), ([5] * 40, 16)])
+def test_decode_lengths_and_heads(cb, hq, hkv, d, lens, page):
+    rng = np.random.default_rng(hq + hkv + d + sum(lens))
+    plan = _plan(cb, hq, hkv, d)
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, page)
+    q = _bits(rng, len(lens), hq, d)
+    out = torch.full((len(lens), hq, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32(lens), out)
+    plan.check()
+    _check_decode(plan, q, out, ks, vs, "decode")
+    first = out.clone()
+    out.fill_(4.0)
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32(lens), out)
+    assert torch.equal(first.view(torch.int16), out.view(torch.int16))  # the same bits from call to call
+    plan.close()
+
+
+@pytest.mark.parametrize("hq,hkv,d,n,page", [(32, 8, 128, 32897, 64), (16, 1, 64, 20011, 128), (4, 2, 64, 9000, 16)])
+def test_decode_long_request(cb, hq, hkv, d, n, page):
+    rng = np.random.default_rng(n)
+    plan = _plan(cb, hq, hkv, d)
+    cache, table, ks, vs = _cache(cb, plan, rng, [n], page)
+    q = _bits(rng, 1, hq, d)
+    out = torch.empty((1, hq, d), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32([n]), out)
+    plan.check()
+    _check_decode(plan, q, out, ks, vs, "long decode")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32([4321]), out, scale=0.02)
+    plan.check()
+    _check_decode(plan, q, out, [ks[0][:4321]], [vs[0][:4321]], "shorter, custom scale", scale=0.02)
+    plan.close()
+
+
+def test_decode_batch_of_many_lengths(cb):
+    rng = np.random.default_rng(12)
+    plan = _plan(cb, 32, 8, 128)
+    lens = [int(x) for x in rng.integers(0, 1500, 90)]
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, 32)
+    q = _bits(rng, len(lens), 32, 128)
+    out = torch.empty((len(lens), 32, 128), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, 32, _i32(table), _i32(lens), out)
+    plan.check()
+    _check_decode(plan, q, out, ks, vs, "batch")
+    plan.close()
+
+
+def test_decode_scores_that_jump_late(cb):
+    # keys aligned with their heads' queries far into the cache: the running max moves by large steps,
+    # within a warp's run and between the partials that are merged
+    rng = np.random.default_rng(13)
+    hq, hkv, d, page, n = 8, 2, 128, 64, 6000
+    plan = _plan(cb, hq, hkv, d)
+    q = _bits(rng, 1, hq, d)
+    qf = bf16_bits_to_f64(q).reshape(hkv, hq // hkv, d).mean(1)
+    kf = 0.3 * rng.standard_normal((n, hkv, d))
+    for at, size in ((40, 2.0), (41, 6.0), (3000, 12.0), (n - 1, 14.0)):
+        kf[at] = size * qf
+    k, v = f32_to_bf16_bits(kf.astype(np.float32)), _bits(rng, n, hkv, d)
+    table = rng.permutation(-(-n // page))[None]
+    cache = torch.zeros((table.size, hkv, serving.page_bytes(page, d)), dtype=torch.uint8, device="cuda")
+    pos = np.arange(n)
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(table[0][pos // page] * page + pos % page), cache, page)
+    qk, qv = (serving.dequantise(*serving.quantise(bf16_bits_to_f64(x))) for x in (k, v))
+    out = torch.empty((1, hq, d), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32([n]), out)
+    plan.check()
+    _check_decode(plan, q, out, [qk], [qv], "late jumps")
+    plan.close()
+
+
+def test_decode_rows_that_are_not_finite_stay_with_their_request(cb):
+    rng = np.random.default_rng(14)
+    plan = _plan(cb, 8, 2, 64)
+    lens, page = [40, 40, 21], 16
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, page)
+    bad = _bits(rng, 2, 2, 64)
+    bad[0, 0, 3], bad[1, 0, 3] = 0x7F80, 0x7FC0
+    # one inside request 1, one in the unused part of request 2's last page (position 21)
+    slots = [table[1, 1] * page + 2, table[2, 1] * page + 5]
+    cb.cb_kv4_store(plan, bf16_tensor(bad), bf16_tensor(bad), _i32(slots), cache, page)
+    q = _bits(rng, 3, 8, 64)
+    out = torch.empty((3, 8, 64), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32(lens), out)
+    plan.check()
+    got = _f64(out)
+    assert np.isnan(got[1, :4]).all()  # kv head 0 of request 1: its scores hold a NaN
+    assert np.isfinite(got[[0, 2]]).all() and np.isfinite(got[1, 4:]).all()
+    for s in (0, 2):
+        ref, sc = decode_attention(bf16_bits_to_f64(q)[s], ks[s], vs[s], return_vscale=True)
+        _close(got[s], ref, sc, 1e-3, f"request {s}")
+    plan.close()
+
+
+def test_decode_bad_pages_and_lengths_are_left_out_and_recorded(cb):
+    rng = np.random.default_rng(15)
+    plan = _plan(cb, 8, 2, 128)
+    lens, page = [64, 40, 30], 16
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, page)
+    q = _bits(rng, 3, 8, 128)
+    out = torch.empty((3, 8, 128), dtype=torch.bfloat16, device="cuda")
+    broken = table.copy()
+    broken[0, 1], broken[0, 2] = cache.shape[0], -3
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(broken), _i32(lens), out)
+    with pytest.raises(cb.CacheBlendError) as e:
+        plan.check()
+    assert e.value.status == 5
+    keep = np.r_[0:16, 48:64]
+    _check_decode(plan, q, out, [ks[0][keep], ks[1], ks[2]], [vs[0][keep], vs[1], vs[2]], "bad pages")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32([1000, -5, 30]), out)
+    with pytest.raises(cb.CacheBlendError):
+        plan.check()
+    _check_decode(plan, q, out, [ks[0], [], ks[2]], [vs[0], [], vs[2]], "bad lengths")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32(lens), out)
+    plan.check()  # and the plan works as before
+    _check_decode(plan, q, out, ks, vs, "after")
+    plan.close()
+
+
+# ---- packed prompts -------------------------------------------------------------------------
+
+
+def _prompt(cb, plan, q, k, v, cu, scale=0.0, out=None):
+    out = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device="cuda") if out is None else out
+    cb.cb_prompt_attention(plan, bf16_tensor(q), bf16_tensor(k), bf16_tensor(v), _i32(cu), out, scale=scale)
+    return out
+
+
+def _check_prompt(q, k, v, cu, out, what, scale=None):
+    qf, kf, vf = (bf16_bits_to_f64(x) for x in (q, k, v))
+    ref, vs = serving.packed_attention(qf, kf, vf, cu, scale=scale)
+    got = _f64(out)
+    inside = np.zeros(len(q), bool)
+    for a, b in zip(cu, cu[1:]):
+        inside[a:b] = True
+    assert (got[~inside] == 9.0).all(), f"{what}: rows of no sequence were written"
+    d = q.shape[2]
+    e = (scale or d**-0.5) * 40 * 2.0**-23 * d * np.abs(qf).max() * np.abs(kf).max()
+    _close(got[inside], ref[inside], vs[inside], min(e, 0.01), what)
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS + [(64, 8, 128)])
+@pytest.mark.parametrize("lens,pad", [([1], 0), ([1, 1, 1], 5), ([0, 5, 0], 1), ([127, 128, 129], 0), ([64, 65, 63, 1, 300], 17),
+                                      ([513], 3), ([256, 0, 31, 32, 33], 0)])
+def test_prompt_lengths_and_heads(cb, hq, hkv, d, lens, pad):
+    rng = np.random.default_rng(hq + d + sum(lens))
+    plan = _plan(cb, hq, hkv, d)
+    n = sum(lens) + pad
+    q, k, v = _bits(rng, n, hq, d), _bits(rng, n, hkv, d), _bits(rng, n, hkv, d)
+    cu = np.cumsum([0] + lens)
+    out = _prompt(cb, plan, q, k, v, cu)
+    plan.check()
+    _check_prompt(q, k, v, cu, out, "prompt")
+    plan.close()
+
+
+@pytest.mark.parametrize("lens", [[2100], [1500, 40, 700, 0, 1, 900], [31] * 70])
+def test_prompt_more_items_than_sms(cb, lens):
+    rng = np.random.default_rng(sum(lens))
+    plan = _plan(cb, 32, 8, 128)
+    n = sum(lens)
+    q, k, v = _bits(rng, n, 32, 128), _bits(rng, n, 8, 128), _bits(rng, n, 8, 128)
+    cu = np.cumsum([0] + lens)
+    out = _prompt(cb, plan, q, k, v, cu, scale=0.05)
+    plan.check()
+    _check_prompt(q, k, v, cu, out, "prompt", scale=0.05)
+    again = _prompt(cb, plan, q, k, v, cu, scale=0.05)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+    plan.close()
+
+
+def test_prompt_many_sequences(cb):
+    rng = np.random.default_rng(30)
+    plan = _plan(cb, 4, 2, 64)
+    lens = [int(x) for x in rng.integers(0, 40, 1500)]
+    n = sum(lens) + 2
+    q, k, v = _bits(rng, n, 4, 64), _bits(rng, n, 2, 64), _bits(rng, n, 2, 64)
+    cu = np.cumsum([0] + lens)
+    out = _prompt(cb, plan, q, k, v, cu)
+    plan.check()
+    _check_prompt(q, k, v, cu, out, "many sequences")
+    plan.close()
+
+
+def test_prompt_first_offset_and_unaligned_output(cb):
+    # the first sequence starts behind row 0; the output is 16-byte but not 32-byte aligned
+    rng = np.random.default_rng(31)
+    plan = _plan(cb, 8, 2, 64)
+    cu = np.array([6, 106, 170])
+    q, k, v = _bits(rng, 190, 8, 64), _bits(rng, 190, 2, 64), _bits(rng, 190, 2, 64)
+    whole = torch.full((190 * 8 * 64 + 8,), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = _prompt(cb, plan, q, k, v, cu, out=whole[8:].view(190, 8, 64))
+    plan.check()
+    _check_prompt(q, k, v, cu, out, "unaligned")
+    assert (whole[:8] == 9.0).all()
+    plan.close()
+
+
+def test_prompt_scores_that_jump(cb):
+    # keys aligned with the queries in later key tiles: the softmax's reference has to move
+    rng = np.random.default_rng(32)
+    hq, hkv, d, n = 8, 2, 128, 700
+    plan = _plan(cb, hq, hkv, d)
+    q = _bits(rng, n, hq, d)
+    base = rng.standard_normal((hkv, d))
+    qf = 0.5 * rng.standard_normal((n, hq, d)) + np.repeat(base, hq // hkv, 0)
+    q = f32_to_bf16_bits(qf.astype(np.float32))
+    kf = 0.3 * rng.standard_normal((n, hkv, d))
+    for at, size in ((3, 0.5), (130, 1.5), (300, 3.0), (301, -3.0), (511, 5.0), (640, 9.0)):
+        kf[at] = size * base
+    k, v = f32_to_bf16_bits(kf.astype(np.float32)), _bits(rng, n, hkv, d)
+    out = _prompt(cb, plan, q, k, v, [0, n])
+    plan.check()
+    _check_prompt(q, k, v, [0, n], out, "jumps")
+    plan.close()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (32, 8, 128), (4, 4, 128)])
+def test_prompt_values_that_are_not_finite_reach_only_rows_that_see_them(cb, hq, hkv, d):
+    rng = np.random.default_rng(33)
+    plan = _plan(cb, hq, hkv, d)
+    lens, pad = [70, 100, 300], 30
+    n = sum(lens) + pad
+    cu = np.cumsum([0] + lens)
+    q, k, v = _bits(rng, n, hq, d), _bits(rng, n, hkv, d), _bits(rng, n, hkv, d)
+    clean_k, clean_v = k.copy(), v.copy()
+    k[470:], v[470:] = 0x7FC0, 0x7F80  # behind the last sequence
+    v[90, 1, 5], k[95, 1, 7] = 0x7FC0, 0x7F80  # in sequence 1, at its tokens 20 and 25
+    v[170 + 250, 0, 9] = 0xFF80  # -inf in sequence 2, at its token 250
+    v[170 + 20, 1, 11], v[170 + 220, 1, 11] = 0x7F80, 0xFF80  # +inf, then -inf: NaN from token 220 on
+    out = _prompt(cb, plan, q, k, v, cu)
+    plan.check()
+    got = _f64(out)
+    ref, vs = serving.packed_attention(*(bf16_bits_to_f64(x) for x in (q, clean_k, clean_v)), cu)
+    g = hq // hkv
+    want_nan = np.zeros(got.shape, bool)
+    want_inf = np.zeros(got.shape)
+    want_nan[90:170, g:2 * g, 5] = True
+    want_nan[95:170, g:2 * g, :] |= bf16_bits_to_f64(q)[95:170, g:2 * g, 7:8] > 0  # a score of +inf
+    want_inf[420:470, :g, 9] = -np.inf
+    want_inf[190:390, g:2 * g, 11] = np.inf
+    want_nan[390:470, g:2 * g, 11] = True
+    # an infinite key gives a score of +inf (NaN weights) or -inf (no weight: that row stays finite)
+    row_inf = np.zeros(got.shape, bool)
+    row_inf[95:170, g:2 * g, :] = True
+    assert np.isnan(got[want_nan]).all()
+    fixed = (want_inf != 0) & ~want_nan
+    assert np.array_equal(got[fixed], want_inf[fixed])
+    rest = ~want_nan & ~fixed & ~row_inf
+    rest[470:] = False
+    assert np.isfinite(got[rest]).all()
+    err = np.abs(got - ref)[rest]
+    assert (err <= (2.0**-8 + 0.002) * vs[rest] + 2.0**-8 * np.abs(ref[rest])).all()
+    assert (got[470:] == 9.0).all()
+    plan.close()
+
+
+def test_prompt_offsets_that_fall_or_leave_the_rows(cb):
+    rng = np.random.default_rng(34)
+    plan = _plan(cb, 8, 2, 128)
+    q, k, v = _bits(rng, 100, 8, 128), _bits(rng, 100, 2, 128), _bits(rng, 100, 2, 128)
+    for cu, clean in (([0, 60, 140], [0, 60, 100]), ([-4, 50, 100], [0, 50, 100]), ([0, 70, 50, 50], [0, 70]),
+                      ([200, 300], [100])):
+        out = _prompt(cb, plan, q, k, v, cu)
+        with pytest.raises(cb.CacheBlendError) as e:
+            plan.check()
+        assert e.value.status == 5
+        _check_prompt(q, k, v, clean, out, f"offsets {cu}")
+    plan.close()
+
+
+# ---- together ---------------------------------------------------------------------------------
+
+
+def test_serving_a_batch_end_to_end(cb):
+    """Three prompts are laid out, encoded, attended and cached in 4 bits, then two decode steps follow,
+    the second and later ones as one captured graph; every step against the oracle."""
+    from oracle.rope import rope_rotate
+
+    hq, hkv, d, page, theta = 8, 2, 128, 32, 1e4
+    rng = np.random.default_rng(40)
+    plan = cb.Plan(1, 512, 0, hq, hkv, d, theta)
+    lens, width, pool = [75, 0, 200], 9, 24
+    n = len(lens)
+    free = rng.permutation(pool)
+    cache = torch.as_tensor(rng.integers(0, 256, (pool, hkv, serving.page_bytes(page, d)), dtype=np.uint8)).cuda()
+    table = _i32(np.full((n, width), -1))
+    ctx, kv, new, frm, to = _i32([0] * n), _i32([0] * n), _i32(lens), _i32([0]), _i32([0])
+    host_k, host_v = [[] for _ in lens], [[] for _ in lens]
+
+    def bufs(rows):
+        return {"cu_seqlens": _i32(np.zeros(n + 1)), "positions": _i32(np.zeros(rows)), "slots": _i32(np.zeros(rows))}
+
+    def lay_out(b):
+        cb.cb_page_tables(plan, ctx, new, page, _i32_free, table, kv_lens=kv, free_to=to, free_from=frm, **b)
+
+    _i32_free = _i32(free)
+    # the prompts: 275 rows in buffers of 300
+    rows = 300
+    b = bufs(rows)
+    q0, k0, v0 = _bits(rng, rows, hq, d), _bits(rng, rows, hkv, d), _bits(rng, rows, hkv, d)
+    q, k, v = bf16_tensor(q0), bf16_tensor(k0), bf16_tensor(v0)
+    lay_out(b)
+    qe, ke = torch.empty_like(q), torch.empty_like(k)
+    cb.cb_rope_rerotate(plan, qe, q, b["positions"])
+    cb.cb_rope_rerotate(plan, ke, k, b["positions"])
+    out = torch.full_like(q, 9.0)
+    cb.cb_prompt_attention(plan, qe, ke, v, b["cu_seqlens"], out)
+    cb.cb_kv4_store(plan, ke, v, b["slots"], cache, page)
+    plan.check()
+    cu = np.cumsum([0] + lens)
+    assert b["cu_seqlens"].cpu().numpy().tolist() == cu.tolist() and kv.cpu().numpy().tolist() == lens
+    pos = np.concatenate([np.arange(x) for x in lens])
+    assert np.array_equal(b["positions"].cpu().numpy()[:275], pos)
+    ref = rope_rotate(bf16_bits_to_f64(k0[:275]), pos, theta, "half")
+    assert np.abs(_f64(ke)[:275] - ref).max() <= 2e-2 + 1e-2 * np.abs(ref).max()
+    _check_prompt(bf16_bits(qe), bf16_bits(ke), v0, cu, out, "prompts")
+    for s in range(n):
+        host_k[s] = [bf16_bits(ke)[cu[s]:cu[s + 1]]]
+        host_v[s] = [v0[cu[s]:cu[s + 1]]]
+    # decode steps: request 1 joins with its first token, request 2 crosses a page
+    b = bufs(n)
+    q1, k1, v1 = (torch.zeros((n, h, d), dtype=torch.bfloat16, device="cuda") for h in (hq, hkv, hkv))
+    qe, ke, out = torch.empty_like(q1), torch.empty_like(k1), torch.empty_like(q1)
+    new.fill_(1)
+
+    def decode_step():
+        ctx.copy_(kv)
+        frm.copy_(to)
+        lay_out(b)
+        cb.cb_rope_rerotate(plan, qe, q1, b["positions"])
+        cb.cb_rope_rerotate(plan, ke, k1, b["positions"])
+        cb.cb_kv4_store(plan, ke, v1, b["slots"], cache, page)
+        cb.cb_kv4_decode_attention(plan, qe, cache, page, table, kv, out)
+
+    graph = None
+    for step in range(26):
+        q0, k0, v0 = _bits(rng, n, hq, d), _bits(rng, n, hkv, d), _bits(rng, n, hkv, d)
+        for dst, src in ((q1, q0), (k1, k0), (v1, v0)):
+            dst.copy_(bf16_tensor(src))
+        if step == 0:
+            decode_step()
+        elif graph is None:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                decode_step()
+        if graph is not None:
+            graph.replay()
+        plan.check()
+        for s in range(n):
+            host_k[s].append(bf16_bits(ke)[s:s + 1])
+            host_v[s].append(v0[s:s + 1])
+        if step in (0, 1, 24, 25):
+            ks, vs = ([serving.dequantise(*serving.quantise(bf16_bits_to_f64(np.concatenate(x)))) for x in h]
+                      for h in (host_k, host_v))
+            assert kv.cpu().numpy().tolist() == [len(x) for x in ks]
+            _check_decode(plan, bf16_bits(qe), out, ks, vs, f"decode step {step}")
+    # the first request's chunk read back for a blend
+    slots = _i32(table.cpu().numpy()[0][np.arange(75) // page] * page + np.arange(75) % page)
+    ko, vo = (torch.empty((75, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cb.cb_kv4_load(plan, cache, page, slots, ko, vo)
+    plan.check()
+    want = serving._to_bf16(serving.dequantise(*serving.quantise(bf16_bits_to_f64(host_k[0][0]))))
+    assert np.array_equal(_f64(ko), want)
+    plan.close()
+
+
+def test_calls_on_another_stream(cb):
+    rng = np.random.default_rng(41)
+    plan = _plan(cb, 8, 2, 64)
+    lens, page = [90, 33], 16
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, page)
+    q = _bits(rng, 2, 8, 64)
+    out = torch.empty((2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    dq, dt, dl = bf16_tensor(q), _i32(table), _i32(lens)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        cb.cb_kv4_decode_attention(plan, dq, cache, page, dt, dl, out)
+    cb.cb_kv4_decode_attention(plan, dq, cache, page, dt, dl, out, stream=side)
+    side.synchronize()
+    plan.check()
+    _check_decode(plan, q, out, ks, vs, "another stream")
+    plan.close()

@@ -1,0 +1,155 @@
+"""Host checks of the serving calls (page tables, 4-bit cache, packed prompts): every refusal comes
+before any CUDA call, so these run without a GPU on a plan that never touches one."""
+
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from rag_kv_cache_gb300 import _lib
+    from rag_kv_cache_gb300.build import build
+
+    return _lib.load(build())
+
+
+@pytest.fixture()
+def plan():
+    """Memory shaped like the head of a plan: the config alone, which is all the host checks read."""
+    from rag_kv_cache_gb300 import _lib
+
+    raw = ctypes.create_string_buffer(4096)
+    cfg = _lib.CbConfig(1, 1, 0, 8, 2, 128, 1e4, 0, 15, 15)
+    ctypes.memmove(raw, ctypes.byref(cfg), ctypes.sizeof(cfg))
+    return raw
+
+
+P = 1 << 20  # an aligned address that no refused call reads
+
+
+def _refused(lib, status, word, want=1):
+    assert status == want, lib.cb_last_error_string()
+    assert word in lib.cb_last_error_string().decode()
+
+
+def test_page_bytes(lib, plan):
+    assert lib.cb_kv4_page_bytes(plan, 16) == 18 * 128
+    assert lib.cb_kv4_page_bytes(plan, 1024) == 64 * 18 * 128
+    for bad in (0, -16, 8, 24, 1040):
+        assert lib.cb_kv4_page_bytes(plan, bad) == 0
+    assert lib.cb_kv4_page_bytes(None, 16) == 0
+
+
+def test_page_tables_refusals(lib, plan):
+    def call(plan_=plan, ctx=P, new=P + 64, n=4, page=16, free=P, n_free=9, frm=None, table=P, width=8, cu=P, kv=P + 128,
+             pos=P, slots=P, rows=5, to=P + 192):
+        return lib.cb_page_tables(plan_, ctx, new, n, page, free, n_free, frm, table, width, cu, kv, pos, slots, rows, to,
+                                  None)
+
+    _refused(lib, call(plan_=None), "plan")
+    for page in (0, 8, 17, 2048):
+        _refused(lib, call(page=page), "page_size")
+    for name in ("n", "n_free", "width", "rows"):
+        _refused(lib, call(**{name: -1}), "negative")
+    _refused(lib, call(n=16385), "n_seqs", 2)
+    _refused(lib, call(n=16384, width=1 << 17), "too large")
+    _refused(lib, call(width=1 << 28, n=1), "too large")
+    for name, said in (("ctx", "ctx_lens"), ("new", "new_lens"), ("free", "free_pages"), ("table", "table"), ("cu", "cu_seqlens"),
+                       ("kv", "kv_lens"), ("pos", "positions"), ("slots", "slots"), ("to", "free_to")):
+        _refused(lib, call(**{name: None}), said)
+    _refused(lib, call(kv=P), "kv_lens must not be")
+    _refused(lib, call(kv=P + 64), "kv_lens must not be")
+    _refused(lib, call(frm=P + 192), "free_to must not be")
+
+
+def test_rows_refusals(lib, plan):
+    for fn, order in ((lib.cb_kv4_store, "kvsn"), (lib.cb_kv4_load, "c")):
+        def call(plan_=plan, k=P, v=P, slots=P, n=3, cache=P, pages=2, page=16):
+            if order == "c":
+                return fn(plan_, cache, pages, page, slots, n, k, v, None)
+            return fn(plan_, k, v, slots, n, cache, pages, page, None)
+
+        _refused(lib, call(plan_=None), "plan")
+        _refused(lib, call(n=-1), "n < 0")
+        _refused(lib, call(pages=-1), "n_pages")
+        _refused(lib, call(page=20), "page_size")
+        _refused(lib, call(pages=1 << 27), "2^31")
+        for name in ("k", "v", "slots", "cache"):
+            _refused(lib, call(**{name: None}), name)
+        for name in ("k", "v", "cache"):
+            _refused(lib, call(**{name: P + 8}), "16-byte")
+        assert call(n=0, k=None, v=None, slots=None, cache=None) == 0  # nothing to do
+
+
+def test_decode_refusals(lib, plan):
+    def call(plan_=plan, q=P, cache=P, pages=2, page=16, table=P, width=4, lens=P, n=3, out=P):
+        return lib.cb_kv4_decode_attention(plan_, q, cache, pages, page, table, width, lens, n, 0.0, out, None)
+
+    _refused(lib, call(plan_=None), "plan")
+    _refused(lib, call(page=12), "page_size")
+    _refused(lib, call(pages=-2), "n_pages")
+    for name in ("n", "width"):
+        _refused(lib, call(**{name: -1}), "negative")
+    _refused(lib, call(n=1 << 30), "2^31")
+    _refused(lib, call(width=1 << 28), "2^31")
+    for name, said in (("q", "q"), ("cache", "cache"), ("table", "table"), ("lens", "kv_lens"), ("out", "out")):
+        _refused(lib, call(**{name: None}), said)
+    for name in ("q", "cache", "out"):
+        _refused(lib, call(**{name: P + 4}), "16-byte")
+    assert call(n=0, q=None) == 0
+
+
+def test_prompt_refusals(lib, plan):
+    def call(plan_=plan, q=P, k=P + 4096, v=P + 4096, cu=P, n=2, rows=8, out=P + 8192):
+        return lib.cb_prompt_attention(plan_, q, k, v, cu, n, rows, 0.0, out, None)
+
+    _refused(lib, call(plan_=None), "plan")
+    for name in ("n", "rows"):
+        _refused(lib, call(**{name: -1}), "negative")
+    _refused(lib, call(n=1 << 30), "work items")
+    for name, said in (("q", "q"), ("k", "k"), ("v", "v"), ("cu", "cu_seqlens"), ("out", "out")):
+        _refused(lib, call(**{name: None}), said)
+    for name in ("q", "k", "v", "out"):
+        _refused(lib, call(**{name: P + 8192 + 2}), "16-byte")
+    _refused(lib, call(out=P), "out must not be")
+    _refused(lib, call(out=P + 4096), "out must not be")
+    assert call(n=0, q=None) == 0 and call(rows=0, q=None) == 0
+
+
+class _FakePlan:
+    hq, hkv, head_dim, device, handle = 8, 2, 128, 0, None
+
+
+def test_binding_checks_shapes_before_the_library(lib, plan):
+    import rag_kv_cache_gb300 as cb
+
+    p = _FakePlan()
+    p.handle = plan
+    assert cb.cb_kv4_page_bytes(p, 64) == 4 * 18 * 128
+    with pytest.raises(cb.CacheBlendError):
+        cb.cb_kv4_page_bytes(p, 20)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    cache = torch.zeros((3, 2, 18 * 128), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="k must have shape"):
+        cb.cb_kv4_store(p, bf(4, 3, 128), bf(4, 2, 128), i32(4), cache, 16)
+    with pytest.raises(ValueError, match="slots must have shape"):
+        cb.cb_kv4_store(p, bf(4, 2, 128), bf(4, 2, 128), i32(5), cache, 16)
+    with pytest.raises(ValueError, match="on a CUDA device"):
+        cb.cb_kv4_load(p, cache, 16, i32(4), bf(4, 2, 128), bf(4, 2, 128))
+    with pytest.raises(ValueError, match="q must have shape"):
+        cb.cb_kv4_decode_attention(p, bf(2, 8, 64), cache, 16, i32(2, 4), i32(2), bf(2, 8, 128))
+    with pytest.raises(ValueError, match="table must have shape"):
+        cb.cb_kv4_decode_attention(p, bf(2, 8, 128), cache, 16, i32(3, 4), i32(2), bf(2, 8, 128))
+    with pytest.raises(ValueError, match="cache must have shape"):
+        cb.cb_kv4_decode_attention(p, bf(2, 8, 128), cache, 32, i32(2, 4), i32(2), bf(2, 8, 128))
+    with pytest.raises(ValueError, match="first offset"):
+        cb.cb_prompt_attention(p, bf(5, 8, 128), bf(5, 2, 128), bf(5, 2, 128), i32(0), bf(5, 8, 128))
+    with pytest.raises(ValueError, match="v must have shape"):
+        cb.cb_prompt_attention(p, bf(5, 8, 128), bf(5, 2, 128), bf(4, 2, 128), i32(2), bf(5, 8, 128))
+    with pytest.raises(ValueError, match="new_lens must have shape"):
+        cb.cb_page_tables(p, i32(3), i32(2), 16, i32(9), i32(3, 4), i32(4), i32(3), i32(5), i32(5), i32(1))
+    with pytest.raises(ValueError, match="cu_seqlens must have shape"):
+        cb.cb_page_tables(p, i32(3), i32(3), 16, i32(9), i32(3, 4), i32(3), i32(3), i32(5), i32(5), i32(1))
