@@ -219,21 +219,31 @@ def cb_kv4_page_bytes(plan, page_size) -> int:
     return n
 
 
-def _shape(t, name, *want):
-    """want: sizes, None for any."""
-    if t is not None and (t.dim() != len(want) or any(w is not None and w != n for n, w in zip(t.shape, want))):
-        raise ValueError(f"{name} must have shape {tuple('*' if w is None else w for w in want)}, got {tuple(t.shape)}")
+def _arg(plan, t, dtype, shape, name):
+    """Device pointer of a tensor that must be a contiguous `dtype` tensor of `shape` on the plan's device."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == plan.device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _ptr(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, the plan on cuda:{plan.device}")
 
 
-def _same_device(plan, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != plan.device:
-            raise ValueError(f"{name} is on {t.device}, the plan on cuda:{plan.device}")
+def _size(t, name, dim=0, dims=1):
+    """Size `dim` of a tensor of `dims` dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dim(s), got shape {tuple(t.shape)}")
+    return t.shape[dim]
 
 
 def _kv4_cache(plan, cache, page_size):
-    _shape(cache, "cache", None, plan.hkv, cb_kv4_page_bytes(plan, page_size))
-    return _ptr(cache, torch.uint8, "cache"), cache.shape[0]
+    n_pages = _size(cache, "cache", 0, 3)
+    return _arg(plan, cache, torch.uint8, (n_pages, plan.hkv, cb_kv4_page_bytes(plan, page_size)), "cache"), n_pages
 
 
 def cb_page_tables(plan, ctx_lens, new_lens, page_size, free_pages, table, cu_seqlens, kv_lens, positions, slots,
@@ -241,80 +251,60 @@ def cb_page_tables(plan, ctx_lens, new_lens, page_size, free_pages, table, cu_se
     """Page table rows, packed offsets, positions and slots of one step from the requests' lengths
     (see cacheblend.h): ctx_lens, new_lens, kv_lens [n], table [n, width], cu_seqlens [n + 1],
     positions and slots [n_rows], free_from and free_to [1]; all int32 on the device."""
-    n, rows = ctx_lens.numel(), slots.numel()
-    for name, t, size in (("ctx_lens", ctx_lens, n), ("new_lens", new_lens, n), ("kv_lens", kv_lens, n),
-                          ("cu_seqlens", cu_seqlens, n + 1), ("positions", positions, rows), ("slots", slots, rows),
-                          ("free_pages", free_pages, None), ("free_from", free_from, 1), ("free_to", free_to, 1)):
-        _shape(t, name, size)
-    _shape(table, "table", n, None)
-    _same_device(plan, ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages, table=table,
-                 cu_seqlens=cu_seqlens, kv_lens=kv_lens, positions=positions, slots=slots, free_to=free_to,
-                 free_from=free_from)
-    i32 = torch.int32
+    n, rows, free = _size(ctx_lens, "ctx_lens"), _size(slots, "slots"), _size(free_pages, "free_pages")
+    width = _size(table, "table", 1, 2)
+    arg = lambda t, name, *shape: _arg(plan, t, torch.int32, shape, name)  # noqa: E731
     check(_lib.load().cb_page_tables(
-        plan.handle, _ptr(ctx_lens, i32, "ctx_lens"), _ptr(new_lens, i32, "new_lens"), n, page_size,
-        _ptr(free_pages, i32, "free_pages"), free_pages.numel(), _ptr(free_from, i32, "free_from"),
-        _ptr(table, i32, "table"), table.shape[1], _ptr(cu_seqlens, i32, "cu_seqlens"), _ptr(kv_lens, i32, "kv_lens"),
-        _ptr(positions, i32, "positions"), _ptr(slots, i32, "slots"), rows, _ptr(free_to, i32, "free_to"),
-        _stream(stream)))
+        plan.handle, arg(ctx_lens, "ctx_lens", n), arg(new_lens, "new_lens", n), n, page_size,
+        arg(free_pages, "free_pages", free), free, arg(free_from, "free_from", 1), arg(table, "table", n, width), width,
+        arg(cu_seqlens, "cu_seqlens", n + 1), arg(kv_lens, "kv_lens", n), arg(positions, "positions", rows),
+        arg(slots, "slots", rows), rows, arg(free_to, "free_to", 1), _stream(stream)))
 
 
 def _kv4_rows(plan, k, v, slots):
-    _shape(k, "k", None, plan.hkv, plan.head_dim)
-    _shape(v, "v", k.shape[0], plan.hkv, plan.head_dim)
-    _shape(slots, "slots", k.shape[0])
-    return (_ptr(k, torch.bfloat16, "k"), _ptr(v, torch.bfloat16, "v"), _ptr(slots, torch.int32, "slots"),
-            k.shape[0])
+    n = _size(slots, "slots")
+    shape = (n, plan.hkv, plan.head_dim)
+    return (_arg(plan, k, torch.bfloat16, shape, "k"), _arg(plan, v, torch.bfloat16, shape, "v"),
+            _arg(plan, slots, torch.int32, (n,), "slots"), n)
 
 
 def cb_kv4_store(plan, k, v, slots, cache, page_size, stream=None):
     """Rows k, v [n, hkv, D] quantised to 4 bits into cache at slots [n] (negative: skipped)."""
-    pk, pv, ps, n = _kv4_rows(plan, k, v, slots)
     pc, n_pages = _kv4_cache(plan, cache, page_size)
-    _same_device(plan, k=k, v=v, slots=slots, cache=cache)
+    pk, pv, ps, n = _kv4_rows(plan, k, v, slots)
     check(_lib.load().cb_kv4_store(plan.handle, pk, pv, ps, n, pc, n_pages, page_size, _stream(stream)))
 
 
 def cb_kv4_load(plan, cache, page_size, slots, k, v, stream=None):
     """k, v [n, hkv, D] = the rows that cache holds at slots [n] (negative: left as they are)."""
-    pk, pv, ps, n = _kv4_rows(plan, k, v, slots)
     pc, n_pages = _kv4_cache(plan, cache, page_size)
-    _same_device(plan, k=k, v=v, slots=slots, cache=cache)
+    pk, pv, ps, n = _kv4_rows(plan, k, v, slots)
     check(_lib.load().cb_kv4_load(plan.handle, pc, n_pages, page_size, ps, n, pk, pv, _stream(stream)))
 
 
 def cb_kv4_decode_attention(plan, q, cache, page_size, table, kv_lens, out, scale=0.0, stream=None):
     """One decode step of a batch: q, out [n, Hq, D] over the pages table [n, width] of the 4-bit cache,
     kv_lens [n] keys each (0: zeros)."""
-    n = kv_lens.numel()
-    _shape(kv_lens, "kv_lens", n)
-    _shape(q, "q", n, plan.hq, plan.head_dim)
-    _shape(out, "out", n, plan.hq, plan.head_dim)
-    _shape(table, "table", n, None)
+    n, width = _size(kv_lens, "kv_lens"), _size(table, "table", 1, 2)
+    shape = (n, plan.hq, plan.head_dim)
     pc, n_pages = _kv4_cache(plan, cache, page_size)
-    _same_device(plan, q=q, cache=cache, table=table, kv_lens=kv_lens, out=out)
     check(_lib.load().cb_kv4_decode_attention(
-        plan.handle, _ptr(q, torch.bfloat16, "q"), pc, n_pages, page_size, _ptr(table, torch.int32, "table"),
-        table.shape[1], _ptr(kv_lens, torch.int32, "kv_lens"), n, float(scale), _ptr(out, torch.bfloat16, "out"),
-        _stream(stream)))
+        plan.handle, _arg(plan, q, torch.bfloat16, shape, "q"), pc, n_pages, page_size,
+        _arg(plan, table, torch.int32, (n, width), "table"), width, _arg(plan, kv_lens, torch.int32, (n,), "kv_lens"), n,
+        float(scale), _arg(plan, out, torch.bfloat16, shape, "out"), _stream(stream)))
 
 
 def cb_prompt_attention(plan, q, k, v, cu_seqlens, out, scale=0.0, stream=None):
     """Causal attention of packed prompts: q, out [n_rows, Hq, D], k, v [n_rows, Hkv, D], sequence s in
     rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 on the device); rows in none keep their out."""
-    n = q.shape[0]
-    _shape(q, "q", n, plan.hq, plan.head_dim)
-    _shape(out, "out", n, plan.hq, plan.head_dim)
-    _shape(k, "k", n, plan.hkv, plan.head_dim)
-    _shape(v, "v", n, plan.hkv, plan.head_dim)
-    _shape(cu_seqlens, "cu_seqlens", None)
-    if cu_seqlens.numel() == 0:
+    rows, n = _size(q, "q", 0, 3), _size(cu_seqlens, "cu_seqlens")
+    if n == 0:
         raise ValueError("cu_seqlens must hold at least the first offset")
-    _same_device(plan, q=q, k=k, v=v, cu_seqlens=cu_seqlens, out=out)
+    bf, q_shape, kv_shape = torch.bfloat16, (rows, plan.hq, plan.head_dim), (rows, plan.hkv, plan.head_dim)
     check(_lib.load().cb_prompt_attention(
-        plan.handle, _ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"), _ptr(v, torch.bfloat16, "v"),
-        _ptr(cu_seqlens, torch.int32, "cu_seqlens"), cu_seqlens.numel() - 1, n, float(scale),
-        _ptr(out, torch.bfloat16, "out"), _stream(stream)))
+        plan.handle, _arg(plan, q, bf, q_shape, "q"), _arg(plan, k, bf, kv_shape, "k"), _arg(plan, v, bf, kv_shape, "v"),
+        _arg(plan, cu_seqlens, torch.int32, (n,), "cu_seqlens"), n - 1, rows, float(scale),
+        _arg(plan, out, bf, q_shape, "out"), _stream(stream)))
 
 
 def cb_attention_uses_paired_tiles(plan, mq) -> bool:

@@ -646,7 +646,7 @@ cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const
   CB_TRY(check_device(plan));
   if (!(scale > 0.0f)) scale = 1.0f / std::sqrt((float)c.head_dim);
   return cuda_status(cb::launch_prompt_attention(q, k, v, cu_seqlens, n_seqs, n_rows, c.hq, c.hkv, c.head_dim, scale,
-                                                 out, plan->decode.sms, plan->err, static_cast<cudaStream_t>(stream)),
+                                                 out, plan->err, static_cast<cudaStream_t>(stream)),
                      "cb_prompt_attention");
 }
 

@@ -14,23 +14,28 @@
 //   on average, and starting a CTA (TMEM, barriers, first loads) costs about 3 us, a quarter of that.
 //   One CTA per SM takes items in turn; the rings of K and V run on across items, and the next
 //   item's first tiles load while the last softmax of the current one runs.
-//   No tile list. The lengths are known on the device only, and the items of one launch should go out
-//   longest first. The order (level, sequence) with level = index of the item in its sequence, from
-//   the largest down, is that order; the producer warp finds the r-th item in it directly: the
-//   sequences with more than `level` items do not change between two distinct item counts, so a run
-//   of levels is skipped at once (two warp reductions over the lengths per distinct count passed).
-//   CTAs take ranks in alternating direction (0 .. n - 1, then 2 n - 1 .. n), which evens out
-//   the sum of a descending cost.
+//   No tile list. The lengths are known on the device only. The grid has a block for every item that
+//   the row count allows; blocks stand for the items in the order longest first, and a running CTA
+//   claims the next block that has not started (cluster launch control) when it has requested its last
+//   K tile. The producer warp finds a block's item by counting sequences. Taken in turn instead, by
+//   index modulo the number of CTAs in alternating direction, the items of 40 prompts of 1 to 1,087 tokens
+//   ended between 290 and 327 us on the various SMs; claimed they end between 298 and 302 us. Items
+//   that share K and V side by side (four or eight levels of a sequence as neighbours in the order) are
+//   slower, not faster: 498 and 513 against 438 us for 16 chunks of 2,048 tokens.
 //   Rows of other sequences. A key tile that reaches past its sequence's end holds the next one's
 //   rows, and one on the diagonal holds keys that some of the rows must not see; their weight is 0, but
 //   0 * V is NaN where V is infinite or NaN. In those tiles (the ones with a key that some row of the
 //   item does not see) the waiter warp looks for such values and sets them to 0 in shared memory; an
 //   item where it found any adds them back to the rows that do see them, in the epilogue. The search
 //   runs while the tile waits for its softmax.
-//   Output. Rows behind a sequence's end belong to others, so the epilogue stores each row from its
-//   thread's registers, 32 bytes (a whole sector) per instruction, instead of a tile by TMA; no
-//   shared memory is needed for it, and the query tiles' buffers are free for the next item.
-//
+//   Output. Each softmax warp stages 64 columns of its 32 rows in shared memory of its own and sends
+//   them off as one box by TMA, which runs on while the warp goes to its next item (stores from
+//   registers or staged ones held the warps for 3,000 - 4,000 cycles per item, an SM's store path taking
+//   about 30 bytes per cycle). A warp whose rows pass the sequence's end, which belong to others, stores
+//   those inside itself. The query tiles' buffers stay free for the next item.
+//   Next scores. After an item's last P_i V the issuer forms the next item's first S_i as soon as its
+//   query tile is there, before the other tile's last product, so that the two softmax warpgroups keep
+//   their half-round distance from item to item.
 // Roles, TMEM columns, register split and bounded waits are those of attention_pp.cu; "round" counts
 // the key tiles of all the CTA's items, and ring stage and parity follow from it. Item descriptions
 // pass from the producer to the other warps through a ring of four. After a wait that gave up
@@ -54,6 +59,7 @@ constexpr int kTiles = 2;     // query tiles per item
 constexpr int kBN = kTileKeys;  // keys per key tile
 constexpr int kStages = 2;    // depth of the K and of the V ring
 constexpr int kItems = 4;     // depth of the item ring
+constexpr uint32_t kOutWarp = 32 * 128;  // output staging of one softmax warp
 constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 128;
 constexpr int kWarpProducerK = 8;
@@ -61,12 +67,11 @@ constexpr int kWarpMma = 9;
 constexpr int kWarpProducerV = 10;
 constexpr int kWarpWaiter = 11;
 constexpr int kBarExit = 1;   // all 384 threads, before the tensor memory is freed
-constexpr int kBarIssue = 2;  // issuer + waiter (64 threads): the first scores of an item
-constexpr int kBarTile0 = 3;  // WG0 + issuer + waiter (192 threads), once per key tile
-constexpr int kBarTile1 = 4;  // WG1 + issuer (160 threads), once per key tile
+constexpr int kBarTile0 = 2;  // WG0 + issuer + waiter (192 threads), once per key tile
+constexpr int kBarTile1 = 3;  // WG1 + issuer (160 threads), once per key tile
 constexpr uint32_t kTmemCols = 512;
-constexpr int kSoftmaxRegs = 224;  // per thread of WG0 / WG1 after setmaxnreg.inc
-constexpr int kOtherRegs = 56;     // per thread of WG2 after setmaxnreg.dec
+constexpr int kSoftmaxRegs = 216;  // per thread of WG0 / WG1 after setmaxnreg.inc
+constexpr int kOtherRegs = 72;     // per thread of WG2 after setmaxnreg.dec
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only when the max grows by > 2^8
 constexpr float kTileSumLimit = 65536.0f;  // a later tile whose P sum exceeds 2^16 moves the reference
 constexpr unsigned long long kItemLimitNs = 5 * kTimeoutNs;  // the producer's own waits end well before
@@ -83,6 +88,10 @@ struct Item {
   int fixed;  // set by the waiter: a V tile held values that are not finite
 };
 
+// First key that is searched for values that are not finite: the first that some row of the item does
+// not see is t0 + 1, and the search goes by 32 keys.
+__device__ __forceinline__ int hidden_from(const Item& x) { return (x.t0 + 1) / 32 * 32; }
+
 struct Bars {
   uint64_t q_full[kTiles];
   uint64_t k_full[kStages];
@@ -90,6 +99,7 @@ struct Bars {
   uint64_t s_full[kTiles][kStages];  // S_i of a round complete (commit); [1][s] also: K stage s free
   uint64_t o_done[kTiles][kStages];  // P_i V of a round complete (commit); [1][s] also: V stage s free
   uint64_t item[kItems];
+  uint64_t claim;  // the answer to a claim of another block has arrived
   uint64_t drain;
 };
 
@@ -101,9 +111,9 @@ struct PromptParams {
   int n_rows;
   int hq;
   int hkv;
-  int group;
-  int tq;    // query tokens per tile = 128 / group
-  int wide;  // out is 32-byte aligned
+  int group;  // query heads per kv head, 1 << lg
+  int lg;
+  int tq;     // query tokens per tile = 128 / group
   float scale_log2;
   int32_t* err;
 };
@@ -116,104 +126,128 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Cluster launch control: ask for a block of this grid that has not been launched yet, to run its work
+// here. The 16-byte answer arrives in shared memory on an mbarrier.
+__device__ __forceinline__ void claim_block(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(bar)
+               : "memory");
+}
+// The claimed block's index, -1 where none was left (no further claim may follow then).
+__device__ __forceinline__ int claimed_block(uint32_t answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return got != 0 ? (int)x : -1;
+}
+
 // First row of each sequence, inside [0, n_rows].
 __device__ __forceinline__ int row_at(const PromptParams& p, int s) {
   const int r = __ldg(p.cu + s);
   return r < 0 ? 0 : min(r, p.n_rows);
 }
 
-// The launch's items by rank (longest first), for a converged warp. Ranks asked for must not fall.
-struct Ranks {
-  int hi, lo;  // levels hi .. lo hold the same `count` sequences each
-  int count;
-  int first;  // rank of the run's first item
+// The launch's items in the order in which blocks stand for them, for a converged warp: by level (the
+// index of an item in its sequence) from the highest down, so the longest first, within a level by
+// sequence and kv head.
+struct Order {
+  int level, count, first;  // current level, the sequences that have it, items of the levels above
+  int s0, before;           // cursor: sequences before s0 hold `before` of them
+  int latest;               // last index asked for
 
+  // Items per kv head of sequence s.
   __device__ __forceinline__ int items_of(const PromptParams& p, int s) const {
     if (s >= p.n_seqs) return 0;
     const int n = row_at(p, s + 1) - row_at(p, s), per = kTiles * p.tq;
-    return n > 0 ? (n + per - 1) / per : 0;
+    return n > 0 ? (n + per - 1) >> (__ffs(per) - 1) : 0;
   }
-  // The run below level `top` (sequences of at least `top` items): its count and lowest level.
-  __device__ __forceinline__ void enter(const PromptParams& p, int top, int lane) {
-    hi = top - 1;
-    int n = 0, next = 0;
-    for (int s = lane; s < p.n_seqs; s += 32) {
-      const int m = items_of(p, s);
-      if (m > hi)
-        ++n;
-      else
-        next = max(next, m);
-    }
+  __device__ __forceinline__ void enter(const PromptParams& p, int lane) {
+    int n = 0;
+    for (int s = lane; s < p.n_seqs; s += 32) n += items_of(p, s) > level ? 1 : 0;
     count = __reduce_add_sync(0xffffffffu, n);
-    lo = __reduce_max_sync(0xffffffffu, next);
+    s0 = before = 0;
   }
   __device__ __forceinline__ void start(const PromptParams& p, int lane) {
     int top = 0;
     for (int s = lane; s < p.n_seqs; s += 32) top = max(top, items_of(p, s));
-    top = __reduce_max_sync(0xffffffffu, top);
-    first = 0;
-    if (top > 0)
-      enter(p, top, lane);
-    else
-      hi = -1, lo = 0, count = 0;
+    level = __reduce_max_sync(0xffffffffu, top) - 1;
+    first = latest = 0;
+    enter(p, lane);
   }
-  // Item of rank r: false past the last one.
-  __device__ __forceinline__ bool find(const PromptParams& p, int r, int lane, int& seq, int& level) {
-    while (hi >= 0 && r >= first + count * (hi - lo + 1)) {
-      first += count * (hi - lo + 1);
-      if (lo == 0) {
-        hi = -1;
-        break;
-      }
-      enter(p, lo, lane);
+  // Item idx: false past the last one. Indices come in rising order but for rare cases, which begin anew.
+  __device__ __forceinline__ bool find(const PromptParams& p, int idx, int lane, int& seq, int& head) {
+    if (idx < latest) start(p, lane);
+    latest = idx;
+    while (level >= 0 && idx - first >= count * p.hkv) {
+      first += count * p.hkv;
+      --level;
+      if (level >= 0) enter(p, lane);
     }
-    if (hi < 0) return false;
-    const uint32_t rel = r - first, up = rel / (uint32_t)count;  // 32 bits: a 64-bit division would be a call
-    level = hi - (int)up;
-    int nth = (int)(rel - up * count);
-    for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {  // `count` sequences have more than hi >= level items
-      const uint32_t has = __ballot_sync(0xffffffffu, items_of(p, s0 + lane) > hi);
+    if (level < 0) return false;
+    const uint32_t rel = idx - first, nth = rel / (uint32_t)p.hkv;  // 32 bits: a 64-bit division would be a call
+    head = (int)(rel - nth * p.hkv);
+    for (; s0 < p.n_seqs; s0 += 32) {
+      uint32_t has = __ballot_sync(0xffffffffu, items_of(p, s0 + lane) > level);
       const int n = __popc(has);
-      if (nth < n) {
-        uint32_t rest = has;
-        for (int i = 0; i < nth; ++i) rest &= rest - 1;
-        seq = s0 + __ffs(rest) - 1;
+      if (before + n > (int)nth) {
+        for (int i = before; i < (int)nth; ++i) has &= has - 1;
+        seq = s0 + __ffs(has) - 1;
         return true;
       }
-      nth -= n;
+      before += n;
     }
     return false;
   }
 };
 
-// A V tile of `bytes` bytes in shared memory: values that are not finite become 0. True (in every
-// lane) if there were any. Called by a converged warp.
-__device__ __forceinline__ bool zero_not_finite(uint32_t tile, uint32_t bytes, int lane) {
+// Rows from .. kBN - 1 (from a multiple of 32) of a V tile in shared memory (boxes of 64 columns, 128
+// bytes per row): values that are not finite become 0. True (in every lane) if there were any. Called
+// by a converged warp; eight loads in flight per lane (one at a time took 4,200 cycles per tile,
+// longer than a round of the tile loop).
+template <int BOXES>
+__device__ __forceinline__ bool zero_not_finite(uint32_t tile, int from, int lane) {
   bool found = false;
-#pragma unroll 4
-  for (uint32_t at = lane * 16; at < bytes; at += 512) {
-    uint32_t w[4];
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(tile + at)
-                 : "memory");
-    // an exponent of all ones, plus one unit of it, carries into the sign bit of its half
-    uint32_t bad = 0;
+#pragma unroll 1
+  for (int b = 0; b < BOXES; ++b) {
+#pragma unroll 1
+    for (int r = from; r < kBN; r += 32) {
+      const uint32_t at = tile + (uint32_t)(b * kBN * 128 + r * 128 + lane * 16);
+      uint32_t bad = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bad |= (w[e] & 0x7f807f80u) + 0x00800080u;
-    if (bad & 0x80008000u) {
-      found = true;
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[4][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
-        if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
+        for (int u = 0; u < 4; ++u)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
+                       : "r"(at + (uint32_t)(h * 4 + u) * 512));
+        // an exponent of all ones, plus one unit of it, carries into the sign bit of its half
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bad |= (w[u][e] & 0x7f807f80u) + 0x00800080u;
       }
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                   "r"(w[3])
-                   : "memory");
+      if (__any_sync(0xffffffffu, bad & 0x80008000u)) {
+        found = true;
+#pragma unroll 1
+        for (int u = 0; u < 32; ++u) {
+          uint32_t x;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at + u / 4 * 512 + u % 4 * 4) : "memory");
+          if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+          if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + u / 4 * 512 + u % 4 * 4), "r"(x) : "memory");
+        }
+      }
     }
   }
-  found = __any_sync(0xffffffffu, found);
   if (found) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it next
   return found;
 }
@@ -221,7 +255,8 @@ __device__ __forceinline__ bool zero_not_finite(uint32_t tile, uint32_t bytes, i
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                            const __grid_constant__ CUtensorMap tm_v, const PromptParams p) {
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                            const PromptParams p) {
   constexpr int kBoxes = D / 64;
   constexpr uint32_t kQBytes = kBM * D * 2;  // one query tile
   constexpr uint32_t kKVBytes = kBN * D * 2;
@@ -231,16 +266,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
   __shared__ Item items[kItems];
+  __shared__ alignas(16) uint4 s_claim;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ int s_first_ok;
   __shared__ int s_round_ok[2];
 
   pdl_launch_dependents();
+  if (threadIdx.x == 32 * kWarpWaiter) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_q) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_v) : "memory");
+  }
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = base;                        // query tile i at sQ + i kQBytes
   const uint32_t sK0 = base + kTiles * kQBytes;    // K stage s at sK0 + s kKVBytes
   const uint32_t sV0 = sK0 + kStages * kKVBytes;   // V stage s at sV0 + s kKVBytes
+  const uint32_t sOut = sV0 + kStages * kKVBytes;  // softmax warp w stages 32 rows of 64 columns at sOut + w kOutWarp
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (warp == kWarpProducerK && lane == 0) {
@@ -254,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     for (int i = 0; i < kItems; ++i) mbar_init(smem_u32(&bars.item[i]), 1);
+    mbar_init(smem_u32(&bars.claim), 1);
     mbar_init(smem_u32(&bars.drain), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -296,25 +338,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a < 0 || b > p.n_rows) record_error(p.err, kErrIndex, s);
           if (b < a) record_error(p.err, kErrOrder, s);
         }
-      Ranks ranks;
-      ranks.start(p, lane);
+      Order order;
+      order.start(p, lane);
       int rounds = 0;  // rounds of the items before
       int nk = 0;      // K tiles requested, by round
       int nq[kTiles] = {0, 0};  // query tiles requested
-      const uint32_t grid = gridDim.x;
-      for (int it = 0;; ++it) {
-        const uint32_t idx = (uint32_t)it * grid + ((it & 1) ? grid - 1 - blockIdx.x : blockIdx.x);
+      // The first item is the block's own; each further one is that of a block which has not started,
+      // claimed when the K tiles of the item before have been requested.
+      int idx = blockIdx.x, claims = 0;
+      for (int it = 0;;) {
         Item x{0, 0, 0, 0, 0, 0};
-        int seq, level;
-        const bool give_up = __any_sync(0xffffffffu, *abort_flag != 0);
-        if (!give_up && ranks.find(p, (int)(idx / (uint32_t)p.hkv), lane, seq, level)) {
+        int seq, head;
+        bool give_up = __any_sync(0xffffffffu, *abort_flag != 0);
+        if (!give_up && idx >= 0 && order.find(p, idx, lane, seq, head)) {
           x.row0 = row_at(p, seq);
           x.len = row_at(p, seq + 1) - x.row0;
-          x.t0 = level * kTiles * p.tq;
-          x.g = (int)(idx % (uint32_t)p.hkv);
+          x.t0 = order.level * kTiles * p.tq;
+          x.g = head;
           x.n_kv = (min(x.t0 + kTiles * p.tq, x.len) - 1) / kBN + 1;
         }
-        if (lane == 0) {
+        const bool end = give_up || idx < 0;  // a block past the last item has none: claim the next
+        if (lane == 0 && (end || x.n_kv > 0)) {
           items[it % kItems] = x;
           mbar_arrive(smem_u32(&bars.item[it % kItems]));
           const int n = x.n_kv;
@@ -349,8 +393,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 1; j < n && ok; ++j) ok = load_k(j);
         }
         __syncwarp();
-        if (x.n_kv == 0) break;
+        if (end) break;
+        if (x.n_kv > 0) ++it;
         rounds += x.n_kv;
+        const uint32_t cb = smem_u32(&bars.claim);
+        if (lane == 0) {
+          mbar_expect_tx(cb, 16);
+          claim_block(smem_u32(&s_claim), cb);
+        }
+        __syncwarp();
+        // not honouring the abort flag: the answer must have landed before the CTA exits
+        const bool there =
+            __all_sync(0xffffffffu, mbar_wait_inl(cb, claims & 1, abort_flag, p.err, 44, false));
+        ++claims;
+        idx = there ? claimed_block(smem_u32(&s_claim)) : -1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before the next answer is written
+        __syncwarp();
       }
       // Before the CTA can exit, every copy issued must have landed (also after an abort).
       if (lane == 0) {
@@ -387,10 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int r = nv < kStages ? 0 : nv - kStages; r < nv; ++r)
           mbar_wait_inl(smem_u32(&bars.v_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 58, false);
     } else if (warp == kWarpWaiter) {
-      // The TMA inputs of an item's first scores (both query tiles and its first K tile), then per key
-      // tile those of its round (V and the next K), published to the issuer through shared memory
-      // before it meets the issuer (and WG0) on a named barrier. Every round is joined, also after a
-      // failure.
+      // Per round, its V tile and the item's next K tile, published to the issuer through shared memory
+      // before the waiter meets the issuer (and WG0) on a named barrier. Every round is joined, also
+      // after a failure.
       auto spin_all = [&](uint32_t bar, uint32_t parity, int site) -> bool {
         return __all_sync(0xffffffffu, mbar_spin_inl(bar, parity, abort_flag, p.err, site));
       };
@@ -399,21 +456,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0;; ++it) {
         const Item x = item_at(it);
         if (x.n_kv == 0) break;
-        ok = ok && spin_all(smem_u32(&bars.q_full[0]), it & 1, 44) && spin_all(smem_u32(&bars.q_full[1]), it & 1, 45) &&
-             spin_all(smem_u32(&bars.k_full[rounds % kStages]), (rounds / kStages) & 1, 46);
-        if (lane == 0) s_first_ok = ok ? 1 : 0;
-        __syncwarp();  // bar.sync is warp-aligned: reach it converged
-        named_sync(kBarIssue, 64);
         for (int j = 0; j < x.n_kv; ++j) {
           const int r = rounds + j, st = r % kStages;
           ok = ok && spin_all(smem_u32(&bars.v_full[st]), (r / kStages) & 1, 47);
           // a tile with a key that the item's first row does not see
-          if (ok && (j + 1) * kBN > x.t0 + 1 && zero_not_finite(sV0 + st * kKVBytes, kKVBytes, lane) && lane == 0)
+          if (ok && (j + 1) * kBN > x.t0 + 1 &&
+              zero_not_finite<kBoxes>(sV0 + st * kKVBytes, max(hidden_from(x) - j * kBN, 0), lane) && lane == 0)
             items[it % kItems].fixed = 1;
           ok = ok && (j + 1 >= x.n_kv ||
                       spin_all(smem_u32(&bars.k_full[(r + 1) % kStages]), ((r + 1) / kStages) & 1, 48));
           if (lane == 0) s_round_ok[r & 1] = ok ? 1 : 0;
-          __syncwarp();
+          __syncwarp();  // bar.sync is warp-aligned: reach it converged
           named_sync(kBarTile0, 192);
         }
         rounds += x.n_kv;
@@ -446,48 +499,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                  (ks > 0 || !first) ? 1u : 0u);
         tc_commit(smem_u32(&bars.o_done[i][st]));
       };
+      // This warp's own wait for query tile i and the first K tile of item it (round r).
+      auto inputs = [&](int i, int it, int r) -> bool {
+        const bool there = mbar_spin_inl(smem_u32(&bars.q_full[i]), it & 1, abort_flag, p.err, 45 + i) &&
+                           mbar_spin_inl(smem_u32(&bars.k_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 47);
+        return __all_sync(0xffffffffu, there);
+      };
       int rounds = 0;
+      Item x = item_at(0);
       bool ok = true;
-      for (int it = 0;; ++it) {
-        const Item x = item_at(it);
-        if (x.n_kv == 0) break;
-        __syncwarp();
-        named_sync(kBarIssue, 64);
-        ok = ok && s_first_ok != 0;
-        if (ok) {
-          tc_fence_after();
-          if (elect_one()) {
-            issue_s(0, rounds);
-            issue_s(1, rounds);
+      if (x.n_kv > 0) {
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          ok = ok && inputs(i, 0, 0);
+          if (ok) {
+            tc_fence_after();
+            if (elect_one()) issue_s(i, 0);
+            __syncwarp();
           }
-          __syncwarp();
         }
+      }
+      for (int it = 0; x.n_kv > 0; ++it) {
+        Item next{0, 0, 0, 0, 0, 0};
         for (int j = 0; j < x.n_kv; ++j) {
           const int r = rounds + j;
-          __syncwarp();
-          named_sync(kBarTile0, 192);  // P_0 in TMEM; this round's V and the next K loaded (waiter)
-          ok = ok && s_round_ok[r & 1] != 0 && !*abort_flag;
-          if (ok) {
-            tc_fence_after();
-            if (elect_one()) {
-              issue_pv(0, r, j == 0);
-              if (j + 1 < x.n_kv) issue_s(0, r + 1);
-            }
+          const bool last = j + 1 == x.n_kv;
+          // Tile i's P is in TMEM; this round's V and the item's next K are loaded (the waiter meets
+          // tile 0's barrier). After the item's last P V come the next item's first scores, as soon as
+          // its query tile is there: its softmax then finds them when it is through with its output.
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) {
             __syncwarp();
-          }
-          __syncwarp();
-          named_sync(kBarTile1, 160);  // P_1 in TMEM
-          ok = ok && !*abort_flag;
-          if (ok) {
-            tc_fence_after();
-            if (elect_one()) {
-              issue_pv(1, r, j == 0);
-              if (j + 1 < x.n_kv) issue_s(1, r + 1);
+            if (i == 0) {
+              named_sync(kBarTile0, 192);
+              ok = ok && s_round_ok[r & 1] != 0;
+            } else {
+              named_sync(kBarTile1, 160);
             }
-            __syncwarp();
+            ok = ok && !*abort_flag;
+            if (ok) {
+              tc_fence_after();
+              if (elect_one()) {
+                issue_pv(i, r, j == 0);
+                if (!last) issue_s(i, r + 1);
+              }
+              __syncwarp();
+            }
+            if (last) {
+              if (i == 0) next = item_at(it + 1);
+              if (next.n_kv > 0) ok = ok && inputs(i, it + 1, r + 1);
+              if (ok && next.n_kv > 0) {
+                tc_fence_after();
+                if (elect_one()) issue_s(i, r + 1);
+                __syncwarp();
+              }
+            }
           }
         }
         rounds += x.n_kv;
+        x = next;
       }
       // All tensor-core work issued by this CTA completes before TMEM is freed.
       if (elect_one()) tc_commit(smem_u32(&bars.drain));
@@ -513,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x.n_kv == 0) break;
       // Position of this thread's row in the sequence; rows past its end repeat the last one and are
       // never stored.
-      const int tok = x.t0 + ti * p.tq + row / p.group;
+      const int tok = x.t0 + ti * p.tq + (row >> p.lg);
       const int my_pos = min(tok, x.len - 1);
       float m_ref = -INFINITY, l = 0.0f;  // reference max (log2 units) that O_ti and l are scaled to
       auto wait_o = [&](int r, int site) -> bool {
@@ -549,9 +619,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kBN; ++c)
             if (c > lim) sv[c] = 0xff800000u;  // -inf
         }
-        // As in attention_pp.cu: a row's first tile sets the reference to its max; later tiles run
-        // against the reference and take their max only where their P sum shows that it jumped.
+        // As in attention_pp.cu, tiles run against a reference and take their max only where their P
+        // sum shows that the reference is too low. The first tile's reference is the max of its first
+        // 32 columns (every row sees column 0): the rest is within 2^16 of it but for rare rows, which
+        // the check finds.
         const uint32_t taddr_p = lane_base + col_s(ti);
+        if (j == 0) {
+          float tm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              tm[u] = max3(tm[u], __uint_as_float(sv[c + 2 * u]), __uint_as_float(sv[c + 2 * u + 1]));
+          m_ref = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3])) * p.scale_log2;
+        }
         bool move_ref = !__all_sync(0xffffffffu, m_ref != -INFINITY);
         float sum = 0.0f;
         if (!move_ref) {
@@ -617,17 +698,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float inv = 1.0f / l;
         const bool fixed = items[it % kItems].fixed != 0;
-        const bool store = tok < x.len;
-        uint8_t* dst = p.out + ((int64_t)(x.row0 + my_pos) * p.hq + x.g * p.group + row % p.group) * (D * 2);
+        const uint32_t stage = sOut + (uint32_t)warp * kOutWarp;
+        const int tokens = x.len - x.t0 - ti * p.tq;  // of this tile that are in the sequence (may be <= 0 or many)
+        const bool whole = tokens >= ((warp % 4) * 32 + 32) >> p.lg;  // every row of this warp is
+        const int token_bytes = p.hq * D * 2;
+        uint8_t* dst = p.out + ((int64_t)(x.row0 + x.t0 + ti * p.tq) * p.hq + x.g * p.group) * (D * 2) + (lane & 7) * 16;
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
-          tmem_ld_x32(lane_base + col_o(ti, D) + c0, o);
+        for (int c0 = 0; c0 < D; c0 += 64) {
+          uint32_t o[64];
+          uint32_t(&o0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&o[0]);
+          uint32_t(&o1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&o[32]);
+          tmem_ld_x32_async(lane_base + col_o(ti, D) + c0, o0);
+          tmem_ld_x32_async(lane_base + col_o(ti, D) + c0 + 32, o1);
+          tmem_wait_ld(o0);
+          tmem_wait_ld(o1);
           if (fixed) {  // the values that were set to 0, of the keys that this row does see
-            for (int key = (x.t0 + 1) / kBN * kBN; key <= my_pos; ++key) {
+            for (int key = hidden_from(x); key <= my_pos; ++key) {
               const uint8_t* src = p.v + (((int64_t)(x.row0 + key) * p.hkv + x.g) * D + c0) * 2;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 8; ++q) {
                 float f[8];
                 unpack8(*reinterpret_cast<const uint4*>(src + q * 16), f);
 #pragma unroll
@@ -635,32 +724,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (!isfinite(f[e])) o[q * 8 + e] = __float_as_uint(__uint_as_float(o[q * 8 + e]) + f[e]);
               }
             }
+            __syncwarp();  // the next load of TMEM is warp-aligned
           }
-          uint4 pk[4];
+          // the rows staged before have been read
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 8; ++q) {
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[q * 8 + e]) * inv;
-            pk[q] = pack8(f);
+            const uint4 pk = pack8(f);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + (uint32_t)((q ^ (lane & 7)) * 16)),
+                         "r"(pk.x), "r"(pk.y), "r"(pk.z), "r"(pk.w)
+                         : "memory");
           }
-          if (store) {
-            if (p.wide) {
-#pragma unroll
-              for (int q = 0; q < 4; q += 2)
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c0 * 2 + q * 16),
-                             "r"(pk[q].x), "r"(pk[q].y), "r"(pk[q].z), "r"(pk[q].w), "r"(pk[q + 1].x),
-                             "r"(pk[q + 1].y), "r"(pk[q + 1].z), "r"(pk[q + 1].w)
-                             : "memory");
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + c0 * 2 + q * 16) = pk[q];
+          if (whole) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(&tm_o),
+                           "r"(c0), "r"(0), "r"(x.g), "r"(x.row0 + x.t0 + ti * p.tq + (((warp % 4) * 32) >> p.lg)), "r"(stage)
+                           : "memory");
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
+            __syncwarp();
+            continue;
           }
-          __syncwarp();  // the next load of TMEM is warp-aligned
+          __syncwarp();
+          // 8 lanes per row: 128 bytes of four rows per instruction, all loads first
+          uint4 pk[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rl = 4 * i + lane / 8;  // row in the warp
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(pk[i].x), "=r"(pk[i].y), "=r"(pk[i].z), "=r"(pk[i].w)
+                         : "r"(stage + rl * 128 + (uint32_t)(((lane & 7) ^ (rl & 7)) * 16)));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rt = (warp % 4) * 32 + 4 * i + lane / 8;  // row in the tile
+            if ((rt >> p.lg) < tokens)
+              *reinterpret_cast<uint4*>(dst + c0 * 2 + (rt >> p.lg) * token_bytes + (rt & (p.group - 1)) * (D * 2)) = pk[i];
+          }
         }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // before shared memory goes
     __syncwarp();
     tc_fence_before();
     named_sync(kBarExit, kThreads);
@@ -673,8 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,
-                            int32_t n_rows, int32_t hq, int32_t hkv, float scale, void* out, int32_t sms,
-                            int32_t* err, cudaStream_t s) {
+                            int32_t n_rows, int32_t hq, int32_t hkv, float scale, void* out, int32_t* err,
+                            cudaStream_t s) {
   const int group = hq / hkv;
   const int tq = kBM / group;
   // The register split: the block is launched with numRegs per thread and setmaxnreg moves them
@@ -689,15 +799,16 @@ cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const i
   }
   if (regs * kThreads < kTiles * kSoftmaxThreads * kSoftmaxRegs + kSoftmaxThreads * kOtherRegs)
     return cudaErrorNotSupported;
-  CUtensorMap tq_map, tk_map, tv_map;
+  CUtensorMap tq_map, tk_map, tv_map, to_map;
   const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)group, (cuuint64_t)hkv, (cuuint64_t)n_rows};
   const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)group * D * 2, (cuuint64_t)hq * D * 2};
   const cuuint32_t qb[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)tq};
+  const cuuint32_t ob[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)(32 / group)};  // the rows of a softmax warp
   const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)hkv, (cuuint64_t)n_rows};
   const cuuint64_t ks[2] = {(cuuint64_t)D * 2, (cuuint64_t)hkv * D * 2};
   const cuuint32_t kbx[3] = {64, 1, (cuuint32_t)kBN};
   if (!encode_map(&tq_map, q, 4, qd, qs, qb) || !encode_map(&tk_map, k, 3, kd, ks, kbx) ||
-      !encode_map(&tv_map, v, 3, kd, ks, kbx))
+      !encode_map(&tv_map, v, 3, kd, ks, kbx) || !encode_map(&to_map, out, 4, qd, qs, ob))
     return cudaErrorInvalidValue;
   PromptParams p;
   p.v = static_cast<const uint8_t*>(v);
@@ -708,17 +819,17 @@ cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const i
   p.hq = hq;
   p.hkv = hkv;
   p.group = group;
+  p.lg = 31 - __builtin_clz(group);
   p.tq = tq;
-  p.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = err;
-  const size_t smem = 1024 + (size_t)(kTiles * kBM + 2 * kStages * kBN) * D * 2;
+  const size_t smem = 1024 + (size_t)(kTiles * kBM + 2 * kStages * kBN) * D * 2 + 2 * kSoftmaxThreads / 32 * kOutWarp;
   static std::atomic<uint64_t> configured{0};
   const cudaError_t e = set_smem_limit_once(prompt_attention_kernel<D>, (int)smem, configured);
   if (e != cudaSuccess) return e;
   const int64_t most = prompt_items(n_seqs, n_rows, hq, hkv);
-  return launch_pdl(prompt_attention_kernel<D>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), smem, s,
-                    tq_map, tk_map, tv_map, p);
+  return launch_pdl(prompt_attention_kernel<D>, dim3((unsigned)most), dim3(kThreads), smem, s,
+                    tq_map, tk_map, tv_map, to_map, p);
 }
 
 }  // namespace
@@ -730,11 +841,11 @@ int64_t prompt_items(int32_t n_seqs, int32_t n_rows, int32_t hq, int32_t hkv) {
 
 cudaError_t launch_prompt_attention(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,
                                     int32_t n_rows, int32_t hq, int32_t hkv, int32_t head_dim, float scale, void* out,
-                                    int32_t sms, int32_t* err, cudaStream_t s) {
+                                    int32_t* err, cudaStream_t s) {
   if (n_seqs <= 0 || n_rows <= 0) return cudaSuccess;
   if (head_dim == 128)
-    return launch_prompt_t<128>(q, k, v, cu, n_seqs, n_rows, hq, hkv, scale, out, sms, err, s);
-  if (head_dim == 64) return launch_prompt_t<64>(q, k, v, cu, n_seqs, n_rows, hq, hkv, scale, out, sms, err, s);
+    return launch_prompt_t<128>(q, k, v, cu, n_seqs, n_rows, hq, hkv, scale, out, err, s);
+  if (head_dim == 64) return launch_prompt_t<64>(q, k, v, cu, n_seqs, n_rows, hq, hkv, scale, out, err, s);
   return cudaErrorInvalidValue;
 }
 

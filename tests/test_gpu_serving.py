@@ -646,3 +646,39 @@ def test_calls_on_another_stream(cb):
     plan.check()
     _check_decode(plan, q, out, ks, vs, "another stream")
     plan.close()
+
+
+def test_binding_refuses_wrong_tensors(cb):
+    plan = _plan(cb, 8, 2, 128)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = torch.zeros((3, 2, 18 * 128), dtype=torch.uint8, device="cuda")
+    k, t, n = bf(4, 2, 128), i32(2, 3), i32(2)
+    for args, said in (((bf(4, 3, 128), k, i32(4), cache), "k must have shape"),
+                       ((k, bf(4, 128, 2).transpose(1, 2), i32(4), cache), "v must be contiguous"),
+                       ((k, k, i32(5), cache), "k must have shape"), ((k, k.float(), i32(4), cache), "v must be torch.bfloat16"),
+                       ((k, k, i32(4).long(), cache), "slots must be torch.int32"),
+                       ((k, k.cpu(), i32(4), cache), "v must be on a CUDA device")):
+        with pytest.raises(ValueError, match=said):
+            cb.cb_kv4_store(plan, *args, 16)
+    for q, table, out, said in ((bf(3, 8, 128), t, bf(2, 8, 128), "q must have shape"), (bf(2, 8, 128), i32(3, 3), bf(2, 8, 128), "table"),
+                                (bf(2, 8, 128), t, bf(2, 8, 64), "out must have shape")):
+        with pytest.raises(ValueError, match=said):
+            cb.cb_kv4_decode_attention(plan, q, cache, 16, table, n, out)
+    q = bf(5, 8, 128)
+    for kk, vv, cu, out, said in ((bf(4, 2, 128), bf(5, 2, 128), n, q.clone(), "k must have shape"),
+                                  (bf(5, 2, 128), bf(5, 2, 64), n, q.clone(), "v must have shape"),
+                                  (bf(5, 2, 128), bf(5, 2, 128), n.float(), q.clone(), "cu_seqlens must be torch.int32"),
+                                  (bf(5, 2, 128), bf(5, 2, 128), n, bf(5, 8, 256)[:, :, ::2], "out must be contiguous")):
+        with pytest.raises(ValueError, match=said):
+            cb.cb_prompt_attention(plan, q, kk, vv, cu, out)
+    with pytest.raises(cb.CacheBlendError, match="out must not be"):
+        cb.cb_prompt_attention(plan, q, bf(5, 2, 128), bf(5, 2, 128), n, q)
+    with pytest.raises(ValueError, match="new_lens must have shape"):
+        cb.cb_page_tables(plan, i32(3), n, 16, i32(9), i32(3, 4), i32(4), i32(3), i32(5), i32(5), i32(1))
+    with pytest.raises(ValueError, match="cu_seqlens must have shape"):
+        cb.cb_page_tables(plan, i32(3), i32(3), 16, i32(9), i32(3, 4), i32(3), i32(3), i32(5), i32(5), i32(1))
+    with pytest.raises(cb.CacheBlendError, match="free_to is NULL"):
+        cb.cb_page_tables(plan, i32(3), i32(3), 16, i32(9), i32(3, 4), i32(4), i32(3), i32(5), i32(5), None)
+    plan.check()
+    plan.close()

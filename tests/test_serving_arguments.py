@@ -133,23 +133,23 @@ def test_binding_checks_shapes_before_the_library(lib, plan):
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
     cache = torch.zeros((3, 2, 18 * 128), dtype=torch.uint8)
-    with pytest.raises(ValueError, match="k must have shape"):
-        cb.cb_kv4_store(p, bf(4, 3, 128), bf(4, 2, 128), i32(4), cache, 16)
-    with pytest.raises(ValueError, match="slots must have shape"):
-        cb.cb_kv4_store(p, bf(4, 2, 128), bf(4, 2, 128), i32(5), cache, 16)
+    with pytest.raises(ValueError, match="cache must have shape"):
+        cb.cb_kv4_store(p, bf(4, 2, 128), bf(4, 2, 128), i32(4), cache, 32)
+    with pytest.raises(ValueError, match="cache must have 3 dim"):
+        cb.cb_kv4_load(p, cache[0], 16, i32(4), bf(4, 2, 128), bf(4, 2, 128))
     with pytest.raises(ValueError, match="on a CUDA device"):
         cb.cb_kv4_load(p, cache, 16, i32(4), bf(4, 2, 128), bf(4, 2, 128))
+    with pytest.raises(ValueError, match="table must have 2 dim"):
+        cb.cb_kv4_decode_attention(p, bf(2, 8, 128), cache, 16, i32(4), i32(2), bf(2, 8, 128))
     with pytest.raises(ValueError, match="q must have shape"):
-        cb.cb_kv4_decode_attention(p, bf(2, 8, 64), cache, 16, i32(2, 4), i32(2), bf(2, 8, 128))
-    with pytest.raises(ValueError, match="table must have shape"):
-        cb.cb_kv4_decode_attention(p, bf(2, 8, 128), cache, 16, i32(3, 4), i32(2), bf(2, 8, 128))
-    with pytest.raises(ValueError, match="cache must have shape"):
-        cb.cb_kv4_decode_attention(p, bf(2, 8, 128), cache, 32, i32(2, 4), i32(2), bf(2, 8, 128))
+        cb.cb_prompt_attention(p, bf(5, 8, 64), bf(5, 2, 128), bf(5, 2, 128), i32(2), bf(5, 8, 128))
+    with pytest.raises(ValueError, match="q must have 3 dim"):
+        cb.cb_prompt_attention(p, bf(5, 1024), bf(5, 2, 128), bf(5, 2, 128), i32(2), bf(5, 8, 128))
     with pytest.raises(ValueError, match="first offset"):
         cb.cb_prompt_attention(p, bf(5, 8, 128), bf(5, 2, 128), bf(5, 2, 128), i32(0), bf(5, 8, 128))
-    with pytest.raises(ValueError, match="v must have shape"):
-        cb.cb_prompt_attention(p, bf(5, 8, 128), bf(5, 2, 128), bf(4, 2, 128), i32(2), bf(5, 8, 128))
-    with pytest.raises(ValueError, match="new_lens must have shape"):
+    with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+        cb.cb_prompt_attention(p, None, bf(5, 2, 128), bf(5, 2, 128), i32(2), bf(5, 8, 128))
+    with pytest.raises(ValueError, match="on a CUDA device"):
         cb.cb_page_tables(p, i32(3), i32(2), 16, i32(9), i32(3, 4), i32(4), i32(3), i32(5), i32(5), i32(1))
-    with pytest.raises(ValueError, match="cu_seqlens must have shape"):
-        cb.cb_page_tables(p, i32(3), i32(3), 16, i32(9), i32(3, 4), i32(3), i32(3), i32(5), i32(5), i32(1))
+    with pytest.raises(ValueError, match="free_pages must have 1 dim"):
+        cb.cb_page_tables(p, i32(3), i32(3), 16, i32(9, 1), i32(3, 4), i32(4), i32(3), i32(5), i32(5), i32(1))
