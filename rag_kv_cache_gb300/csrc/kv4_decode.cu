@@ -12,7 +12,8 @@
 //   (word >> 4 i & 0x000f000f) | 0x43004300 = two bf16 of value 128 + nibble = 136 + code (exact),
 // so that no subtraction or conversion is needed. The offset 136 leaves through the accumulators:
 //   scores   S^T = K Q^T (M = 16 keys, N = 8 heads, inner = dims), one accumulator per group of 32
-//            dims that starts at -136 * sum of q over the group, then times the key's scale;
+//            dims, times the key's scale, added to one more product of the keys' scales with
+//            -136 * (sum of q over the group), the latter as three bf16 terms;
 //   output   O^T += V^T P^T (M = 16 dims, N = 8 heads, inner = 16 keys) with P_g = bf16(p * scale of
 //            the key's group g), and one more product per group with ones in place of V, which sums
 //            the same rounded P_g: O - 136 * that sum is the result, so the offset adds no rounding.
@@ -31,15 +32,26 @@
 #include "kernels.h"
 #include "attn_common.cuh"
 #include "kv4_layout.cuh"
+#include "tc_common.cuh"
 
 namespace cb {
 namespace {
 
-constexpr float kRescale = 8.0f;          // log2 units: a max that grows by less leaves the reference alone
+constexpr float kHigh = 256.0f;           // a weight above it moves the reference
+constexpr float kLow = -3e38f;            // reference of a head that has seen nothing
+constexpr int kMaxCtas = 160;             // of a launch (one wave: one per SM)
 constexpr float kOffset = 136.0f;         // value of a widened nibble of code 0
 constexpr uint32_t kNibbles = 0x000f000fu;
 constexpr uint32_t kBias = 0x43004300u;   // two bf16 of 128: the last place is 1
 constexpr uint32_t kOnes = 0x3f803f80u;   // two bf16 of 1
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+struct Masks {
+  uint32_t nibbles, bias, ones;
+};
 
 struct Kv4DecodeParams {
   const uint8_t* q;
@@ -54,6 +66,7 @@ struct Kv4DecodeParams {
   int32_t hkv;
   int32_t G;      // query heads per kv head
   float scale_log2;
+  Masks masks;
   float* part_o;     // [CTA][2][16 heads][D]
   float2* part_ml;   // [CTA][2][16 heads]
   int32_t* tickets;  // [CTA]
@@ -68,44 +81,37 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same from zero.
+__device__ __forceinline__ void mma_bf16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-__device__ __forceinline__ uint32_t widen(uint32_t word, int i) { return (word >> (4 * i) & kNibbles) | kBias; }
+// Pairs `from` and from + 1 of the four pairs of nibbles of a word, widened:
+// (word >> 4 i & 0x000f000f) | 0x43004300.
+__device__ __forceinline__ void widen(uint32_t word, int from, const Masks& k, uint32_t (&x)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) x[i] = (word >> (4 * (from + i)) & k.nibbles) | k.bias;
+}
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// One lane's share of a record: K words of tokens r and r + 8, V words of both halves, and the
-// scales of tokens r and r + 8 ([K NG, V NG] bf16 each).
 template <int NG>
-struct Words {
-  uint32_t k[2][NG], v[2][NG], sc[2][NG];
-};
-
-template <int NG>
-__device__ __forceinline__ void load_vec(uint32_t (&w)[NG], const uint8_t* p) {
-  if constexpr (NG == 4) {
-    const uint4 x = ld_stream(p);
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-  } else {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = x.x, w[1] = x.y;
-  }
-}
-
-template <int D>
-__device__ __forceinline__ void load_record(Words<Kv4<D>::kGroups>& w, const uint8_t* rec, int lane) {
-  constexpr int NG = Kv4<D>::kGroups;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    load_vec<NG>(w.k[h], rec + h * Kv4<D>::kPlane + lane * (4 * NG));
-    load_vec<NG>(w.v[h], rec + Kv4<D>::kV + h * Kv4<D>::kPlane + lane * (4 * NG));
-    load_vec<NG>(w.sc[h], rec + Kv4<D>::kScales + (lane / 4 + 8 * h) * (4 * NG));
-  }
+__device__ __forceinline__ void load_vec(uint32_t (&w)[NG], uint32_t at) {
+  if constexpr (NG == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+  else
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
 }
 
 // Running state of a warp over one (request, kv head): heads 8 t + 2 c and + 1 per lane (c = lane % 4).
@@ -129,18 +135,19 @@ __device__ __forceinline__ void reset(State<D, NT>& st) {
     for (int g = 0; g < State<D, NT>::NG; ++g)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.ones[t][g][e] = 0.0f;
-    st.m[t][0] = st.m[t][1] = -INFINITY;
+    st.m[t][0] = st.m[t][1] = kLow;
     st.l[t][0] = st.l[t][1] = 0.0f;
   }
 }
 
-// Query operand of one (request, kv head): pairs of dims 32 g + 8 c + .. of head 8 t + r, and
-// -136 * (sum of the group's dims) of heads 8 t + 2 c and + 1.
+// Query operand of one (request, kv head): pairs of dims 32 g + 8 c + .. of head 8 t + r; and the operand
+// of the correction, whose inner dimension is (term, group): -136 * (sum of the group's dims) in three
+// bf16 terms, which hold all 24 bits of it.
 template <int D, int NT>
 struct Query {
   static constexpr int NG = Kv4<D>::kGroups;
   uint32_t b[NT][NG][4];
-  float c0[NT][NG][2];
+  uint32_t fix[NT][2];
 };
 
 template <int D, int NT>
@@ -148,7 +155,8 @@ __device__ __forceinline__ void load_query(Query<D, NT>& qf, const uint8_t* q, i
   constexpr int NG = Kv4<D>::kGroups;
   const int r = lane / 4, c = lane % 4;
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < NT; ++t) {
+    float off[4] = {0.f, 0.f, 0.f, 0.f};  // of head 8 t + r
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       uint4 x = make_uint4(0, 0, 0, 0);
@@ -158,84 +166,117 @@ __device__ __forceinline__ void load_query(Query<D, NT>& qf, const uint8_t* q, i
       unpack8(x, f);
       float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);  // head 8 t + r
-      qf.c0[t][g][0] = -kOffset * __shfl_sync(0xffffffffu, sum, 8 * c);
-      qf.c0[t][g][1] = -kOffset * __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      off[g] = -kOffset * sum;
     }
+    // inner index 2 c + {0, 1} (and + 8): term c / 2 (and 2, for c < 2), groups 2 (c % 2) + {0, 1}
+    const float x0 = c % 2 ? off[2] : off[0], x1 = c % 2 ? off[3] : off[1];
+    uint32_t term[3];
+    float y0 = x0, y1 = x1;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      term[i] = pack2(y0, y1);
+      y0 -= bf16_lo(term[i]);
+      y1 -= bf16_hi(term[i]);
+    }
+    qf.fix[t][0] = c < 2 ? term[0] : term[1];
+    qf.fix[t][1] = c < 2 ? term[2] : 0u;
+  }
 }
 
 // One record of up to 16 keys, the first `valid` of them in the request.
-template <int D, int NT>
-__device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, Words<Kv4<D>::kGroups>& w, int valid,
-                                     float scale_log2, int lane) {
+template <int D, int NT, bool WHOLE>
+__device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, uint32_t rec, int valid, float scale_log2,
+                                     const Masks& mk, int lane) {
   constexpr int NG = Kv4<D>::kGroups;
   const int r = lane / 4;
-  if (valid < kKv4Block) {  // scales of slots behind the request's end may be anything: 0 keeps them finite
+  uint32_t sc[2][NG];  // scales of tokens r and r + 8: [K NG, V NG] bf16
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (r + 8 * h >= valid)
+  for (int h = 0; h < 2; ++h) {
+    load_vec<NG>(sc[h], rec + Kv4<D>::kScales + (r + 8 * h) * (4 * NG));
+    // slots behind the request's end may hold any scales: 0 keeps what they give finite
+    if (!WHOLE && r + 8 * h >= valid)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) w.sc[h][g] = 0;
+      for (int g = 0; g < NG; ++g) sc[h][g] = 0;
   }
-  // K scales of group g: element g of [K NG, V NG] bf16
-  auto ks = [&](int h, int g) { return g % 2 ? bf16_hi(w.sc[h][g / 2]) : bf16_lo(w.sc[h][g / 2]); };
+  auto ks = [&](int h, int g) { return g % 2 ? bf16_hi(sc[h][g / 2]) : bf16_lo(sc[h][g / 2]); };
   auto vs = [&](int h, int g) {
-    return g % 2 ? bf16_hi(w.sc[h][NG / 2 + g / 2]) : bf16_lo(w.sc[h][NG / 2 + g / 2]);
+    return g % 2 ? bf16_hi(sc[h][NG / 2 + g / 2]) : bf16_lo(sc[h][NG / 2 + g / 2]);
   };
-  float s[NT][4];
+  uint32_t w[2][NG];  // K words of tokens r and r + 8
 #pragma unroll
-  for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
+  for (int h = 0; h < 2; ++h) load_vec<NG>(w[h], rec + h * Kv4<D>::kPlane + lane * (4 * NG));
+  float s[NT][4];
+  {
+    // the offset's part of the scores first: -136 sum_g scale_g(key) (sum of q over g)
+    const bool odd = lane & 1;
+    const uint32_t k0 = NG == 2 ? (odd ? 0u : sc[0][0]) : (odd ? sc[0][NG / 2 - 1] : sc[0][0]);
+    const uint32_t k1 = NG == 2 ? (odd ? 0u : sc[1][0]) : (odd ? sc[1][NG / 2 - 1] : sc[1][0]);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) mma_bf16_new(s[t], k0, k1, k0, k1, qf.fix[t][0], qf.fix[t][1]);
+  }
+  // Both products of a group depend on one another: all groups' first ones, then all second ones, so
+  // that a product's latency passes under the other groups' widening.
+  float acc[NT][NG][4];
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      uint32_t x[2], y[2];  // tokens r, r + 8
+      widen(w[0][g], 2 * half, mk, x);
+      widen(w[1][g], 2 * half, mk, y);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (half == 0)
+          mma_bf16_new(acc[t][g], x[0], y[0], x[1], y[1], qf.b[t][g][0], qf.b[t][g][1]);
+        else
+          mma_bf16(acc[t][g], x[0], y[0], x[1], y[1], qf.b[t][g][2], qf.b[t][g][3]);
+      }
+    }
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    uint32_t a[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[2 * i] = widen(w.k[0][g], i);
-      a[2 * i + 1] = widen(w.k[1][g], i);
-    }
     const float s0 = ks(0, g), s1 = ks(1, g);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float acc[4] = {qf.c0[t][g][0], qf.c0[t][g][1], qf.c0[t][g][0], qf.c0[t][g][1]};
-      mma_bf16(acc, a[0], a[1], a[2], a[3], qf.b[t][g][0], qf.b[t][g][1]);
-      mma_bf16(acc, a[4], a[5], a[6], a[7], qf.b[t][g][2], qf.b[t][g][3]);
-      s[t][0] = fmaf(s0, acc[0], s[t][0]);
-      s[t][1] = fmaf(s0, acc[1], s[t][1]);
-      s[t][2] = fmaf(s1, acc[2], s[t][2]);
-      s[t][3] = fmaf(s1, acc[3], s[t][3]);
+      s[t][0] = fmaf(s0, acc[t][g][0], s[t][0]);
+      s[t][1] = fmaf(s0, acc[t][g][1], s[t][1]);
+      s[t][2] = fmaf(s1, acc[t][g][2], s[t][2]);
+      s[t][3] = fmaf(s1, acc[t][g][3], s[t][3]);
     }
   }
-  // scores in log2 units; -inf behind the request's end
+  // -inf behind the request's end
+  if (!WHOLE) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s[t][e] *= scale_log2;
-      if (valid < kKv4Block && r + 8 * (e / 2) >= valid) s[t][e] = -INFINITY;
-    }
-  // the record's max per head, and a new reference where it passes the old one by more than 2^8
-  float top[NT][2];
-  bool up = false;
+      for (int e = 0; e < 4; ++e)
+        if (r + 8 * (e / 2) >= valid) s[t][e] = -INFINITY;
+  }
+  // P = 2^(s scale - m) against the reference. The references are raised only where a weight passes 2^8
+  // (or, at a request's first record, where there is none): the max costs 8 comparisons and 6
+  // shuffles per record.
+  float pr[NT][4];
+  float most = 0.0f;
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float x = fmaxf(s[t][e], s[t][e + 2]);
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-      top[t][e] = x;
-      up |= x > st.m[t][e] + kRescale;
-    }
-  if (__any_sync(0xffffffffu, up)) {
+    for (int e = 0; e < 4; ++e) pr[t][e] = ex2(fmaf(s[t][e], scale_log2, -st.m[t][e % 2]));
+    most = fmaxf(max3(most, pr[t][0], pr[t][1]), fmaxf(pr[t][2], pr[t][3]));
+  }
+  const bool high = most > kHigh;
+  if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float alpha[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const bool move = top[t][e] > st.m[t][e] + kRescale;
-        alpha[e] = move ? ex2(st.m[t][e] - top[t][e]) : 1.0f;  // 0 where the head had nothing
-        if (move) st.m[t][e] = top[t][e];
+        float top = fmaxf(s[t][e], s[t][e + 2]);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) * scale_log2;
+        const bool move = top > st.m[t][e];
+        alpha[e] = move ? ex2(st.m[t][e] - top) : 1.0f;  // 0 where the head had nothing
+        if (move) st.m[t][e] = top;
         st.l[t][e] *= alpha[e];
       }
 #pragma unroll
@@ -246,42 +287,66 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, W
       for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.ones[t][g][e] *= alpha[e % 2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        pr[t][e] = ex2(fmaf(s[t][e], scale_log2, -st.m[t][e % 2]));
+      }
     }
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float ref = st.m[t][e % 2];
-      s[t][e] = ex2(s[t][e] - (ref == -INFINITY ? 0.0f : ref));
-    }
-    st.l[t][0] += s[t][0] + s[t][2];
-    st.l[t][1] += s[t][1] + s[t][3];
+    st.l[t][0] += pr[t][0] + pr[t][2];
+    st.l[t][1] += pr[t][1] + pr[t][3];
   }
+  // V words of both halves
+#pragma unroll
+  for (int h = 0; h < 2; ++h) load_vec<NG>(w[h], rec + Kv4<D>::kV + h * Kv4<D>::kPlane + lane * (4 * NG));
+  uint32_t pb[NT][NG][2];  // P times the scales of group g: keys 0-7, keys 8-15
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const uint32_t v0 = w.v[0][g], v1 = w.v[1][g];
     const float s0 = vs(0, g), s1 = vs(1, g);
-    const uint32_t a0 = widen(v0, 0), a1 = widen(v0, 1), a2 = widen(v1, 0), a3 = widen(v1, 1);
-    const uint32_t a4 = widen(v0, 2), a5 = widen(v0, 3), a6 = widen(v1, 2), a7 = widen(v1, 3);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const uint32_t b0 = transpose8x8(pack2(s[t][0] * s0, s[t][1] * s0));  // keys 0-7
-      const uint32_t b1 = transpose8x8(pack2(s[t][2] * s1, s[t][3] * s1));  // keys 8-15
-      mma_bf16(st.o[t][2 * g], a0, a1, a2, a3, b0, b1);
-      mma_bf16(st.o[t][2 * g + 1], a4, a5, a6, a7, b0, b1);
-      mma_bf16(st.ones[t][g], kOnes, kOnes, kOnes, kOnes, b0, b1);
+      pb[t][g][0] = transpose8x8(pack2(pr[t][0] * s0, pr[t][1] * s0));
+      pb[t][g][1] = transpose8x8(pack2(pr[t][2] * s1, pr[t][3] * s1));
     }
   }
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t x[2], y[2];  // tokens of half 0, half 1
+      widen(w[0][g], 2 * half, mk, x);
+      widen(w[1][g], 2 * half, mk, y);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma_bf16(st.o[t][2 * g + half], x[0], x[1], y[0], y[1], pb[t][g][0], pb[t][g][1]);
+        if (half == 0) mma_bf16(st.ones[t][g], mk.ones, mk.ones, mk.ones, mk.ones, pb[t][g][0], pb[t][g][1]);
+      }
+    }
 }
 
 // Warps of a CTA: two n-tiles of heads take twice the registers and half the warps.
 template <int NT>
-constexpr int kWarpsOf = NT == 1 ? 16 : 8;
+constexpr int kWarpsOf = NT == 1 ? 12 : 8;
 
-// A partial result in shared memory: O [heads][D] and (reference, sum) [heads].
+// A partial result's O [heads][D] in shared memory (its references and sums lie in s_ml).
 template <int D, int NT>
-constexpr int kSlotFloats = 8 * NT * (D + 2);
+constexpr int kSlotFloats = 8 * NT * D;
+
+// Records on their way to one warp, or held for it: about 36 KB per SM keep HBM busy.
+template <int NT>
+constexpr int kStagesOf = NT == 1 ? 5 : 8;
+
+// Bytes of a warp's shared memory: the partial result of its first (request, kv head), then its ring,
+// which holds the partial result of the last one when the warp is through.
+template <int D, int NT>
+constexpr int kWarpBytes = kSlotFloats<D, NT> * 4 + kStagesOf<NT> * Kv4<D>::kRecord;
+
+// A warp's place in the batch's records.
+struct Place {
+  int s, h, i, n;  // request, kv head, record of it, its records
+};
 
 struct SlotInfo {
   int64_t p0, p1;  // the records of its (request, kv head) in the batch's order
@@ -301,29 +366,43 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   constexpr int NG = Kv4<D>::kGroups;
   constexpr int kWarps = kWarpsOf<NT>, kThreads = kWarps * 32;
   constexpr int kSlot = kSlotFloats<D, NT>;
-  extern __shared__ float slots[];  // [2 kWarps][kSlot]
-  __shared__ SlotInfo info[2 * kWarps];
-  __shared__ int64_t s_start[kWarps];  // first record of the request that a warp's run begins in
-  __shared__ int32_t s_seq[kWarps];    // that request
+  constexpr int kStages = kStagesOf<NT>;
+  constexpr int kRecord = Kv4<D>::kRecord;
+  static_assert(kStages * kRecord >= kSlot * 4 && kSlot % 4 == 0, "a partial result fits a warp's ring");
+  extern __shared__ __align__(16) uint8_t smem[];  // [kWarps] first partial result, ring
+  __shared__ uint64_t full[kWarps][kStages];
+  __shared__ int s_abort;
+  constexpr int kSlots = 2 * kWarps, kHeads = 8 * NT;
+  __shared__ SlotInfo info[kSlots];
+  __shared__ float2 s_ml[kSlots][kHeads];     // (reference, sum) of the partial results
+  __shared__ float s_weight[kSlots][kHeads];  // their weights in their groups
+  __shared__ float2 s_group[kSlots][kHeads];  // (max, sum) of the group that begins at a slot
+  __shared__ int64_t s_start[kWarps];         // first record of the request that a warp's run begins in
+  __shared__ int32_t s_seq[kWarps];           // that request
   __shared__ int64_t w_sum[kWarps];
-  __shared__ int s_last;
+  __shared__ int s_last[2];
 
   pdl_launch_dependents();
+  if (threadIdx.x < kWarps * kStages) mbar_init(smem_u32(&full[0][threadIdx.x]), 1);
+  if (threadIdx.x == 0) s_abort = 0;
+  if (threadIdx.x < kSlots) info[threadIdx.x].pair = -1;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   pdl_wait();
+  auto slot_at = [&](int slot) -> float* {
+    return reinterpret_cast<float*>(smem + (slot / 2) * kWarpBytes<D, NT> + (slot % 2) * kSlot * 4);
+  };
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int r = lane / 4, c = lane % 4;
-  const int64_t room = (int64_t)p.width * p.page_size;
-  auto len_of = [&](int s) -> int32_t {
-    const int32_t n = p.lens[s];
-    return n < 0 ? 0 : (n < room ? n : (int32_t)room);
-  };
-  auto records_of = [&](int s) -> int64_t { return ((int64_t)len_of(s) + kKv4Block - 1) / kKv4Block; };
+  const int32_t room = p.width * p.page_size;  // fits: the host checks
+  auto len_of = [&](int s) -> int32_t { return min(max(__ldg(p.lens + s), 0), room); };
+  auto records_of = [&](int s) -> int { return (int)(((int64_t)len_of(s) + kKv4Block - 1) / kKv4Block); };
 
   // The batch's records, and where each warp's run of them begins.
-  const int run = (p.n_seqs + kThreads - 1) / kThreads;
-  const int q0 = min(tid * run, p.n_seqs), q1 = min(q0 + run, p.n_seqs);
+  const int run_s = (p.n_seqs + kThreads - 1) / kThreads;
+  const int q0 = min(tid * run_s, p.n_seqs), q1 = min(q0 + run_s, p.n_seqs);
   int64_t mine = 0;
-  for (int s = q0; s < q1; ++s) mine += records_of(s) * p.hkv;
+  for (int s = q0; s < q1; ++s) mine += (int64_t)records_of(s) * p.hkv;
   int64_t up = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -331,70 +410,142 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
     if (lane >= d) up += x;
   }
   if (lane == 31) w_sum[warp] = up;
-  if (tid < 2 * kWarps) info[tid].pair = -1;
   __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += w_sum[w];
-    all += w_sum[w];
+  int64_t sums = lane < kWarps ? w_sum[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < kWarps; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, sums, d);
+    if (lane >= d) sums += x;
   }
-  before += up - mine;
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
-  const int64_t quota = (all + warps - 1) / warps;  // records per warp
-  const int64_t cta0 = blockIdx.x * kWarps * quota;
-  if (mine > 0) {
+  const int64_t all = __shfl_sync(0xffffffffu, sums, kWarps - 1);
+  const int64_t before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0) * (warp > 0) + up - mine;
+  const int warps = gridDim.x * kWarps;
+  const int64_t quota =  // records per warp
+      all < 0x7fffffff - warps ? ((uint32_t)all + warps - 1) / (uint32_t)warps : (all + warps - 1) / warps;
+  const int64_t cta_records = kWarps * quota, cta0 = blockIdx.x * cta_records, cta1 = min(cta0 + cta_records, all);
+  if (mine > 0 && before < cta1 && before + mine > cta0) {
     for (int w = 0; w < kWarps; ++w) {
       const int64_t a = cta0 + w * quota;
       if (a < before || a >= before + mine) continue;
       int64_t at = before;
       int s = q0;
-      while (a >= at + records_of(s) * p.hkv) at += records_of(s++) * p.hkv;
+      while (a >= at + (int64_t)records_of(s) * p.hkv) at += (int64_t)records_of(s++) * p.hkv;
       s_seq[w] = s;
       s_start[w] = at;
     }
   }
-  // Requests without keys get zeros; lengths outside [0, room] are recorded.
-  for (int s = blockIdx.x; s < p.n_seqs; s += gridDim.x) {
-    const int32_t n = p.lens[s];
-    if ((n < 0 || n > room) && tid == 0) record_error(p.err, kErrIndex, s);
-    if (n <= 0)
-      for (int i = tid; i < p.hkv * p.G * D / 8; i += kThreads)
-        reinterpret_cast<uint4*>(p.out)[(int64_t)s * p.hkv * p.G * D / 8 + i] = make_uint4(0, 0, 0, 0);
-  }
   __syncthreads();
-  if (cta0 >= all) return;
+  // Requests without keys get zeros; lengths outside [0, room] are recorded.
+  auto check_requests = [&]() {
+    for (int s = blockIdx.x * kWarps + warp; s < p.n_seqs; s += warps) {
+      const int32_t n = __ldg(p.lens + s);
+      if ((n < 0 || n > room) && lane == 0) record_error(p.err, kErrIndex, s);
+      if (n <= 0 || room == 0)
+        for (int i = lane; i < p.hkv * p.G * D / 8; i += 32)
+          reinterpret_cast<uint4*>(p.out)[(int64_t)s * p.hkv * p.G * D / 8 + i] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (cta0 >= all) {
+    check_requests();
+    return;
+  }
 
   const int blocks = p.page_size / kKv4Block;  // records per page and kv head
-  const int64_t a0 = cta0 + warp * quota;
-  int64_t a = a0;
-  const int64_t a_end = min(a0 + quota, all);
-  if (a < a_end) {
-    int s = s_seq[warp];
-    int64_t n = records_of(s);
-    int h = (int)((a - s_start[warp]) / n);
-    int64_t b = (a - s_start[warp]) - h * n;
+  const int64_t a0 = cta0 + warp * quota, a_end = min(a0 + quota, all);
+  if (a0 < a_end) {
+    int rest = (int)(a_end - a0);  // records still to take
+    volatile int* abort_flag = &s_abort;
+    const uint32_t ring = smem_u32(smem) + warp * kWarpBytes<D, NT> + kSlot * 4;
+    Place at;
+    at.s = s_seq[warp];
+    at.n = records_of(at.s);
+    const uint32_t behind = (uint32_t)(a0 - s_start[warp]);  // in the request: below 2^27 hkv records
+    at.h = (int)(behind / (uint32_t)at.n);
+    at.i = (int)(behind - (uint32_t)at.h * at.n);
+    auto next = [&](Place& x) {
+      if (++x.i < x.n) return;
+      x.i = 0;
+      if (++x.h < p.hkv) return;
+      x.h = 0;
+      do {
+        ++x.s;
+        x.n = x.s < p.n_seqs ? records_of(x.s) : 1;
+      } while (x.n == 0);
+    };
+    // The warp's own producer: records in the order of its run, kStages ahead. `run` records from src on
+    // are neighbours in a page; behind them the next page's id comes from lane (page index - w0) of a
+    // window of 32 entries of the table's row. All lanes keep the producer's state, lane 0 acts.
+    Place to = at;       // first record behind the neighbours
+    int left = rest;     // records still to request
+    int run = 0, w0 = 0, ws = -1;
+    int32_t win = -1;
+    bool page_ok = false;
+    const uint8_t* src = nullptr;
+    uint32_t bad = 0;  // stages whose record's page is none
+    const uint32_t bar0 = smem_u32(&full[warp][0]);
+    uint32_t fill_bar = bar0, fill_dst = ring, fill_bit = 1;
+    auto next_page = [&]() {
+      const int pi = to.i / blocks, in_page = to.i - pi * blocks;
+      if (to.s != ws || pi < w0 || pi >= w0 + 32) {
+        ws = to.s;
+        w0 = pi;
+        win = (int64_t)(pi + lane) * blocks < to.n ? p.table[(int64_t)ws * p.width + pi + lane] : -1;
+      }
+      const int32_t page = __shfl_sync(0xffffffffu, win, pi - w0);
+      page_ok = page >= 0 && page < p.n_pages;
+      src = p.cache + (((int64_t)(page_ok ? page : 0) * p.hkv + to.h) * blocks + in_page) * kRecord;
+      if (!page_ok && lane == 0) record_error(p.err, kErrIndex, to.s);
+      run = min(blocks - in_page, to.n - to.i);
+      to.i += run - 1;
+      next(to);
+    };
+    auto request = [&]() {
+      if (left == 0) return;
+      if (run == 0) next_page();
+      if (page_ok) {
+        bad &= ~fill_bit;
+        if (lane == 0) {
+          mbar_expect_tx(fill_bar, kRecord);
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(fill_dst),
+              "l"(src), "r"(kRecord), "r"(fill_bar)
+              : "memory");
+        }
+      } else {
+        bad |= fill_bit;
+        if (lane == 0) mbar_arrive(fill_bar);  // the phase passes without a copy
+      }
+      src += kRecord;
+      --run;
+      --left;
+      const bool wrap = fill_bit == 1u << (kStages - 1);
+      fill_bar = wrap ? bar0 : fill_bar + 8;
+      fill_dst = wrap ? ring : fill_dst + kRecord;
+      fill_bit = wrap ? 1 : fill_bit << 1;
+    };
+    for (int k = 0; k < kStages; ++k) request();
+    check_requests();  // while the first records come
+    int stage = 0, parity = 0;
     State<D, NT> st;
     Query<D, NT> qf;
-    while (a < a_end) {
-      const int64_t count = min(n - b, a_end - a);
-      const int32_t len = len_of(s);
+    bool first = true;
+    while (rest > 0) {
+      const int s = at.s, h = at.h;
+      const int count = min(at.n - at.i, rest);
       load_query<D, NT>(qf, p.q + ((int64_t)s * p.hkv + h) * p.G * D * 2, p.G, lane);
       reset(st);
-      for (int64_t i = b; i < b + count; ++i) {
-        const int32_t page = p.table[(int64_t)s * p.width + i / blocks];
-        int valid = (int)min((int64_t)len - i * kKv4Block, (int64_t)kKv4Block);
-        Words<NG> w;
-        if (page >= 0 && page < p.n_pages) {
-          load_record<D>(w, p.cache + (((int64_t)page * p.hkv + h) * blocks + i % blocks) * Kv4<D>::kRecord, lane);
-        } else {
-          if (lane == 0) record_error(p.err, kErrIndex, s);
-          valid = 0;
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int g = 0; g < NG; ++g) w.k[x][g] = w.v[x][g] = w.sc[x][g] = 0;
-        }
-        step<D, NT>(st, qf, w, valid, p.scale_log2, lane);
+      int keys = len_of(s) - at.i * kKv4Block;  // from the record on
+      for (int i = 0; i < count; ++i, keys -= kKv4Block) {
+        mbar_spin(bar0 + 8 * stage, parity, abort_flag, p.err, 80);
+        __syncwarp();
+        const uint32_t rec = ring + stage * kRecord;
+        if (keys >= kKv4Block && !(bad >> stage & 1))
+          step<D, NT, true>(st, qf, rec, kKv4Block, p.scale_log2, p.masks, lane);
+        else  // without its page, a stage holds an earlier record: weight 0
+          step<D, NT, false>(st, qf, rec, bad >> stage & 1 ? 0 : min(keys, kKv4Block), p.scale_log2, p.masks, lane);
+        __syncwarp();
+        request();  // into the stage just read
+        if (++stage == kStages) stage = 0, parity ^= 1;
       }
       // sums over the lanes of a head
 #pragma unroll
@@ -407,9 +558,9 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
           x += __shfl_xor_sync(0xffffffffu, x, 16);
           st.l[t][e] = x;
         }
-      const bool whole = b == 0 && count == n;
-      const int slot = 2 * warp + (a == a0 ? 0 : 1);
-      float* so = slots + slot * kSlot;
+      const bool whole = count == at.n;
+      const int slot = 2 * warp + (first ? 0 : 1);
+      float* so = slot_at(slot);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -427,103 +578,200 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
             else
               *reinterpret_cast<float4*>(so + head * D + 32 * g + 4 * r) = x;
           }
-          if (!whole && r == 0) {
-            so[8 * NT * D + 2 * head] = st.m[t][e];
-            so[8 * NT * D + 2 * head + 1] = st.l[t][e];
-          }
+          if (!whole && r == 0) s_ml[slot][head] = make_float2(st.m[t][e], st.l[t][e]);
         }
       if (!whole && lane == 0) {
         info[slot].pair = s * p.hkv + h;
-        info[slot].p0 = a - b;
-        info[slot].p1 = a - b + n;
+        info[slot].p0 = a_end - rest - at.i;
+        info[slot].p1 = info[slot].p0 + at.n;
       }
-      a += count;
-      b = 0;
-      if (++h == p.hkv && a < a_end) {
-        h = 0;
-        do {
-          ++s;
-          n = records_of(s);
-        } while (n == 0);
+      rest -= count;
+      at.i += count - 1;
+      next(at);
+      first = false;
+    }
+  } else {
+    check_requests();
+  }
+  __syncthreads();
+
+  // Merge the partial results of each (request, kv head) of this CTA, then those of a (request, kv head)
+  // that spans CTAs, by the last of them. Slots of one (request, kv head) are neighbours (a group, with
+  // empty slots among them); lane k of every warp looks at slot k; groups begin at the set bits of `groups`.
+  const int n4 = p.G * D / 4;
+  const int my_pair = lane < kSlots ? info[lane].pair : -1;
+  const uint32_t held = __ballot_sync(0xffffffffu, my_pair >= 0);
+  const int prev = 31 - __clz(held & ((1u << lane) - 1));  // -1: none
+  const int prev_pair = __shfl_sync(0xffffffffu, my_pair, prev < 0 ? 0 : prev);
+  const uint32_t groups = __ballot_sync(0xffffffffu, my_pair >= 0 && (prev < 0 || prev_pair != my_pair));
+  auto group_end = [&](int k) -> int {  // one past the group that begins at slot k
+    const uint32_t later = groups & ~((2u << k) - 1);
+    return later ? __ffs(later) - 1 : kSlots;
+  };
+  // Weights: a warp per head, sums and maxima over the lanes of a group by segmented scans.
+  {
+    const uint32_t upto = groups & ((2u << lane) - 1);
+    const int g0 = upto ? 31 - __clz(upto) : 0;
+    const int end = min(upto ? group_end(g0) : lane + 1, 32) - 1;
+    for (int head = warp; head < p.G; head += kWarps) {
+      const float2 ml = my_pair >= 0 ? s_ml[lane][head] : make_float2(kLow, 0.0f);
+      float m = ml.x;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const float x = __shfl_up_sync(0xffffffffu, m, d);
+        if (lane - d >= g0) m = fmaxf(m, x);
+      }
+      m = __shfl_sync(0xffffffffu, m, end);
+      const float wk = my_pair >= 0 ? ex2(ml.x - m) : 0.0f;
+      float l = wk * ml.y;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const float x = __shfl_up_sync(0xffffffffu, l, d);
+        if (lane - d >= g0) l += x;
+      }
+      l = __shfl_sync(0xffffffffu, l, end);
+      if (my_pair >= 0) {
+        s_weight[lane][head] = wk;
+        if (lane == g0) s_group[lane][head] = make_float2(m, l);
       }
     }
   }
   __syncthreads();
-
-  // Merge the partials of each (request, kv head) of this CTA; then those of a (request, kv head) that
-  // spans CTAs, by the last of them.
-  const int64_t cta_records = kWarps * quota;
-  const int64_t cta1 = min(cta0 + cta_records, all);
-  const int n4 = p.G * D / 4;
-  for (int i = 0; i < 2 * kWarps;) {
-    const int pair = info[i].pair;
-    if (pair < 0) {
-      ++i;
+  uint32_t to_do = groups;
+  for (int at = tid; to_do != 0;) {  // all groups' elements in one range
+    if (at >= n4) {
+      at -= n4;
+      to_do &= to_do - 1;
       continue;
     }
-    int j = i + 1;  // slots i .. j - 1 hold it, some of them may be empty
-    while (j < 2 * kWarps && (info[j].pair == pair || info[j].pair < 0)) ++j;
-    const int64_t p0 = info[i].p0, p1 = info[i].p1;
-    const bool inside = p0 >= cta0 && p1 <= cta1;
-    const int part = blockIdx.x * 2 + (p0 < cta0 ? 0 : 1);
-    for (int x = tid; x < n4; x += kThreads) {
-      const int head = x * 4 / D;
-      float m = -INFINITY;
-      for (int k = i; k < j; ++k)
-        if (info[k].pair >= 0) m = fmaxf(m, slots[k * kSlot + 8 * NT * D + 2 * head]);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l = 0.0f;
-      for (int k = i; k < j; ++k) {
-        if (info[k].pair < 0) continue;
-        const float* so = slots + k * kSlot;
-        const float mk = so[8 * NT * D + 2 * head];
-        const float wk = mk == -INFINITY ? 0.0f : ex2(mk - m);
-        const float4 v = *reinterpret_cast<const float4*>(so + x * 4);
-        l = fmaf(wk, so[8 * NT * D + 2 * head + 1], l);
-        acc.x = fmaf(wk, v.x, acc.x);
-        acc.y = fmaf(wk, v.y, acc.y);
-        acc.z = fmaf(wk, v.z, acc.z);
-        acc.w = fmaf(wk, v.w, acc.w);
+    const int g0 = __ffs(to_do) - 1, head = at * 4 / D;
+    const int g1 = group_end(g0);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t some = held & (0xffffffffu >> (32 - g1)) & ~((1u << g0) - 1); some != 0;) {
+      int k[4];  // up to four slots at a time
+      float wk[4];
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        k[u] = some ? __ffs(some) - 1 : g0;
+        wk[u] = some ? s_weight[k[u]][head] : 0.0f;
+        some &= some - 1;
+        v[u] = *reinterpret_cast<const float4*>(slot_at(k[u]) + at * 4);
       }
-      if (inside) {
-        write_out4(p.out, (int64_t)pair * p.G + head, D, x % (D / 4), acc, inverse(l));
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + ((int64_t)part * 16 * D + x * 4)) = acc;
-        if (x % (D / 4) == 0) p.part_ml[part * 16 + head] = make_float2(m, l);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (wk[u] == 0.0f) continue;  // (a slot of no keys, or none: 0 times what is not finite)
+        acc.x = fmaf(wk[u], v[u].x, acc.x);
+        acc.y = fmaf(wk[u], v[u].y, acc.y);
+        acc.z = fmaf(wk[u], v[u].z, acc.z);
+        acc.w = fmaf(wk[u], v[u].w, acc.w);
       }
     }
-    if (!inside) {
-      const int c0 = (int)(p0 / cta_records), c1 = (int)((p1 - 1) / cta_records);
+    const SlotInfo& x = info[g0];
+    const float2 ml = s_group[g0][head];
+    if (x.p0 >= cta0 && x.p1 <= cta1) {
+      write_out4(p.out, (int64_t)x.pair * p.G + head, D, at % (D / 4), acc, inverse(ml.y));
+    } else {
+      const int part = blockIdx.x * 2 + (x.p0 < cta0 ? 0 : 1);
+      *reinterpret_cast<float4*>(p.part_o + part * kKv4MaxGroup * D + at * 4) = acc;
+      if (at % (D / 4) == 0) p.part_ml[part * kKv4MaxGroup + head] = ml;
+    }
+    at += kThreads;
+  }
+  // At most the first and the last group reach past this CTA.
+  const int edge[2] = {groups ? __ffs(groups) - 1 : -1, groups ? 31 - __clz(groups) : -1};
+  auto reaches = [&](int e) -> bool {
+    if (edge[e] < 0 || (e == 1 && edge[1] == edge[0])) return false;
+    const SlotInfo& x = info[edge[e]];
+    return x.p0 < cta0 || x.p1 > cta1;
+  };
+  if (!reaches(0) && !reaches(1)) return;
+  __syncthreads();  // the CTA's parts are written
+  if (tid < 2) {
+    s_last[tid] = 0;
+    if (reaches(tid)) {
+      const SlotInfo& x = info[edge[tid]];
+      const int c0 = (int)(x.p0 / cta_records), c1 = (int)((x.p1 - 1) / cta_records);
       __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomicAdd(&p.tickets[c0], 1) == c1 - c0;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        for (int x = tid; x < n4; x += kThreads) {
-          const int head = x * 4 / D;
-          float m = -INFINITY;
-          for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg(&p.part_ml[(2 * k + (k == c0)) * 16 + head]).x);
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float l = 0.0f;
-          for (int k = c0; k <= c1; ++k) {
-            const int64_t at = 2 * k + (k == c0);
-            const float2 ml = __ldcg(&p.part_ml[at * 16 + head]);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * 16 * D + x * 4));
-            const float wk = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
-            l = fmaf(wk, ml.y, l);
-            acc.x = fmaf(wk, v.x, acc.x);
-            acc.y = fmaf(wk, v.y, acc.y);
-            acc.z = fmaf(wk, v.z, acc.z);
-            acc.w = fmaf(wk, v.w, acc.w);
-          }
-          write_out4(p.out, (int64_t)pair * p.G + head, D, x % (D / 4), acc, inverse(l));
-        }
-        if (tid == 0) p.tickets[c0] = 0;  // ready for the next call
+      if (atomicAdd(&p.tickets[c0], 1) == c1 - c0) {
+        s_last[tid] = 1;
+        p.tickets[c0] = 0;  // ready for the next call
       }
-      __syncthreads();
+      __threadfence();
     }
-    i = j;
+  }
+  __syncthreads();
+  float* scratch = reinterpret_cast<float*>(smem);  // the partial results in it have been read
+  constexpr int kSums = kMaxCtas * kKv4MaxGroup, kTeams = kSums + kKv4MaxGroup;
+  static_assert(kWarps * kWarpBytes<D, NT> >= (kTeams + 4 * kThreads) * 4, "scratch of the merge over CTAs");
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    if (!s_last[e]) continue;
+    const SlotInfo x = info[edge[e]];
+    const int c0 = (int)(x.p0 / cta_records), parts = (int)((x.p1 - 1) / cta_records) - c0 + 1;
+    auto part_of = [&](int k) -> int { return 2 * (c0 + k) + (k == 0 ? 1 : 0); };
+    // weights of the parts, a warp per head: scratch [part][head], then the heads' sums
+    for (int head = warp; head < p.G; head += kWarps) {
+      float2 ml[kMaxCtas / 32];  // parts lane, lane + 32, ...
+      float m = kLow, l = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kMaxCtas / 32; ++u) {
+        ml[u] = make_float2(kLow, 0.0f);
+        if (lane + 32 * u < parts) ml[u] = __ldcg(&p.part_ml[part_of(lane + 32 * u) * kKv4MaxGroup + head]);
+      }
+#pragma unroll
+      for (int u = 0; u < kMaxCtas / 32; ++u) m = fmaxf(m, ml[u].x);
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+      for (int u = 0; u < kMaxCtas / 32; ++u) {
+        const float wk = ex2(ml[u].x - m);
+        l = fmaf(wk, ml[u].y, l);
+        if (lane + 32 * u < parts) scratch[(lane + 32 * u) * kKv4MaxGroup + head] = wk;
+      }
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      if (lane == 0) scratch[kSums + head] = l;
+    }
+    __syncthreads();
+    // the threads in teams of n4 (a power of two), each taking every (kThreads / n4)-th part
+    const int teams = kThreads >= n4 ? kThreads / n4 : 1;
+    if (tid < teams * n4 || teams == 1)
+      for (int at = tid & (n4 - 1), team = teams > 1 ? tid / n4 : 0; at < n4; at += kThreads) {
+        const int head = at * 4 / D;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = team; k < parts; k += 4 * teams) {
+          float4 v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (k + u * teams < parts)
+              v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + part_of(k + u * teams) * kKv4MaxGroup * D + at * 4));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (k + u * teams >= parts) continue;
+            const float wk = scratch[(k + u * teams) * kKv4MaxGroup + head];
+            acc.x = fmaf(wk, v[u].x, acc.x);
+            acc.y = fmaf(wk, v[u].y, acc.y);
+            acc.z = fmaf(wk, v[u].z, acc.z);
+            acc.w = fmaf(wk, v[u].w, acc.w);
+          }
+        }
+        if (teams > 1)
+          *reinterpret_cast<float4*>(scratch + kTeams + 4 * (team * n4 + at)) = acc;
+        else
+          write_out4(p.out, (int64_t)x.pair * p.G + head, D, at % (D / 4), acc, inverse(scratch[kSums + head]));
+      }
+    __syncthreads();
+    if (teams > 1 && tid < n4) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int team = 0; team < teams; ++team) {
+        const float4 v = *reinterpret_cast<const float4*>(scratch + kTeams + 4 * (team * n4 + tid));
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      }
+      write_out4(p.out, (int64_t)x.pair * p.G + tid * 4 / D, D, tid % (D / 4), acc,
+                 inverse(scratch[kSums + tid * 4 / D]));
+    }
+    __syncthreads();  // the scratch is used again
   }
 }
 
@@ -532,8 +780,9 @@ cudaError_t launch_t(const Kv4DecodeParams& p, int32_t sms, cudaStream_t s) {
   constexpr int kWarps = kWarpsOf<NT>;
   const int64_t most = (int64_t)p.n_seqs * p.hkv * p.width * (p.page_size / kKv4Block);  // records at most
   const int64_t ctas = (most + kWarps - 1) / kWarps;
+  if (sms > kMaxCtas) sms = kMaxCtas;
   const int grid = (int)(ctas < sms ? (ctas > 0 ? ctas : 1) : sms);
-  const size_t smem = sizeof(float) * 2 * kWarps * kSlotFloats<D, NT>;
+  const size_t smem = (size_t)kWarps * kWarpBytes<D, NT>;
   static std::atomic<uint64_t> configured{0};
   const cudaError_t e = set_smem_limit_once(kv4_decode_kernel<D, NT>, (int)smem, configured);
   if (e != cudaSuccess) return e;
@@ -559,6 +808,7 @@ cudaError_t launch_kv4_decode(const void* q, const void* cache, int32_t n_pages,
   p.hkv = hkv;
   p.G = hq / hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.masks = Masks{kNibbles, kBias, kOnes};
   p.part_o = ws.part_o;
   p.part_ml = ws.part_ml;
   p.tickets = ws.tickets;
