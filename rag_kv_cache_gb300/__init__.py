@@ -221,11 +221,13 @@ def cb_kv4_page_bytes(plan, page_size) -> int:
 
 def _arg(plan, t, dtype, shape, name):
     """Device pointer of a tensor that must be a contiguous `dtype` tensor of `shape` on the plan's device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == plan.device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == plan.device
-            and t.is_contiguous()):
-        return t.data_ptr()
     if isinstance(t, torch.Tensor) and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     _ptr(t, dtype, name)
@@ -234,16 +236,24 @@ def _arg(plan, t, dtype, shape, name):
 
 def _size(t, name, dim=0, dims=1):
     """Size `dim` of a tensor of `dims` dimensions."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dim(s), got shape {tuple(t.shape)}")
-    return t.shape[dim]
+    try:
+        shape = t.shape
+        if len(shape) == dims:
+            return shape[dim]
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    raise ValueError(f"{name} must have {dims} dim(s), got shape {tuple(shape)}")
 
 
 def _kv4_cache(plan, cache, page_size):
     n_pages = _size(cache, "cache", 0, 3)
-    return _arg(plan, cache, torch.uint8, (n_pages, plan.hkv, cb_kv4_page_bytes(plan, page_size)), "cache"), n_pages
+    # cb_kv4_page_bytes; the library refuses a page_size that is not supported
+    return _arg(plan, cache, torch.uint8, (n_pages, plan.hkv, page_size // 16 * 18 * plan.head_dim), "cache"), n_pages
+
+
+def _plan_stream(plan, stream):
+    """`stream`, or the current stream of the plan's device."""
+    return torch._C._cuda_getCurrentRawStream(plan.device) if stream is None else _stream(stream)
 
 
 def cb_page_tables(plan, ctx_lens, new_lens, page_size, free_pages, table, cu_seqlens, kv_lens, positions, slots,
@@ -258,7 +268,7 @@ def cb_page_tables(plan, ctx_lens, new_lens, page_size, free_pages, table, cu_se
         plan.handle, arg(ctx_lens, "ctx_lens", n), arg(new_lens, "new_lens", n), n, page_size,
         arg(free_pages, "free_pages", free), free, arg(free_from, "free_from", 1), arg(table, "table", n, width), width,
         arg(cu_seqlens, "cu_seqlens", n + 1), arg(kv_lens, "kv_lens", n), arg(positions, "positions", rows),
-        arg(slots, "slots", rows), rows, arg(free_to, "free_to", 1), _stream(stream)))
+        arg(slots, "slots", rows), rows, arg(free_to, "free_to", 1), _plan_stream(plan, stream)))
 
 
 def _kv4_rows(plan, k, v, slots):
@@ -272,14 +282,14 @@ def cb_kv4_store(plan, k, v, slots, cache, page_size, stream=None):
     """Rows k, v [n, hkv, D] quantised to 4 bits into cache at slots [n] (negative: skipped)."""
     pc, n_pages = _kv4_cache(plan, cache, page_size)
     pk, pv, ps, n = _kv4_rows(plan, k, v, slots)
-    check(_lib.load().cb_kv4_store(plan.handle, pk, pv, ps, n, pc, n_pages, page_size, _stream(stream)))
+    check(_lib.load().cb_kv4_store(plan.handle, pk, pv, ps, n, pc, n_pages, page_size, _plan_stream(plan, stream)))
 
 
 def cb_kv4_load(plan, cache, page_size, slots, k, v, stream=None):
     """k, v [n, hkv, D] = the rows that cache holds at slots [n] (negative: left as they are)."""
     pc, n_pages = _kv4_cache(plan, cache, page_size)
     pk, pv, ps, n = _kv4_rows(plan, k, v, slots)
-    check(_lib.load().cb_kv4_load(plan.handle, pc, n_pages, page_size, ps, n, pk, pv, _stream(stream)))
+    check(_lib.load().cb_kv4_load(plan.handle, pc, n_pages, page_size, ps, n, pk, pv, _plan_stream(plan, stream)))
 
 
 def cb_kv4_decode_attention(plan, q, cache, page_size, table, kv_lens, out, scale=0.0, stream=None):
@@ -291,7 +301,7 @@ def cb_kv4_decode_attention(plan, q, cache, page_size, table, kv_lens, out, scal
     check(_lib.load().cb_kv4_decode_attention(
         plan.handle, _arg(plan, q, torch.bfloat16, shape, "q"), pc, n_pages, page_size,
         _arg(plan, table, torch.int32, (n, width), "table"), width, _arg(plan, kv_lens, torch.int32, (n,), "kv_lens"), n,
-        float(scale), _arg(plan, out, torch.bfloat16, shape, "out"), _stream(stream)))
+        float(scale), _arg(plan, out, torch.bfloat16, shape, "out"), _plan_stream(plan, stream)))
 
 
 def cb_prompt_attention(plan, q, k, v, cu_seqlens, out, scale=0.0, stream=None):
@@ -304,7 +314,7 @@ def cb_prompt_attention(plan, q, k, v, cu_seqlens, out, scale=0.0, stream=None):
     check(_lib.load().cb_prompt_attention(
         plan.handle, _arg(plan, q, bf, q_shape, "q"), _arg(plan, k, bf, kv_shape, "k"), _arg(plan, v, bf, kv_shape, "v"),
         _arg(plan, cu_seqlens, torch.int32, (n,), "cu_seqlens"), n - 1, rows, float(scale),
-        _arg(plan, out, bf, q_shape, "out"), _stream(stream)))
+        _arg(plan, out, bf, q_shape, "out"), _plan_stream(plan, stream)))
 
 
 def cb_attention_uses_paired_tiles(plan, mq) -> bool:

@@ -18,6 +18,7 @@ namespace cb {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int32_t kRunRows = 1024;
 
 struct Kv4RowParams {
   const int32_t* slots;
@@ -63,12 +64,57 @@ __device__ __forceinline__ Lane<D> lane_of(const Kv4RowParams& p) {
   return x;
 }
 
+// What a group's codes are made with: its scale's bf16 bits, the scale (0: all codes are 0) and its
+// reciprocal (0: the scale is too small for one).
+struct Step {
+  uint32_t bits;
+  float scale, inverse;
+};
+// Of a group whose largest magnitude has the bf16 bits `top` (0x7f80 and up: not finite).
+__device__ __forceinline__ Step step_of(uint32_t top) {
+  const __nv_bfloat16 scale = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top << 16), 7.0f));
+  const bool finite = top < 0x7f80u;
+  Step s;
+  s.bits = finite ? (uint32_t)__bfloat16_as_ushort(scale) : 0x7fc0u;
+  s.scale = finite ? __bfloat162float(scale) : 0.0f;
+  s.inverse = s.scale > 1e-36f ? __fdiv_rn(1.0f, s.scale) : 0.0f;
+  return s;
+}
+
+// (code + 8) << at of x. The quotient q = x / scale needs its ties exact: a product with the reciprocal
+// and one Newton correction (the remainder x - q scale is exact in an fma) give the quotient wherever
+// fp32 holds it, which it does on every half; elsewhere it is at least 2^-9 away from one. A division per
+// value took three times as long as the kernel's loads and stores. Adding 1.5 * 2^23 + 8 rounds to the
+// integer (ties to even) and leaves code + 8 in the low bits; |code| <= 7 since the scale is within 2^-9
+// of max|x| / 7. Scales near the subnormal range take the division and a clamp.
+__device__ __forceinline__ uint32_t nibble(float x, const Step& s, int at) {
+  const float q = x * s.inverse;
+  const float y = fmaf(fmaf(-q, s.scale, x), s.inverse, q);
+  return (__float_as_uint(y + 12582920.0f) & 15u) << at;
+}
+__device__ __noinline__ uint32_t small_nibble(float x, float scale) {
+  const float c = scale > 0.0f ? rintf(__fdiv_rn(x, scale)) : 0.0f;
+  return (uint32_t)((int)fminf(fmaxf(c, -7.0f), 7.0f) + 8);
+}
+
+// Word of 8 values of one group, value i at bits at[i] (compile-time positions).
+template <typename At>
+__device__ __forceinline__ uint32_t nibbles8(const float (&f)[8], const Step& s, At at) {
+  uint32_t word = 0;
+  if (s.inverse != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) word |= nibble(f[i], s, at(i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) word |= small_nibble(f[i], s.scale) << at(i);
+  }
+  return word;
+}
+
+// One work item of a converged warp.
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_store_kernel(const uint8_t* k, const uint8_t* v, uint8_t* cache,
-                                                             const Kv4RowParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const Lane<D> x = lane_of<D>(p);
+__device__ __forceinline__ void store_row(const uint8_t* k, const uint8_t* v, uint8_t* cache, const Kv4RowParams& p,
+                                          const Lane<D>& x) {
   uint4 raw = make_uint4(0, 0, 0, 0);
   if (x.slot >= 0) raw = ld_stream((x.kv ? v : k) + ((x.row * p.hkv + x.h) * D + x.l * 8) * 2);
   // the group's largest magnitude as bf16 bits (ordered like the magnitudes; 0x7f80 and up: not finite)
@@ -79,44 +125,28 @@ __global__ void __launch_bounds__(kThreads) kv4_store_kernel(const uint8_t* k, c
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   if (x.slot < 0) return;
-  const bool finite = top < 0x7f80u;
-  const __nv_bfloat16 scale = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top << 16), 7.0f));
-  const float step = __bfloat162float(scale);
+  const Step step = step_of(top);
   float f[8];
   unpack8(raw, f);
-  uint32_t nib[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float c = finite && step > 0.0f ? rintf(__fdiv_rn(f[e], step)) : 0.0f;
-    nib[e] = (uint32_t)((int)fminf(fmaxf(c, -7.0f), 7.0f) + 8);  // |c| may pass 7 for subnormal scales
-  }
   constexpr int NG = Kv4<D>::kGroups;
   const int g = x.l / 4, c = x.l % 4, t = x.slot % kKv4Block;
   uint8_t* rec = cache + record_offset<D>(x.slot, x.h, p.hkv, p.page_size);
   if (x.kv == 0) {
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) word |= nib[2 * i] << (4 * i) | nib[2 * i + 1] << (16 + 4 * i);
-    *reinterpret_cast<uint32_t*>(rec + t * (D / 2) + (c * NG + g) * 4) = word;
+    *reinterpret_cast<uint32_t*>(rec + t * (D / 2) + (c * NG + g) * 4) =
+        nibbles8(f, step, [](int e) { return 4 * (e / 2) + 16 * (e % 2); });
   } else {
     uint8_t* vb = rec + Kv4<D>::kV + (t / 8) * Kv4<D>::kPlane + (t % 8 / 2) * (4 * NG) + g * 4 + (t % 2) * 2;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {  // dims 8 c + 4 q .. of the group: r = 2 c + q
-      const uint32_t half = nib[4 * q] | nib[4 * q + 1] << 4 | nib[4 * q + 2] << 8 | nib[4 * q + 3] << 12;
-      *reinterpret_cast<uint16_t*>(vb + (2 * c + q) * (16 * NG)) = (uint16_t)half;
-    }
+    const uint32_t word = nibbles8(f, step, [](int e) { return 4 * e; });  // r = 2 c in the low half, 2 c + 1 in the high
+    *reinterpret_cast<uint16_t*>(vb + 2 * c * (16 * NG)) = (uint16_t)word;
+    *reinterpret_cast<uint16_t*>(vb + (2 * c + 1) * (16 * NG)) = (uint16_t)(word >> 16);
   }
   if (c == 0)
-    *reinterpret_cast<uint16_t*>(rec + Kv4<D>::kScales + t * (4 * NG) + x.kv * (2 * NG) + g * 2) =
-        finite ? __bfloat16_as_ushort(scale) : (uint16_t)0x7fc0u;
+    *reinterpret_cast<uint16_t*>(rec + Kv4<D>::kScales + t * (4 * NG) + x.kv * (2 * NG) + g * 2) = (uint16_t)step.bits;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_load_kernel(uint8_t* k, uint8_t* v, const uint8_t* cache,
-                                                            const Kv4RowParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const Lane<D> x = lane_of<D>(p);
+__device__ __forceinline__ void load_row(uint8_t* k, uint8_t* v, const uint8_t* cache, const Kv4RowParams& p,
+                                         const Lane<D>& x) {
   if (x.slot < 0) return;
   constexpr int NG = Kv4<D>::kGroups;
   const int g = x.l / 4, c = x.l % 4, t = x.slot % kKv4Block;
@@ -146,16 +176,248 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(uint8_t* k, uint8_t*
   st_stream((x.kv ? v : k) + ((x.row * p.hkv + x.h) * D + x.l * 8) * 2, pack8(f));
 }
 
+template <int D, bool STORE>
+__global__ void __launch_bounds__(kThreads) kv4_rows_kernel(uint8_t* k, uint8_t* v, uint8_t* cache, const Kv4RowParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const Lane<D> x = lane_of<D>(p);
+  if (STORE)
+    store_row<D>(k, v, cache, p, x);
+  else
+    load_row<D>(k, v, cache, p, x);
+}
+
+// ---- whole records ---------------------------------------------------------------------------------
+//
+// Chunks fill pages in order, so most rows of a large call come in runs of 16 neighbours that are one
+// record (slots 16 m .. 16 m + 15). A warp takes one kv head of such a run with the decode kernel's lane
+// layout: 16-byte accesses of the record, 64-byte pieces of the bf16 rows, groups reduced by shuffles,
+// and two values per instruction where the arithmetic is exact in bf16 (a nibble widened to
+// 128 + nibble; minus 136; times the scale, one rounding). Row by row the V nibbles are 2-byte accesses
+// in eight sectors per row: 32,768 rows of 8 heads took 85 us to store and 66 us to load, in runs 48 and 28
+// (their bytes at the copy rate: 26).
+
+// What a warp finds in the 16 rows from `row0` on.
+struct Window {
+  int start;      // row of a whole record that begins here, -1: none
+  uint32_t rest;  // rows (bit i: row0 + i) that belong to no whole record and have a slot
+};
+
+__device__ __forceinline__ Window look_at(const Kv4RowParams& p, int64_t row0, int lane) {
+  // slots of rows row0 - 16 .. row0 + 47, two per lane (-1 outside the rows)
+  const int64_t a = row0 - 16 + lane, b = a + 32;
+  const int32_t sa = a >= 0 && a < p.n ? p.slots[a] : -1, sb = b < p.n ? p.slots[b] : -1;
+  // bit i: row row0 - 16 + i is followed by the next slot
+  const int32_t sa1 = __shfl_down_sync(0xffffffffu, sa, 1), sb1 = __shfl_down_sync(0xffffffffu, sb, 1);
+  const int32_t sb0 = __shfl_sync(0xffffffffu, sb, 0);
+  const bool fa = sa >= 0 && sa == (lane == 31 ? sb0 : sa1) - 1, fb = lane < 31 && sb >= 0 && sb == sb1 - 1;
+  const uint64_t follows = (uint64_t)__ballot_sync(0xffffffffu, fb) << 32 | __ballot_sync(0xffffffffu, fa);
+  // bit i: a whole record inside the cache begins at row row0 - 16 + i (i < 32)
+  const bool whole = sa >= 0 && sa % kKv4Block == 0 && (int64_t)sa + kKv4Block <= p.n_slots &&
+                     ((follows >> lane) & 0x7fffu) == 0x7fffu;
+  const uint32_t starts = __ballot_sync(0xffffffffu, whole);
+  uint32_t covered = 0;  // bit i: row row0 + i
+#pragma unroll
+  for (int d = 0; d < kKv4Block; ++d) covered |= (uint32_t)(((uint64_t)starts << d) >> 16);
+  Window w;
+  w.start = starts >> 16 ? __ffs(starts >> 16) - 1 : -1;
+  // slots of the window's rows: lanes 16 .. 31
+  w.rest = (__ballot_sync(0xffffffffu, sa >= 0) >> 16) & ~covered & 0xffffu;
+  return w;
+}
+
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {  // of two bf16 pairs' magnitudes, by half
+  return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
+}
+__device__ __forceinline__ uint32_t shuffled_max2(uint32_t x, int d) {
+  return __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, d));
+}
+
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+template <int NG>
+__device__ __forceinline__ void put_words(uint8_t* p, const uint32_t (&w)[NG]) {
+  if constexpr (NG == 4)
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+template <int NG>
+__device__ __forceinline__ void get_words(const uint8_t* p, uint32_t (&w)[NG]) {
+  if constexpr (NG == 4) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = x.x, w[1] = x.y;
+  }
+}
+
+// Rows row .. row + 15 of kv head h into their record.
 template <int D>
-cudaError_t launch_rows(bool store, const void* k, const void* v, const void* cache, const Kv4RowParams& p,
-                        cudaStream_t s) {
-  const int64_t lanes = (int64_t)p.n * p.hkv * 2 * (D / 8);
+__device__ __forceinline__ void store_record(const uint8_t* k, const uint8_t* v, uint8_t* rec, int64_t row, int h,
+                                             int hkv, int lane) {
+  constexpr int NG = Kv4<D>::kGroups;
+  const int r = lane / 4, c = lane % 4;
+  const int64_t pitch = (int64_t)hkv * D * 2, base = row * pitch + (int64_t)h * D * 2;
+  // K: tokens r and r + 8, 8 dims of each group per lane
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint4 x[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) x[g] = ld_stream(k + base + (r + 8 * half) * pitch + g * 64 + c * 16);
+    uint32_t word[NG], bits[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      uint32_t m = __vmaxu2(abs_max2(x[g].x, x[g].y), abs_max2(x[g].z, x[g].w));
+      m = shuffled_max2(shuffled_max2(m, 1), 2);
+      const Step step = step_of(max(m & 0xffffu, m >> 16));
+      bits[g] = step.bits;
+      float f[8];
+      unpack8(x[g], f);
+      word[g] = nibbles8(f, step, [](int e) { return 4 * (e / 2) + 16 * (e % 2); });
+    }
+    put_words<NG>(rec + half * Kv4<D>::kPlane + lane * (4 * NG), word);
+    if (c == 0)
+#pragma unroll
+      for (int g = 0; g < NG; g += 2)
+        *reinterpret_cast<uint32_t*>(rec + Kv4<D>::kScales + (r + 8 * half) * (4 * NG) + g * 2) = bits[g] | bits[g + 1] << 16;
+  }
+  // V: tokens 8 half + 2 c and + 1, dims 32 g + 4 r .. of each group per lane
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint2 x[2][NG];
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        x[o][g] = *reinterpret_cast<const uint2*>(v + base + (8 * half + 2 * c + o) * pitch + g * 64 + r * 8);
+    uint32_t word[NG], bits[2][NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      // both tokens' maxima in one register
+      const uint32_t m0 = abs_max2(x[0][g].x, x[0][g].y), m1 = abs_max2(x[1][g].x, x[1][g].y);
+      uint32_t m = max(m0 & 0xffffu, m0 >> 16) | max(m1 & 0xffffu, m1 >> 16) << 16;
+      m = shuffled_max2(shuffled_max2(shuffled_max2(m, 4), 8), 16);
+      word[g] = 0;
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const Step step = step_of(o ? m >> 16 : m & 0xffffu);
+        bits[o][g] = step.bits;
+        const float f[4] = {lo16(x[o][g].x), hi16(x[o][g].x), lo16(x[o][g].y), hi16(x[o][g].y)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          word[g] |= step.inverse != 0.0f ? nibble(f[e], step, 16 * o + 4 * e) : small_nibble(f[e], step.scale) << (16 * o + 4 * e);
+      }
+    }
+    put_words<NG>(rec + Kv4<D>::kV + half * Kv4<D>::kPlane + lane * (4 * NG), word);
+    if (r == 0)
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int g = 0; g < NG; g += 2)
+          *reinterpret_cast<uint32_t*>(rec + Kv4<D>::kScales + (8 * half + 2 * c + o) * (4 * NG) + 2 * NG + g * 2) =
+              bits[o][g] | bits[o][g + 1] << 16;
+  }
+}
+
+// A pair of nibbles at bits 0 and 16 as bf16 codes (exact), times a pair of scales (one rounding).
+__device__ __forceinline__ uint32_t codes_times(uint32_t nibbles, uint32_t scales) {
+  const uint32_t w = (nibbles & 0x000f000fu) | 0x43004300u;  // 128 + nibble
+  const __nv_bfloat162 code = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&w), __floats2bfloat162_rn(136.0f, 136.0f));
+  const __nv_bfloat162 x = __hmul2_rn(code, *reinterpret_cast<const __nv_bfloat162*>(&scales));
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// A record's 16 rows of kv head h.
+template <int D>
+__device__ __forceinline__ void load_record(uint8_t* k, uint8_t* v, const uint8_t* rec, int64_t row, int h, int hkv,
+                                            int lane) {
+  constexpr int NG = Kv4<D>::kGroups;
+  const int r = lane / 4, c = lane % 4;
+  const int64_t pitch = (int64_t)hkv * D * 2, base = row * pitch + (int64_t)h * D * 2;
+  uint32_t kw[2][NG], vw[2][NG], ksc[2][NG / 2], vsc[2][2][NG / 2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    get_words<NG>(rec + half * Kv4<D>::kPlane + lane * (4 * NG), kw[half]);
+    get_words<NG>(rec + Kv4<D>::kV + half * Kv4<D>::kPlane + lane * (4 * NG), vw[half]);
+#pragma unroll
+    for (int g = 0; g < NG / 2; ++g) {
+      const uint8_t* sc = rec + Kv4<D>::kScales + g * 4;
+      ksc[half][g] = __ldg(reinterpret_cast<const uint32_t*>(sc + (r + 8 * half) * (4 * NG)));
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+        vsc[half][o][g] = __ldg(reinterpret_cast<const uint32_t*>(sc + (8 * half + 2 * c + o) * (4 * NG) + 2 * NG));
+    }
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      // K: dims 8 c .. of the group, two neighbours per product
+      const uint32_t s2 = __byte_perm(ksc[half][g / 2], 0, g % 2 ? 0x3232 : 0x1010);
+      const uint32_t w = kw[half][g];
+      st_stream(k + base + (r + 8 * half) * pitch + g * 64 + c * 16,
+                make_uint4(codes_times(w, s2), codes_times(w >> 4, s2), codes_times(w >> 8, s2), codes_times(w >> 12, s2)));
+      // V: dims 4 r .. of the group, tokens 2 c (low halves) and 2 c + 1 (high) per product
+      const uint32_t t2 = __byte_perm(vsc[half][0][g / 2], vsc[half][1][g / 2], g % 2 ? 0x7632 : 0x5410);
+      const uint32_t y = vw[half][g];
+      const uint32_t d0 = codes_times(y, t2), d1 = codes_times(y >> 4, t2), d2 = codes_times(y >> 8, t2),
+                     d3 = codes_times(y >> 12, t2);
+      uint8_t* to = v + base + (8 * half + 2 * c) * pitch + g * 64 + r * 8;
+      *reinterpret_cast<uint2*>(to) = make_uint2(__byte_perm(d0, d1, 0x5410), __byte_perm(d2, d3, 0x5410));
+      *reinterpret_cast<uint2*>(to + pitch) = make_uint2(__byte_perm(d0, d1, 0x7632), __byte_perm(d2, d3, 0x7632));
+    }
+}
+
+// A warp per 16 rows and kv head: the whole record that begins in them, then the rows of no whole
+// record one by one (half a warp for K, half for V).
+template <int D, bool STORE>
+__global__ void __launch_bounds__(kThreads) kv4_runs_kernel(uint8_t* k, uint8_t* v, uint8_t* cache, const Kv4RowParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x % 32;
+  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32;
+  const int64_t row0 = unit / p.hkv * kKv4Block;
+  const int h = (int)(unit % p.hkv);
+  if (row0 >= p.n) return;
+  const Window w = look_at(p, row0, lane);
+  if (w.start >= 0) {
+    const int64_t row = row0 + w.start;
+    uint8_t* rec = cache + record_offset<D>(p.slots[row], h, p.hkv, p.page_size);
+    if (STORE)
+      store_record<D>(k, v, rec, row, h, p.hkv, lane);
+    else
+      load_record<D>(k, v, rec, row, h, p.hkv, lane);
+  }
+  for (uint32_t rest = w.rest; rest != 0; rest &= rest - 1) {
+    Lane<D> x;
+    x.row = row0 + __ffs(rest) - 1;
+    x.h = h;
+    x.kv = lane / 16;
+    x.l = lane % 16;
+    x.slot = x.l < D / 8 ? p.slots[x.row] : -1;
+    if (x.slot >= p.n_slots) {
+      if (h == 0 && lane == 0) record_error(p.err, kErrIndex, (int32_t)x.row);
+      x.slot = -1;
+    }
+    if (STORE)
+      store_row<D>(k, v, cache, p, x);
+    else
+      load_row<D>(k, v, cache, p, x);
+  }
+}
+
+template <int D, bool STORE>
+cudaError_t launch_rows(void* k, void* v, void* cache, const Kv4RowParams& p, cudaStream_t s) {
+  // By runs from kRunRows rows on, where there are warps enough to take 16 rows each; row by row below.
+  const bool runs = p.n >= kRunRows;
+  const int64_t lanes = runs ? ((int64_t)p.n + kKv4Block - 1) / kKv4Block * p.hkv * 32 : (int64_t)p.n * p.hkv * 2 * (D / 8);
   const int64_t blocks = (lanes + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  uint8_t *kb = static_cast<uint8_t*>(const_cast<void*>(k)), *vb = static_cast<uint8_t*>(const_cast<void*>(v)),
-          *cb = static_cast<uint8_t*>(const_cast<void*>(cache));
-  if (store) return launch_pdl(kv4_store_kernel<D>, dim3((unsigned)blocks), dim3(kThreads), 0, s, kb, vb, cb, p);
-  return launch_pdl(kv4_load_kernel<D>, dim3((unsigned)blocks), dim3(kThreads), 0, s, kb, vb, cb, p);
+  return launch_pdl(runs ? kv4_runs_kernel<D, STORE> : kv4_rows_kernel<D, STORE>, dim3((unsigned)blocks), dim3(kThreads), 0, s,
+                    static_cast<uint8_t*>(k), static_cast<uint8_t*>(v), static_cast<uint8_t*>(cache), p);
 }
 
 }  // namespace
@@ -165,8 +427,8 @@ cudaError_t launch_kv4_rows(bool store, void* k, void* v, const int32_t* slots, 
                             cudaStream_t s) {
   if (n <= 0) return cudaSuccess;
   const Kv4RowParams p{slots, n, hkv, page_size, (int64_t)n_pages * page_size, err};
-  if (head_dim == 128) return launch_rows<128>(store, k, v, cache, p, s);
-  if (head_dim == 64) return launch_rows<64>(store, k, v, cache, p, s);
+  if (head_dim == 128) return store ? launch_rows<128, true>(k, v, cache, p, s) : launch_rows<128, false>(k, v, cache, p, s);
+  if (head_dim == 64) return store ? launch_rows<64, true>(k, v, cache, p, s) : launch_rows<64, false>(k, v, cache, p, s);
   return cudaErrorInvalidValue;
 }
 

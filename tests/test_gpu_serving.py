@@ -174,6 +174,56 @@ def test_store_and_load(cb, hkv, d, n, page):
     plan.close()
 
 
+@pytest.mark.parametrize("hkv,d,page", [(2, 64, 16), (3, 128, 48), (8, 128, 256)])
+def test_store_and_load_by_runs(cb, hkv, d, page):
+    # calls of 1,024 rows and more: whole records at any offset of the rows, broken runs, runs that begin
+    # or end inside a record, padding, rows that a quantiser meets seldom, the last record of the cache
+    rng = np.random.default_rng(hkv + d + page)
+    plan = _plan(cb, hkv, hkv, d)
+    n_pages = -(-1500 // page) + 3
+    total = n_pages * page
+    pieces, at = [], 0
+    for size in (16, 5, 32, 11, 64, 16, 15, 17, 1, 100, 16, 240, 30, 33, 200, 7, 129):
+        start = at if len(pieces) % 3 else -(-at // 16) * 16  # some pieces begin inside a record
+        pieces.append(np.arange(start, start + size))
+        at = start + size
+        if size == 30:
+            pieces.append(np.full(3, -1))
+    rest = np.arange(-(-at // 16) * 16, total - 16)
+    pieces.append(rng.permutation(rest)[:150])
+    pieces.append(np.arange(total - 16, total))
+    slots = np.concatenate(pieces)
+    slots[130], slots[300] = slots[131], -1
+    slots[131] = -1  # (a slot that was there is named once)
+    n = len(slots)
+    assert n >= 1024 and len(set(slots[slots >= 0])) == (slots >= 0).sum()
+    k, v = _bits(rng, n, hkv, d), _bits(rng, n, hkv, d, scale=9.0)
+    for x in (k, v):
+        x[3], x[40], x[41, 0] = 0, f32_to_bf16_bits((rng.standard_normal((hkv, d)) * 1e-39).astype(np.float32)), 0x8000
+        x[50] = f32_to_bf16_bits((rng.standard_normal((hkv, d)) * 5e37).astype(np.float32))
+        x[60, 0, 33], x[61, 1, 1] = 0xFF80, 0x7FC1
+    before = rng.integers(0, 256, (n_pages, hkv, serving.page_bytes(page, d)), dtype=np.uint8)
+    cache = torch.as_tensor(before).cuda()
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(slots), cache, page)
+    want = before.copy()
+    serving.store(want, page, slots, bf16_bits_to_f64(k), bf16_bits_to_f64(v))
+    assert np.array_equal(cache.cpu().numpy(), want)
+    ok, ov = (torch.full((n, hkv, d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cb.cb_kv4_load(plan, cache, page, _i32(slots), ok, ov)
+    plan.check()
+    wk, wv = serving.load(want, page, np.maximum(slots, 0), d)
+    for g, w in ((_f64(ok), wk), (_f64(ov), wv)):
+        w = np.where((slots >= 0)[:, None, None], serving._to_bf16(w), 7.0)
+        assert np.array_equal(np.isnan(g), np.isnan(w))
+        assert np.array_equal(g[~np.isnan(w)], w[~np.isnan(w)])
+    # one slot past the cache in a long call
+    slots[700] = total
+    cb.cb_kv4_load(plan, cache, page, _i32(slots), ok, ov)
+    with pytest.raises(cb.CacheBlendError):
+        plan.check()
+    plan.close()
+
+
 def test_store_skips_and_records_slots_past_the_cache(cb):
     rng = np.random.default_rng(5)
     plan = _plan(cb, 4, 2, 64)
