@@ -415,7 +415,8 @@ cb_status cb_kv4_load(cb_plan* plan, const void* cache, int32_t n_pages, int32_t
  * behind a request's length may hold any bytes. Requests may share pages. fp32 scores, softmax and
  * accumulation; the softmax weights times V's scales are rounded to bf16 before the product.
  * Recorded as CB_ERR_DEVICE_CHECK: a negative length (as 0), one past table_width * P (cut there), a
- * table entry outside [0, n_pages) (its keys are left out). Partial results meet in the plan's
+ * table entry outside [0, n_pages) (its keys are left out). n_seqs * hkv * table_width * P must stay below
+ * 2^34 (CB_ERR_UNSUPPORTED). Partial results meet in the plan's
  * scratch: calls of this function on one plan must not overlap on the GPU; order them on one stream,
  * or give each stream its own plan. */
 cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,

@@ -614,6 +614,8 @@ cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cach
   if (n_seqs < 0 || table_width < 0) return fail(CB_ERR_INVALID_ARG, "negative size");
   if ((int64_t)n_seqs * c.hkv > 0x7fffffffll || (int64_t)table_width * page_size > 0x7fffffffll)
     return fail(CB_ERR_INVALID_ARG, "n_seqs * hkv or table_width * page_size above 2^31 - 1");
+  if ((int64_t)n_seqs * c.hkv * ((int64_t)table_width * page_size / 16) >= (1ll << 30))
+    return fail(CB_ERR_UNSUPPORTED, "n_seqs * hkv * table_width * page_size above 2^34");
   if (n_seqs == 0) return CB_OK;
   CB_TRY(need_tensor(q, "q"));
   if (n_pages > 0) CB_TRY(need_tensor(cache, "cache"));

@@ -39,6 +39,7 @@ namespace {
 
 constexpr float kHigh = 256.0f;           // a weight above it moves the reference
 constexpr float kLow = -3e38f;            // reference of a head that has seen nothing
+constexpr int kAlone = 6;                 // records per warp up to which a CTA takes a (request, kv head) alone
 constexpr int kMaxCtas = 160;             // of a launch (one wave: one per SM)
 constexpr float kOffset = 136.0f;         // value of a widened nibble of code 0
 constexpr uint32_t kNibbles = 0x000f000fu;
@@ -349,7 +350,7 @@ struct Place {
 };
 
 struct SlotInfo {
-  int64_t p0, p1;  // the records of its (request, kv head) in the batch's order
+  int32_t p0, p1;  // the records of its (request, kv head) in the batch's order
   int32_t pair;    // request * hkv + kv head, -1: empty
 };
 
@@ -377,9 +378,9 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   __shared__ float2 s_ml[kSlots][kHeads];     // (reference, sum) of the partial results
   __shared__ float s_weight[kSlots][kHeads];  // their weights in their groups
   __shared__ float2 s_group[kSlots][kHeads];  // (max, sum) of the group that begins at a slot
-  __shared__ int64_t s_start[kWarps];         // first record of the request that a warp's run begins in
+  __shared__ int32_t s_start[kWarps];         // first record of the request that a warp's run begins in
   __shared__ int32_t s_seq[kWarps];           // that request
-  __shared__ int64_t w_sum[kWarps];
+  __shared__ int32_t w_sum[kWarps];
   __shared__ int s_last[2];
 
   pdl_launch_dependents();
@@ -398,43 +399,60 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   auto len_of = [&](int s) -> int32_t { return min(max(__ldg(p.lens + s), 0), room); };
   auto records_of = [&](int s) -> int { return (int)(((int64_t)len_of(s) + kKv4Block - 1) / kKv4Block); };
 
-  // The batch's records, and where each warp's run of them begins.
+  // The batch's records, and where each warp's run of them begins (32 bits hold them: the host checks).
   const int run_s = (p.n_seqs + kThreads - 1) / kThreads;
   const int q0 = min(tid * run_s, p.n_seqs), q1 = min(q0 + run_s, p.n_seqs);
-  int64_t mine = 0;
-  for (int s = q0; s < q1; ++s) mine += (int64_t)records_of(s) * p.hkv;
-  int64_t up = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, up, d);
-    if (lane >= d) up += x;
+  int mine = 0, longest = 0;
+  for (int s = q0; s < q1; ++s) {
+    const int n = records_of(s);
+    mine += n * p.hkv;
+    longest = max(longest, n);
   }
-  if (lane == 31) w_sum[warp] = up;
-  __syncthreads();
-  int64_t sums = lane < kWarps ? w_sum[lane] : 0;
-#pragma unroll
-  for (int d = 1; d < kWarps; d <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, sums, d);
-    if (lane >= d) sums += x;
-  }
-  const int64_t all = __shfl_sync(0xffffffffu, sums, kWarps - 1);
-  const int64_t before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0) * (warp > 0) + up - mine;
   const int warps = gridDim.x * kWarps;
-  const int64_t quota =  // records per warp
-      all < 0x7fffffff - warps ? ((uint32_t)all + warps - 1) / (uint32_t)warps : (all + warps - 1) / warps;
-  const int64_t cta_records = kWarps * quota, cta0 = blockIdx.x * cta_records, cta1 = min(cta0 + cta_records, all);
-  if (mine > 0 && before < cta1 && before + mine > cta0) {
-    for (int w = 0; w < kWarps; ++w) {
-      const int64_t a = cta0 + w * quota;
-      if (a < before || a >= before + mine) continue;
-      int64_t at = before;
-      int s = q0;
-      while (a >= at + (int64_t)records_of(s) * p.hkv) at += (int64_t)records_of(s++) * p.hkv;
-      s_seq[w] = s;
-      s_start[w] = at;
+  int quota, cta_records, cta0, cta1;  // records per warp, per CTA, this CTA's first and last
+  if (__syncthreads_and(p.n_seqs * p.hkv <= (int)gridDim.x && longest <= kAlone * kWarps)) {
+    // A small batch of short requests: a CTA for each (request, kv head), so that none is merged over CTAs.
+    const int s = blockIdx.x / p.hkv, h = blockIdx.x - s * p.hkv;
+    const int n = s < p.n_seqs ? records_of(s) : 0;
+    quota = (n + kWarps - 1) / kWarps;
+    cta_records = n;
+    cta0 = h * n;  // counted from the request's first record
+    cta1 = cta0 + n;
+    if (lane == 0) s_seq[warp] = s, s_start[warp] = 0;
+    __syncwarp();
+  } else {
+    int up = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, up, d);
+      if (lane >= d) up += x;
     }
+    if (lane == 31) w_sum[warp] = up;
+    __syncthreads();
+    int sums = lane < kWarps ? w_sum[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < kWarps; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sums, d);
+      if (lane >= d) sums += x;
+    }
+    const int all = __shfl_sync(0xffffffffu, sums, kWarps - 1);
+    const int earlier = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+    const int before = (warp > 0 ? earlier : 0) + up - mine;
+    quota = (int)(((uint32_t)all + warps - 1) / (uint32_t)warps);
+    cta_records = kWarps * quota;
+    cta0 = (int)min((int64_t)blockIdx.x * cta_records, (int64_t)all);
+    cta1 = (int)min((int64_t)cta0 + cta_records, (int64_t)all);
+    if (before < cta1 && before + mine > cta0)
+      for (int w = 0; w < kWarps; ++w) {
+        const int a = cta0 + w * quota;
+        if (a < before || a >= before + mine) continue;
+        int at = before, s = q0;
+        for (int n; a >= at + (n = records_of(s) * p.hkv); ++s) at += n;
+        s_seq[w] = s;
+        s_start[w] = at;
+      }
+    __syncthreads();
   }
-  __syncthreads();
   // Requests without keys get zeros; lengths outside [0, room] are recorded.
   auto check_requests = [&]() {
     for (int s = blockIdx.x * kWarps + warp; s < p.n_seqs; s += warps) {
@@ -445,23 +463,22 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
           reinterpret_cast<uint4*>(p.out)[(int64_t)s * p.hkv * p.G * D / 8 + i] = make_uint4(0, 0, 0, 0);
     }
   };
-  if (cta0 >= all) {
+  if (cta0 >= cta1) {
     check_requests();
     return;
   }
 
   const int blocks = p.page_size / kKv4Block;  // records per page and kv head
-  const int64_t a0 = cta0 + warp * quota, a_end = min(a0 + quota, all);
+  const int a0 = cta0 + warp * quota, a_end = min(a0 + quota, cta1);
   if (a0 < a_end) {
-    int rest = (int)(a_end - a0);  // records still to take
+    int rest = a_end - a0;  // records still to take
     volatile int* abort_flag = &s_abort;
     const uint32_t ring = smem_u32(smem) + warp * kWarpBytes<D, NT> + kSlot * 4;
     Place at;
     at.s = s_seq[warp];
     at.n = records_of(at.s);
-    const uint32_t behind = (uint32_t)(a0 - s_start[warp]);  // in the request: below 2^27 hkv records
-    at.h = (int)(behind / (uint32_t)at.n);
-    at.i = (int)(behind - (uint32_t)at.h * at.n);
+    at.h = (a0 - s_start[warp]) / at.n;
+    at.i = a0 - s_start[warp] - at.h * at.n;
     auto next = [&](Place& x) {
       if (++x.i < x.n) return;
       x.i = 0;
@@ -691,7 +708,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
     s_last[tid] = 0;
     if (reaches(tid)) {
       const SlotInfo& x = info[edge[tid]];
-      const int c0 = (int)(x.p0 / cta_records), c1 = (int)((x.p1 - 1) / cta_records);
+      const int c0 = x.p0 / cta_records, c1 = (x.p1 - 1) / cta_records;
       __threadfence();
       if (atomicAdd(&p.tickets[c0], 1) == c1 - c0) {
         s_last[tid] = 1;
@@ -708,7 +725,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   for (int e = 0; e < 2; ++e) {
     if (!s_last[e]) continue;
     const SlotInfo x = info[edge[e]];
-    const int c0 = (int)(x.p0 / cta_records), parts = (int)((x.p1 - 1) / cta_records) - c0 + 1;
+    const int c0 = x.p0 / cta_records, parts = (x.p1 - 1) / cta_records - c0 + 1;
     auto part_of = [&](int k) -> int { return 2 * (c0 + k) + (k == 0 ? 1 : 0); };
     // weights of the parts, a warp per head: scratch [part][head], then the heads' sums
     for (int head = warp; head < p.G; head += kWarps) {
@@ -779,14 +796,17 @@ template <int D, int NT>
 cudaError_t launch_t(const Kv4DecodeParams& p, int32_t sms, cudaStream_t s) {
   constexpr int kWarps = kWarpsOf<NT>;
   const int64_t most = (int64_t)p.n_seqs * p.hkv * p.width * (p.page_size / kKv4Block);  // records at most
-  const int64_t ctas = (most + kWarps - 1) / kWarps;
+  const int64_t pairs = (int64_t)p.n_seqs * p.hkv;
   if (sms > kMaxCtas) sms = kMaxCtas;
-  const int grid = (int)(ctas < sms ? (ctas > 0 ? ctas : 1) : sms);
+  int64_t grid = (most + kWarps - 1) / kWarps;
+  if (pairs > grid) grid = pairs;
+  if (grid > sms) grid = sms;
+  if (grid < 1) grid = 1;
   const size_t smem = (size_t)kWarps * kWarpBytes<D, NT>;
   static std::atomic<uint64_t> configured{0};
   const cudaError_t e = set_smem_limit_once(kv4_decode_kernel<D, NT>, (int)smem, configured);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_decode_kernel<D, NT>, dim3(grid), dim3(kWarps * 32), smem, s, p);
+  return launch_pdl(kv4_decode_kernel<D, NT>, dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p);
 }
 
 }  // namespace

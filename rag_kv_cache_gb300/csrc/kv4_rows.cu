@@ -70,14 +70,18 @@ struct Step {
   uint32_t bits;
   float scale, inverse;
 };
-// Of a group whose largest magnitude has the bf16 bits `top` (0x7f80 and up: not finite).
+// Of a group whose largest magnitude has the bf16 bits `top` (0x7f80 and up: not finite). top times
+// fp32's 1 / 7 rounds to the same bf16 as the quotient: with top = m 2^e, m an integer of 8 bits, m / 7 is
+// either an integer (a bf16) or at least 1 / 112 away from a midpoint of two bf16s, which are odd
+// multiples of 1 / 16 there (1 / 14 of a last place among subnormals), far above fp32's error.
 __device__ __forceinline__ Step step_of(uint32_t top) {
-  const __nv_bfloat16 scale = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top << 16), 7.0f));
+  const __nv_bfloat16 scale = __float2bfloat16_rn(__uint_as_float(top << 16) * (1.0f / 7.0f));
   const bool finite = top < 0x7f80u;
   Step s;
   s.bits = finite ? (uint32_t)__bfloat16_as_ushort(scale) : 0x7fc0u;
   s.scale = finite ? __bfloat162float(scale) : 0.0f;
-  s.inverse = s.scale > 1e-36f ? __fdiv_rn(1.0f, s.scale) : 0.0f;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inverse) : "f"(s.scale));  // the correction below makes up for its error
+  if (!(s.scale > 1e-36f)) s.inverse = 0.0f;
   return s;
 }
 
