@@ -38,7 +38,9 @@
 //   their half-round distance from item to item.
 // Roles, TMEM columns, register split and bounded waits are those of attention_pp.cu; "round" counts
 // the key tiles of all the CTA's items, and ring stage and parity follow from it. Item descriptions
-// pass from the producer to the other warps through a ring of four. After a wait that gave up
+// pass from the producer to the other warps through a ring of eight: the producer
+// requests item i + 7's keys only once both tiles' scores of item i + 5 are formed, for which the softmax
+// warps are through with item i + 3. After a wait that gave up
 // (abort flag) every warp still walks through the rounds of the current item, without work, and the
 // producer ends the list, so no named barrier is left short.
 #include <cuda.h>
@@ -58,7 +60,7 @@ constexpr int kBM = 128;      // rows per query tile
 constexpr int kTiles = 2;     // query tiles per item
 constexpr int kBN = kTileKeys;  // keys per key tile
 constexpr int kStages = 2;    // depth of the K and of the V ring
-constexpr int kItems = 4;     // depth of the item ring
+constexpr int kItems = 8;     // depth of the item ring
 constexpr uint32_t kOutWarp = 32 * 128;  // output staging of one softmax warp
 constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 128;
@@ -90,7 +92,7 @@ struct Item {
 
 // First key that is searched for values that are not finite: the first that some row of the item does
 // not see is t0 + 1, and the search goes by 32 keys.
-__device__ __forceinline__ int hidden_from(const Item& x) { return (x.t0 + 1) / 32 * 32; }
+__device__ __forceinline__ int hidden_from(int t0) { return (t0 + 1) / 32 * 32; }
 
 struct Bars {
   uint64_t q_full[kTiles];
@@ -117,6 +119,15 @@ struct PromptParams {
   float scale_log2;
   int32_t* err;
 };
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+      "[%7];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ void named_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
@@ -312,8 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
-  // The it-th item of this CTA; n_kv = 0 at the end (and, never expected, if it does not come).
-  auto item_at = [&](int it) -> Item {
+  // Key tiles of the it-th item of this CTA, which lies in items[it % kItems]; 0 at the end (and, never
+  // expected, if it does not come).
+  auto item_at = [&](int it) -> int {
     const uint32_t bar = smem_u32(&bars.item[it % kItems]);
     bool there = mbar_test(bar, (it / kItems) & 1);
     if (!there) {
@@ -322,10 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((n & 7u) == 0 && global_timer() - t0 > kItemLimitNs) break;
     }
     there = __all_sync(0xffffffffu, there);
-    if (there) return items[it % kItems];
+    if (there) return items[it % kItems].n_kv;
     *abort_flag = 1;
     record_error(p.err, kErrTimeout, 40);
-    return Item{0, 0, 0, 0, 0, 0};
+    return 0;
   };
 
   if (warp >= kTiles * (kSoftmaxThreads / 32)) {
@@ -342,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       order.start(p, lane);
       int rounds = 0;  // rounds of the items before
       int nk = 0;      // K tiles requested, by round
-      int nq[kTiles] = {0, 0};  // query tiles requested
       // The first item is the block's own; each further one is that of a block which has not started,
       // claimed when the K tiles of the item before have been requested.
       int idx = blockIdx.x, claims = 0;
@@ -370,27 +381,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               return false;
             const uint32_t kb = smem_u32(&bars.k_full[st]);
             mbar_expect_tx(kb, kKVBytes);
-#pragma unroll
-            for (int b = 0; b < kBoxes; ++b)
-              tma_load_3d(sK0 + st * kKVBytes + b * kKVBox, &tm_k, kb, b * 64, x.g, x.row0 + j * kBN);
+            tma_load_4d(sK0 + st * kKVBytes, &tm_k, kb, 0, x.row0 + j * kBN, 0, x.g);
             nk = r + 1;
             return true;
           };
-          bool ok = n > 0 && load_k(0);
-          // Query tile i: its buffer is free once S_i of the round before (the last of the item before)
-          // is complete. Rows past the sequence's end are other sequences' (or the fill value).
-          for (int i = 0; i < kTiles && ok; ++i) {
-            const int r = rounds - 1;
-            ok = r < 0 || mbar_wait_inl(smem_u32(&bars.s_full[i][r % kStages]), (r / kStages) & 1, abort_flag, p.err, 42);
-            if (!ok) break;
-            const uint32_t qb = smem_u32(&bars.q_full[i]);
-            mbar_expect_tx(qb, kQBytes);
-#pragma unroll
-            for (int b = 0; b < kBoxes; ++b)
-              tma_load_4d(sQ + i * kQBytes + b * kQBox, &tm_q, qb, b * 64, 0, x.g, x.row0 + x.t0 + i * p.tq);
-            ++nq[i];
-          }
-          for (int j = 1; j < n && ok; ++j) ok = load_k(j);
+          bool ok = true;
+          for (int j = 0; j < n && ok; ++j) ok = load_k(j);
         }
         __syncwarp();
         if (end) break;
@@ -412,35 +408,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Before the CTA can exit, every copy issued must have landed (also after an abort).
       if (lane == 0) {
-        for (int i = 0; i < kTiles; ++i)
-          if (nq[i] > 0) mbar_wait_inl(smem_u32(&bars.q_full[i]), (nq[i] - 1) & 1, abort_flag, p.err, 56, false);
         for (int r = nk < kStages ? 0 : nk - kStages; r < nk; ++r)
           mbar_wait_inl(smem_u32(&bars.k_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 57, false);
       }
     } else if (warp == kWarpProducerV) {
-      int rounds = 0, nv = 0;
+      int rounds = 0, nv = 0, nq = 0;  // V tiles, query tiles requested
       bool ok = true;
       for (int it = 0;; ++it) {
-        const Item x = item_at(it);
-        if (x.n_kv == 0) break;
+        const int n_kv = item_at(it);
+        if (n_kv == 0) break;
         if (lane == 0) {
-          for (int j = 0; j < x.n_kv && ok; ++j) {
+          const int row0 = items[it % kItems].row0, t0 = items[it % kItems].t0, g = items[it % kItems].g;
+          auto load_v = [&](int j) {
             const int r = rounds + j, st = r % kStages;
             // V of round r - 2 held this stage: free once P_1 V of that round (after P_0 V) is complete
             ok = r < kStages ||
                  mbar_wait_inl(smem_u32(&bars.o_done[1][st]), ((r / kStages) - 1) & 1, abort_flag, p.err, 43);
-            if (!ok) break;
+            if (!ok) return;
             const uint32_t vb = smem_u32(&bars.v_full[st]);
             mbar_expect_tx(vb, kKVBytes);
-#pragma unroll
-            for (int b = 0; b < kBoxes; ++b)
-              tma_load_3d(sV0 + st * kKVBytes + b * kKVBox, &tm_v, vb, b * 64, x.g, x.row0 + j * kBN);
+            tma_load_4d(sV0 + st * kKVBytes, &tm_v, vb, 0, row0 + j * kBN, 0, g);
             nv = r + 1;
+          };
+          if (it > 0) load_v(0);  // (its stage is free before the query tiles' buffers are)
+          // Query tile i: its buffer is free once S_i of the round before (the last of the item before)
+          // is complete. Rows past the sequence's end are other sequences' (or the fill value).
+          for (int i = 0; i < kTiles && ok; ++i) {
+            const int r = rounds - 1;
+            ok = r < 0 || mbar_wait_inl(smem_u32(&bars.s_full[i][r % kStages]), (r / kStages) & 1, abort_flag, p.err, 42);
+            if (!ok) break;
+            const uint32_t qb = smem_u32(&bars.q_full[i]);
+            mbar_expect_tx(qb, kQBytes);
+            tma_load_5d(sQ + i * kQBytes, &tm_q, qb, 0, 0, row0 + t0 + i * p.tq, 0, g);
+            ++nq;
           }
+          for (int j = it > 0 ? 1 : 0; j < n_kv && ok; ++j) load_v(j);
         }
         __syncwarp();
-        rounds += x.n_kv;
+        rounds += n_kv;
       }
+      // Before the CTA can exit, every copy issued must have landed (also after an abort).
+      if (lane == 0)
+        for (int i = 0; i < kTiles; ++i) {
+          const int n = (nq + 1 - i) / kTiles;  // tiles i requested
+          if (n > 0) mbar_wait_inl(smem_u32(&bars.q_full[i]), (n - 1) & 1, abort_flag, p.err, 56, false);
+        }
       if (lane == 0)
         for (int r = nv < kStages ? 0 : nv - kStages; r < nv; ++r)
           mbar_wait_inl(smem_u32(&bars.v_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 58, false);
@@ -454,22 +466,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       int rounds = 0;
       bool ok = true;
       for (int it = 0;; ++it) {
-        const Item x = item_at(it);
-        if (x.n_kv == 0) break;
-        for (int j = 0; j < x.n_kv; ++j) {
+        const int n_kv = item_at(it);
+        if (n_kv == 0) break;
+        const int hidden = hidden_from(items[it % kItems].t0), first_edge = items[it % kItems].t0 + 1;
+        for (int j = 0; j < n_kv; ++j) {
           const int r = rounds + j, st = r % kStages;
           ok = ok && spin_all(smem_u32(&bars.v_full[st]), (r / kStages) & 1, 47);
           // a tile with a key that the item's first row does not see
-          if (ok && (j + 1) * kBN > x.t0 + 1 &&
-              zero_not_finite<kBoxes>(sV0 + st * kKVBytes, max(hidden_from(x) - j * kBN, 0), lane) && lane == 0)
+          if (ok && (j + 1) * kBN > first_edge &&
+              zero_not_finite<kBoxes>(sV0 + st * kKVBytes, max(hidden - j * kBN, 0), lane) && lane == 0)
             items[it % kItems].fixed = 1;
-          ok = ok && (j + 1 >= x.n_kv ||
+          ok = ok && (j + 1 >= n_kv ||
                       spin_all(smem_u32(&bars.k_full[(r + 1) % kStages]), ((r + 1) / kStages) & 1, 48));
           if (lane == 0) s_round_ok[r & 1] = ok ? 1 : 0;
           __syncwarp();  // bar.sync is warp-aligned: reach it converged
           named_sync(kBarTile0, 192);
         }
-        rounds += x.n_kv;
+        rounds += n_kv;
       }
     } else if (warp == kWarpMma) {
       constexpr uint32_t idesc_s = idesc_bf16(kBM, kBN, false);
@@ -505,25 +518,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                            mbar_spin_inl(smem_u32(&bars.k_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 47);
         return __all_sync(0xffffffffu, there);
       };
+      // An item's first S_i, once per item: as a loop, which leaves the registers to the rounds' products.
+      auto first_s = [&](int i, int r) {
+        tc_fence_after();
+        if (elect_one()) {
+          const int st = r % kStages;
+#pragma unroll 1
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(tmem + (uint32_t)(i * kBN), sdesc(sQ + i * kQBytes + (ks / 4) * kQBox + ks % 4 * 32, 16, 1024),
+                   sdesc(sK0 + st * kKVBytes + (ks / 4) * kKVBox + ks % 4 * 32, 16, 1024), idesc_s, ks > 0 ? 1u : 0u);
+          tc_commit(smem_u32(&bars.s_full[i][st]));
+        }
+        __syncwarp();
+      };
       int rounds = 0;
-      Item x = item_at(0);
+      int n_kv = item_at(0);
       bool ok = true;
-      if (x.n_kv > 0) {
-#pragma unroll
+      if (n_kv > 0) {
+#pragma unroll 1
         for (int i = 0; i < kTiles; ++i) {
           ok = ok && inputs(i, 0, 0);
-          if (ok) {
-            tc_fence_after();
-            if (elect_one()) issue_s(i, 0);
-            __syncwarp();
-          }
+          if (ok) first_s(i, 0);
         }
       }
-      for (int it = 0; x.n_kv > 0; ++it) {
-        Item next{0, 0, 0, 0, 0, 0};
-        for (int j = 0; j < x.n_kv; ++j) {
+      for (int it = 0; n_kv > 0; ++it) {
+        int next = 0;
+        for (int j = 0; j < n_kv; ++j) {
           const int r = rounds + j;
-          const bool last = j + 1 == x.n_kv;
+          const bool last = j + 1 == n_kv;
           // Tile i's P is in TMEM; this round's V and the item's next K are loaded (the waiter meets
           // tile 0's barrier). After the item's last P V come the next item's first scores, as soon as
           // its query tile is there: its softmax then finds them when it is through with its output.
@@ -547,17 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (last) {
               if (i == 0) next = item_at(it + 1);
-              if (next.n_kv > 0) ok = ok && inputs(i, it + 1, r + 1);
-              if (ok && next.n_kv > 0) {
-                tc_fence_after();
-                if (elect_one()) issue_s(i, r + 1);
-                __syncwarp();
-              }
+              if (next > 0) ok = ok && inputs(i, it + 1, r + 1);
+              if (ok && next > 0) first_s(i, r + 1);
             }
           }
         }
-        rounds += x.n_kv;
-        x = next;
+        rounds += n_kv;
+        n_kv = next;
       }
       // All tensor-core work issued by this CTA completes before TMEM is freed.
       if (elect_one()) tc_commit(smem_u32(&bars.drain));
@@ -579,12 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int rounds = 0;
     bool ok = true;
     for (int it = 0;; ++it) {
-      const Item x = item_at(it);
-      if (x.n_kv == 0) break;
+      const int n_kv = item_at(it);
+      if (n_kv == 0) break;
       // Position of this thread's row in the sequence; rows past its end repeat the last one and are
       // never stored.
-      const int tok = x.t0 + ti * p.tq + (row >> p.lg);
-      const int my_pos = min(tok, x.len - 1);
+      const int my_pos = min(items[it % kItems].t0 + ti * p.tq + (row >> p.lg), items[it % kItems].len - 1);
       float m_ref = -INFINITY, l = 0.0f;  // reference max (log2 units) that O_ti and l are scaled to
       auto wait_o = [&](int r, int site) -> bool {
         const bool w =
@@ -682,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // Every softmax warp syncs once per key tile on its tile's named barrier, also after a failed
       // wait (then without work), so every round of the issuer and the waiter completes.
-      for (int j = 0; j < x.n_kv; ++j) {
+      for (int j = 0; j < n_kv; ++j) {
         if (ok) ok = tile(j);
         tc_fence_before();
         __syncwarp();
@@ -691,13 +708,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           named_sync(kBarTile1, 160);
       }
-      rounds += x.n_kv;
+      rounds += n_kv;
       if (ok) ok = wait_o(rounds - 1, 54 + ti);
       // Epilogue: out = O_ti / l, each thread its row.
       if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
         tc_fence_after();
         const float inv = 1.0f / l;
-        const bool fixed = items[it % kItems].fixed != 0;
+        const Item x = items[it % kItems];
+        const bool fixed = x.fixed != 0;
         const uint32_t stage = sOut + (uint32_t)warp * kOutWarp;
         const int tokens = x.len - x.t0 - ti * p.tq;  // of this tile that are in the sequence (may be <= 0 or many)
         const bool whole = tokens >= ((warp % 4) * 32 + 32) >> p.lg;  // every row of this warp is
@@ -713,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld(o0);
           tmem_wait_ld(o1);
           if (fixed) {  // the values that were set to 0, of the keys that this row does see
-            for (int key = hidden_from(x); key <= my_pos; ++key) {
+            for (int key = hidden_from(x.t0); key <= my_pos; ++key) {
               const uint8_t* src = p.v + (((int64_t)(x.row0 + key) * p.hkv + x.g) * D + c0) * 2;
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
@@ -743,8 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-              asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(&tm_o),
-                           "r"(c0), "r"(0), "r"(x.g), "r"(x.row0 + x.t0 + ti * p.tq + (((warp % 4) * 32) >> p.lg)), "r"(stage)
+              asm volatile("cp.async.bulk.tensor.5d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4, %5}], [%6];" ::"l"(&tm_o),
+                           "r"(0), "r"(0), "r"(x.row0 + x.t0 + ti * p.tq + (((warp % 4) * 32) >> p.lg)), "r"(c0 / 64), "r"(x.g), "r"(stage)
                            : "memory");
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
@@ -800,15 +818,17 @@ cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const i
   if (regs * kThreads < kTiles * kSoftmaxThreads * kSoftmaxRegs + kSoftmaxThreads * kOtherRegs)
     return cudaErrorNotSupported;
   CUtensorMap tq_map, tk_map, tv_map, to_map;
-  const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)group, (cuuint64_t)hkv, (cuuint64_t)n_rows};
-  const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)group * D * 2, (cuuint64_t)hq * D * 2};
-  const cuuint32_t qb[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)tq};
-  const cuuint32_t ob[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)(32 / group)};  // the rows of a softmax warp
-  const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)hkv, (cuuint64_t)n_rows};
-  const cuuint64_t ks[2] = {(cuuint64_t)D * 2, (cuuint64_t)hkv * D * 2};
-  const cuuint32_t kbx[3] = {64, 1, (cuuint32_t)kBN};
-  if (!encode_map(&tq_map, q, 4, qd, qs, qb) || !encode_map(&tk_map, k, 3, kd, ks, kbx) ||
-      !encode_map(&tv_map, v, 3, kd, ks, kbx) || !encode_map(&to_map, out, 4, qd, qs, ob))
+  // Columns in blocks of 64 (128 bytes, the swizzle's span) as a dimension of their own, so that one copy
+  // brings a tile's blocks one behind the other: [64, heads of g, tokens, block, g] and [64, keys, block, g].
+  const cuuint64_t qd[5] = {64, (cuuint64_t)group, (cuuint64_t)n_rows, D / 64, (cuuint64_t)hkv};
+  const cuuint64_t qs[4] = {(cuuint64_t)D * 2, (cuuint64_t)hq * D * 2, 128, (cuuint64_t)group * D * 2};
+  const cuuint32_t qb[5] = {64, (cuuint32_t)group, (cuuint32_t)tq, D / 64, 1};
+  const cuuint32_t ob[5] = {64, (cuuint32_t)group, (cuuint32_t)(32 / group), 1, 1};  // the rows of a softmax warp
+  const cuuint64_t kd[4] = {64, (cuuint64_t)n_rows, D / 64, (cuuint64_t)hkv};
+  const cuuint64_t ks[3] = {(cuuint64_t)hkv * D * 2, 128, (cuuint64_t)D * 2};
+  const cuuint32_t kbx[4] = {64, (cuuint32_t)kBN, D / 64, 1};
+  if (!encode_map(&tq_map, q, 5, qd, qs, qb) || !encode_map(&tk_map, k, 4, kd, ks, kbx) ||
+      !encode_map(&tv_map, v, 4, kd, ks, kbx) || !encode_map(&to_map, out, 5, qd, qs, ob))
     return cudaErrorInvalidValue;
   PromptParams p;
   p.v = static_cast<const uint8_t*>(v);
