@@ -2,14 +2,15 @@
 //
 // Store: for each kv head and group of 32 dims of a K or V row x,
 //   scale = bf16(max|x| / 7),  code = round-half-even(x / scale) in -7 .. 7,
-// with the quotient in IEEE fp32: x and scale have 8 significant bits, so the fp32 quotient lies on a
-// half exactly when the real one does, and the codes are those of exact arithmetic. A group that
+// the codes of exact arithmetic (x and scale have 8 significant bits, which keeps the quotients that are not
+// halves away from them). A group that
 // holds a NaN or an infinity gets a NaN scale and stands for NaN throughout; a group of zeros has
-// scale 0 and codes 0. Load writes bf16(scale * code), the product exact in fp32.
+// scale 0 and codes 0. Load writes bf16(scale * code), rounded once.
 //
 // Both are bound by HBM: a (token, kv head) is 4 D bytes of bf16 K and V and 18/16 D bytes of cache.
 // Eight dims per lane (one 16-byte access of the bf16 row), four lanes per group: the group's maximum
 // is two shuffles.
+#include "attn_common.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4_layout.cuh"
@@ -18,7 +19,8 @@ namespace cb {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int32_t kRunRows = 1024;
+constexpr int kRunThreads = 64, kRunBlocks = 10;  // whole records: threads per block, blocks per SM at least
+constexpr int32_t kRunRows = 4096;
 
 struct Kv4RowParams {
   const int32_t* slots;
@@ -64,63 +66,94 @@ __device__ __forceinline__ Lane<D> lane_of(const Kv4RowParams& p) {
   return x;
 }
 
-// What a group's codes are made with: its scale's bf16 bits, the scale (0: all codes are 0) and its
-// reciprocal (0: the scale is too small for one).
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// What a group's codes are made with: its scale's bf16 bits and the scale's reciprocal (0: the scale is 0, too
+// small for one, or not finite).
 struct Step {
   uint32_t bits;
-  float scale, inverse;
+  float inverse;
 };
 // Of a group whose largest magnitude has the bf16 bits `top` (0x7f80 and up: not finite). top times
 // fp32's 1 / 7 rounds to the same bf16 as the quotient: with top = m 2^e, m an integer of 8 bits, m / 7 is
 // either an integer (a bf16) or at least 1 / 112 away from a midpoint of two bf16s, which are odd
 // multiples of 1 / 16 there (1 / 14 of a last place among subnormals), far above fp32's error.
 __device__ __forceinline__ Step step_of(uint32_t top) {
-  const __nv_bfloat16 scale = __float2bfloat16_rn(__uint_as_float(top << 16) * (1.0f / 7.0f));
-  const bool finite = top < 0x7f80u;
+  const float seventh = __uint_as_float(top << 16) * (1.0f / 7.0f);
+  const __nv_bfloat16 scale = __float2bfloat16_rn(seventh);
   Step s;
-  s.bits = finite ? (uint32_t)__bfloat16_as_ushort(scale) : 0x7fc0u;
-  s.scale = finite ? __bfloat162float(scale) : 0.0f;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inverse) : "f"(s.scale));  // the correction below makes up for its error
-  if (!(s.scale > 1e-36f)) s.inverse = 0.0f;
+  s.bits = top < 0x7f80u ? (uint32_t)__bfloat16_as_ushort(scale) : 0x7fc0u;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.inverse) : "f"(__bfloat162float(scale)));  // within 2^-22 of it
+  if (!(seventh > 1e-36f && seventh < 1e38f)) s.inverse = 0.0f;
   return s;
 }
 
-// (code + 8) << at of x. The quotient q = x / scale needs its ties exact: a product with the reciprocal
-// and one Newton correction (the remainder x - q scale is exact in an fma) give the quotient wherever
-// fp32 holds it, which it does on every half; elsewhere it is at least 2^-9 away from one. A division per
-// value took three times as long as the kernel's loads and stores. Adding 1.5 * 2^23 + 8 rounds to the
-// integer (ties to even) and leaves code + 8 in the low bits; |code| <= 7 since the scale is within 2^-9
-// of max|x| / 7. Scales near the subnormal range take the division and a clamp.
-__device__ __forceinline__ uint32_t nibble(float x, const Step& s, int at) {
-  const float q = x * s.inverse;
-  const float y = fmaf(fmaf(-q, s.scale, x), s.inverse, q);
-  return (__float_as_uint(y + 12582920.0f) & 15u) << at;
+// The codes (+ 8) of two values x and y of a group, as the low bits of the halves of the result, with the
+// fp32 bits of 1.5 * 2^23 above them. The quotient q = x / scale needs its ties exact. Both have 8
+// significant bits, so q is a half or at least 2^-9 away from one: rounded to multiples of 2^-10 (an
+// addition of 1.5 * 2^13) the product with the reciprocal, |q| 2^-21 off at most, gives a half where q is
+// one and stays on q's side of it elsewhere. The second sum is exact up to its rounding to an
+// integer, ties to even. |code| <= 7 since the scale is within 2^-8 of max|x| / 7. A division per value
+// took three times as long as the kernel's loads and stores.
+constexpr float kSnap = 12288.0f, kWhole = 12582912.0f;
+constexpr uint32_t kWholeBits = 0x4b400000u;
+__device__ __forceinline__ uint64_t codes2(uint64_t xy, uint64_t inverse2) {
+  return f2_add(f2_fma(xy, inverse2, f2_pack(kSnap, kSnap)), f2_pack(kWhole + 8.0f - kSnap, kWhole + 8.0f - kSnap));
 }
-__device__ __noinline__ uint32_t small_nibble(float x, float scale) {
-  const float c = scale > 0.0f ? rintf(__fdiv_rn(x, scale)) : 0.0f;
-  return (uint32_t)((int)fminf(fmaxf(c, -7.0f), 7.0f) + 8);
-}
-
-// Word of 8 values of one group, value i at bits at[i] (compile-time positions).
-template <typename At>
-__device__ __forceinline__ uint32_t nibbles8(const float (&f)[8], const Step& s, At at) {
+// Pairs of codes as nibbles: the code of value i, shifted to at(i) (a compile-time position), summed; the bits
+// above each code add up to a constant.
+template <int N, typename At>
+__device__ __forceinline__ uint32_t nibbles(const uint32_t (&x)[N], const Step& s, At at) {
+  const uint64_t inverse2 = f2_pack(s.inverse, s.inverse);
   uint32_t word = 0;
-  if (s.inverse != 0.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) word |= nibble(f[i], s, at(i));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) word |= small_nibble(f[i], s.scale) << at(i);
+  for (int i = 0; i < N; ++i) {
+    float a, b;
+    f2_unpack(codes2(f2_pack(lo16(x[i]), hi16(x[i])), inverse2), a, b);
+    word += ((__float_as_uint(a) - kWholeBits) << at(2 * i)) + ((__float_as_uint(b) - kWholeBits) << at(2 * i + 1));
   }
   return word;
 }
+// The same of a group whose scale has no reciprocal in fp32: zeros, subnormal steps (a division each) and groups
+// that are not finite (codes 0).
+template <int N, typename At>
+__device__ __forceinline__ uint32_t odd_nibbles(const uint32_t (&x)[N], uint32_t bits, At at) {
+  const float scale = __uint_as_float(bits << 16);
+  uint32_t word = 0;
+#pragma unroll 1
+  for (int i = 0; i < 2 * N; ++i) {
+    const float v = i % 2 ? hi16(x[i / 2]) : lo16(x[i / 2]);
+    const float c = scale > 0.0f ? rintf(__fdiv_rn(v, scale)) : 0.0f;
+    word |= (uint32_t)((int)fminf(fmaxf(c, -7.0f), 7.0f) + 8) << at(i);
+  }
+  return word;
+}
+__device__ __noinline__ uint32_t odd_k(uint4 x, uint32_t bits) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  return odd_nibbles(w, bits, [](int e) { return 4 * (e / 2) + 16 * (e % 2); });
+}
+__device__ __noinline__ uint32_t odd_v(uint2 x, uint32_t bits) {
+  const uint32_t w[2] = {x.x, x.y};
+  return odd_nibbles(w, bits, [](int e) { return 4 * e; });
+}
+// 8 values of a K row, values e and e + 1 in the halves; 4 of a V row, one behind the other.
+__device__ __forceinline__ uint32_t k_word(const uint4& x, const Step& s) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  return s.inverse != 0.0f ? nibbles(w, s, [](int e) { return 4 * (e / 2) + 16 * (e % 2); }) : odd_k(x, s.bits);
+}
+__device__ __forceinline__ uint32_t v_word(const uint2& x, const Step& s) {
+  const uint32_t w[2] = {x.x, x.y};
+  return s.inverse != 0.0f ? nibbles(w, s, [](int e) { return 4 * e; }) : odd_v(x, s.bits);
+}
 
-// One work item of a converged warp.
+// One work item of a converged warp: its values, and what becomes of them.
 template <int D>
-__device__ __forceinline__ void store_row(const uint8_t* k, const uint8_t* v, uint8_t* cache, const Kv4RowParams& p,
-                                          const Lane<D>& x) {
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (x.slot >= 0) raw = ld_stream((x.kv ? v : k) + ((x.row * p.hkv + x.h) * D + x.l * 8) * 2);
+__device__ __forceinline__ uint4 row_values(const uint8_t* k, const uint8_t* v, const Kv4RowParams& p, const Lane<D>& x) {
+  return x.slot >= 0 ? ld_stream((x.kv ? v : k) + ((x.row * p.hkv + x.h) * D + x.l * 8) * 2) : make_uint4(0, 0, 0, 0);
+}
+template <int D>
+__device__ __forceinline__ void store_row(const uint4& raw, uint8_t* cache, const Kv4RowParams& p, const Lane<D>& x) {
   // the group's largest magnitude as bf16 bits (ordered like the magnitudes; 0x7f80 and up: not finite)
   uint32_t top = 0;
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -130,53 +163,50 @@ __device__ __forceinline__ void store_row(const uint8_t* k, const uint8_t* v, ui
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   if (x.slot < 0) return;
   const Step step = step_of(top);
-  float f[8];
-  unpack8(raw, f);
   constexpr int NG = Kv4<D>::kGroups;
   const int g = x.l / 4, c = x.l % 4, t = x.slot % kKv4Block;
   uint8_t* rec = cache + record_offset<D>(x.slot, x.h, p.hkv, p.page_size);
   if (x.kv == 0) {
-    *reinterpret_cast<uint32_t*>(rec + t * (D / 2) + (c * NG + g) * 4) =
-        nibbles8(f, step, [](int e) { return 4 * (e / 2) + 16 * (e % 2); });
+    *reinterpret_cast<uint32_t*>(rec + t * (D / 2) + (c * NG + g) * 4) = k_word(raw, step);
   } else {
     uint8_t* vb = rec + Kv4<D>::kV + (t / 8) * Kv4<D>::kPlane + (t % 8 / 2) * (4 * NG) + g * 4 + (t % 2) * 2;
-    const uint32_t word = nibbles8(f, step, [](int e) { return 4 * e; });  // r = 2 c in the low half, 2 c + 1 in the high
-    *reinterpret_cast<uint16_t*>(vb + 2 * c * (16 * NG)) = (uint16_t)word;
-    *reinterpret_cast<uint16_t*>(vb + (2 * c + 1) * (16 * NG)) = (uint16_t)(word >> 16);
+    *reinterpret_cast<uint16_t*>(vb + 2 * c * (16 * NG)) = (uint16_t)v_word(make_uint2(raw.x, raw.y), step);
+    *reinterpret_cast<uint16_t*>(vb + (2 * c + 1) * (16 * NG)) = (uint16_t)v_word(make_uint2(raw.z, raw.w), step);
   }
   if (c == 0)
     *reinterpret_cast<uint16_t*>(rec + Kv4<D>::kScales + t * (4 * NG) + x.kv * (2 * NG) + g * 2) = (uint16_t)step.bits;
 }
 
+// A lane's 8 codes of a stored row (two values of K in the halves, four of V one behind the other; + 8) and their
+// scale's bits.
+struct Codes {
+  uint32_t word, scale;
+};
 template <int D>
-__device__ __forceinline__ void load_row(uint8_t* k, uint8_t* v, const uint8_t* cache, const Kv4RowParams& p,
-                                         const Lane<D>& x) {
-  if (x.slot < 0) return;
+__device__ __forceinline__ Codes row_codes(const uint8_t* cache, const Kv4RowParams& p, const Lane<D>& x) {
+  Codes r{0, 0};
+  if (x.slot < 0) return r;
   constexpr int NG = Kv4<D>::kGroups;
   const int g = x.l / 4, c = x.l % 4, t = x.slot % kKv4Block;
   const uint8_t* rec = cache + record_offset<D>(x.slot, x.h, p.hkv, p.page_size);
-  const float step = __uint_as_float(
-      (uint32_t)*reinterpret_cast<const uint16_t*>(rec + Kv4<D>::kScales + t * (4 * NG) + x.kv * (2 * NG) + g * 2) << 16);
-  int nib[8];
+  r.scale = __ldg(reinterpret_cast<const uint16_t*>(rec + Kv4<D>::kScales + t * (4 * NG) + x.kv * (2 * NG) + g * 2));
   if (x.kv == 0) {
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(rec + t * (D / 2) + (c * NG + g) * 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      nib[2 * i] = word >> (4 * i) & 15;
-      nib[2 * i + 1] = word >> (16 + 4 * i) & 15;
-    }
+    r.word = __ldg(reinterpret_cast<const uint32_t*>(rec + t * (D / 2) + (c * NG + g) * 4));
   } else {
     const uint8_t* vb = rec + Kv4<D>::kV + (t / 8) * Kv4<D>::kPlane + (t % 8 / 2) * (4 * NG) + g * 4 + (t % 2) * 2;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t half = *reinterpret_cast<const uint16_t*>(vb + (2 * c + q) * (16 * NG));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) nib[4 * q + i] = half >> (4 * i) & 15;
-    }
+    r.word = __ldg(reinterpret_cast<const uint16_t*>(vb + 2 * c * (16 * NG))) |
+             (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(vb + (2 * c + 1) * (16 * NG))) << 16;
   }
+  return r;
+}
+template <int D>
+__device__ __forceinline__ void load_row(uint8_t* k, uint8_t* v, const Codes& r, const Kv4RowParams& p, const Lane<D>& x) {
+  if (x.slot < 0) return;
+  const float step = __uint_as_float(r.scale << 16);
   float f[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = step * (float)(nib[e] - 8);
+  for (int e = 0; e < 8; ++e)
+    f[e] = step * (float)((int)(r.word >> (x.kv == 0 ? 4 * (e / 2) + 16 * (e % 2) : 4 * e) & 15) - 8);
   st_stream((x.kv ? v : k) + ((x.row * p.hkv + x.h) * D + x.l * 8) * 2, pack8(f));
 }
 
@@ -186,9 +216,9 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(uint8_t* k, uint8_t*
   pdl_wait();
   const Lane<D> x = lane_of<D>(p);
   if (STORE)
-    store_row<D>(k, v, cache, p, x);
+    store_row<D>(row_values<D>(k, v, p, x), cache, p, x);
   else
-    load_row<D>(k, v, cache, p, x);
+    load_row<D>(k, v, row_codes<D>(cache, p, x), p, x);
 }
 
 // ---- whole records ---------------------------------------------------------------------------------
@@ -197,9 +227,11 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(uint8_t* k, uint8_t*
 // record (slots 16 m .. 16 m + 15). A warp takes one kv head of such a run with the decode kernel's lane
 // layout: 16-byte accesses of the record, 64-byte pieces of the bf16 rows, groups reduced by shuffles,
 // and two values per instruction where the arithmetic is exact in bf16 (a nibble widened to
-// 128 + nibble; minus 136; times the scale, one rounding). Row by row the V nibbles are 2-byte accesses
-// in eight sectors per row: 32,768 rows of 8 heads took 85 us to store and 66 us to load, in runs 48 and 28
-// (their bytes at the copy rate: 26).
+// 128 + nibble; minus 136; times the scale, one rounding). A warp asks for all its bytes first (the store's 8 KB
+// of K and V: 64 registers a lane) and blocks are of two warps: of eight, they hold their registers until the last
+// warp is through, and the store takes 40 us instead of 31; with registers for 12 blocks an SM, 36.
+// 32,768 rows of 8 heads of 128 dims (172 MB, 25.7 us at the copy rate): store 31 us, load 27; row by row, where
+// V's nibbles are 2-byte accesses in eight sectors per row, 70 and 59.
 
 // What a warp finds in the 16 rows from `row0` on.
 struct Window {
@@ -230,15 +262,17 @@ __device__ __forceinline__ Window look_at(const Kv4RowParams& p, int64_t row0, i
   return w;
 }
 
+__device__ __forceinline__ uint2 ld_stream2(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {  // of two bf16 pairs' magnitudes, by half
   return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
 }
 __device__ __forceinline__ uint32_t shuffled_max2(uint32_t x, int d) {
   return __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, d));
 }
-
-__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 template <int NG>
 __device__ __forceinline__ void put_words(uint8_t* p, const uint32_t (&w)[NG]) {
@@ -266,21 +300,31 @@ __device__ __forceinline__ void store_record(const uint8_t* k, const uint8_t* v,
   const int r = lane / 4, c = lane % 4;
   const int64_t pitch = (int64_t)hkv * D * 2, base = row * pitch + (int64_t)h * D * 2;
   // K: tokens r and r + 8, 8 dims of each group per lane
+  uint4 kx[2][NG];
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) kx[half][g] = ld_stream(k + base + (r + 8 * half) * pitch + g * 64 + c * 16);
+  // V: tokens 8 half + 2 c and + 1, dims 32 g + 4 r .. of each group per lane
+  uint2 vx[2][2][NG];
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        vx[half][o][g] = ld_stream2(v + base + (8 * half + 2 * c + o) * pitch + g * 64 + r * 8);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    uint4 x[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) x[g] = ld_stream(k + base + (r + 8 * half) * pitch + g * 64 + c * 16);
     uint32_t word[NG], bits[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      uint32_t m = __vmaxu2(abs_max2(x[g].x, x[g].y), abs_max2(x[g].z, x[g].w));
+      const uint4& x = kx[half][g];
+      uint32_t m = __vmaxu2(abs_max2(x.x, x.y), abs_max2(x.z, x.w));
       m = shuffled_max2(shuffled_max2(m, 1), 2);
       const Step step = step_of(max(m & 0xffffu, m >> 16));
       bits[g] = step.bits;
-      float f[8];
-      unpack8(x[g], f);
-      word[g] = nibbles8(f, step, [](int e) { return 4 * (e / 2) + 16 * (e % 2); });
+      word[g] = k_word(x, step);
     }
     put_words<NG>(rec + half * Kv4<D>::kPlane + lane * (4 * NG), word);
     if (c == 0)
@@ -288,32 +332,20 @@ __device__ __forceinline__ void store_record(const uint8_t* k, const uint8_t* v,
       for (int g = 0; g < NG; g += 2)
         *reinterpret_cast<uint32_t*>(rec + Kv4<D>::kScales + (r + 8 * half) * (4 * NG) + g * 2) = bits[g] | bits[g + 1] << 16;
   }
-  // V: tokens 8 half + 2 c and + 1, dims 32 g + 4 r .. of each group per lane
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    uint2 x[2][NG];
-#pragma unroll
-    for (int o = 0; o < 2; ++o)
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-        x[o][g] = *reinterpret_cast<const uint2*>(v + base + (8 * half + 2 * c + o) * pitch + g * 64 + r * 8);
     uint32_t word[NG], bits[2][NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       // both tokens' maxima in one register
-      const uint32_t m0 = abs_max2(x[0][g].x, x[0][g].y), m1 = abs_max2(x[1][g].x, x[1][g].y);
-      uint32_t m = max(m0 & 0xffffu, m0 >> 16) | max(m1 & 0xffffu, m1 >> 16) << 16;
+      const uint2 &x0 = vx[half][0][g], &x1 = vx[half][1][g];
+      const uint32_t m0 = abs_max2(x0.x, x0.y), m1 = abs_max2(x1.x, x1.y);
+      uint32_t m = __vmaxu2(__byte_perm(m0, m1, 0x5410), __byte_perm(m0, m1, 0x7632));
       m = shuffled_max2(shuffled_max2(shuffled_max2(m, 4), 8), 16);
-      word[g] = 0;
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const Step step = step_of(o ? m >> 16 : m & 0xffffu);
-        bits[o][g] = step.bits;
-        const float f[4] = {lo16(x[o][g].x), hi16(x[o][g].x), lo16(x[o][g].y), hi16(x[o][g].y)};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          word[g] |= step.inverse != 0.0f ? nibble(f[e], step, 16 * o + 4 * e) : small_nibble(f[e], step.scale) << (16 * o + 4 * e);
-      }
+      const Step s0 = step_of(m & 0xffffu), s1 = step_of(m >> 16);
+      bits[0][g] = s0.bits;
+      bits[1][g] = s1.bits;
+      word[g] = v_word(x0, s0) + (v_word(x1, s1) << 16);
     }
     put_words<NG>(rec + Kv4<D>::kV + half * Kv4<D>::kPlane + lane * (4 * NG), word);
     if (r == 0)
@@ -378,11 +410,12 @@ __device__ __forceinline__ void load_record(uint8_t* k, uint8_t* v, const uint8_
 // A warp per 16 rows and kv head: the whole record that begins in them, then the rows of no whole
 // record one by one (half a warp for K, half for V).
 template <int D, bool STORE>
-__global__ void __launch_bounds__(kThreads) kv4_runs_kernel(uint8_t* k, uint8_t* v, uint8_t* cache, const Kv4RowParams p) {
+__global__ void __launch_bounds__(kRunThreads, kRunBlocks)
+    kv4_runs_kernel(uint8_t* k, uint8_t* v, uint8_t* cache, const Kv4RowParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x % 32;
-  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32;
+  const int64_t unit = ((int64_t)blockIdx.x * kRunThreads + threadIdx.x) / 32;
   const int64_t row0 = unit / p.hkv * kKv4Block;
   const int h = (int)(unit % p.hkv);
   if (row0 >= p.n) return;
@@ -395,32 +428,50 @@ __global__ void __launch_bounds__(kThreads) kv4_runs_kernel(uint8_t* k, uint8_t*
     else
       load_record<D>(k, v, rec, row, h, p.hkv, lane);
   }
-  for (uint32_t rest = w.rest; rest != 0; rest &= rest - 1) {
-    Lane<D> x;
-    x.row = row0 + __ffs(rest) - 1;
-    x.h = h;
-    x.kv = lane / 16;
-    x.l = lane % 16;
-    x.slot = x.l < D / 8 ? p.slots[x.row] : -1;
-    if (x.slot >= p.n_slots) {
-      if (h == 0 && lane == 0) record_error(p.err, kErrIndex, (int32_t)x.row);
-      x.slot = -1;
+  for (uint32_t rest = w.rest; rest != 0;) {  // four rows at a time, so that their reads overlap
+    constexpr int kRows = 4;
+    Lane<D> x[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      x[i].row = row0 + (rest != 0 ? __ffs(rest) - 1 : 0);
+      x[i].h = h;
+      x[i].kv = lane / 16;
+      x[i].l = lane % 16;
+      x[i].slot = rest != 0 && x[i].l < D / 8 ? p.slots[x[i].row] : -1;
+      if (x[i].slot >= p.n_slots) {
+        if (h == 0 && lane == 0) record_error(p.err, kErrIndex, (int32_t)x[i].row);
+        x[i].slot = -1;
+      }
+      rest &= rest - 1;  // (stays 0)
     }
-    if (STORE)
-      store_row<D>(k, v, cache, p, x);
-    else
-      load_row<D>(k, v, cache, p, x);
+    if constexpr (STORE) {
+      uint4 raw[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) raw[i] = row_values<D>(k, v, p, x[i]);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) store_row<D>(raw[i], cache, p, x[i]);
+    } else {
+      Codes r[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) r[i] = row_codes<D>(cache, p, x[i]);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) load_row<D>(k, v, r[i], p, x[i]);
+    }
   }
 }
 
 template <int D, bool STORE>
 cudaError_t launch_rows(void* k, void* v, void* cache, const Kv4RowParams& p, cudaStream_t s) {
-  // By runs from kRunRows rows on, where there are warps enough to take 16 rows each; row by row below.
+  // By runs from kRunRows rows on, where there are warps enough to take 16 rows each; row by row below. Whole
+  // pages of 8 heads of 128 dims, by runs against row by row, store and load: 2,048 rows 6.2 and 5.1 against
+  // 5.2 and 4.6 us, 4,096 rows 6.6 and 4.6 against 9.2 and 7.8. Scattered slots cost the other way: 4,096
+  // rows 13.8 and 13.4 against 9.2 and 7.9, 32,768 rows 72 and 66 against 71 and 65.
   const bool runs = p.n >= kRunRows;
   const int64_t lanes = runs ? ((int64_t)p.n + kKv4Block - 1) / kKv4Block * p.hkv * 32 : (int64_t)p.n * p.hkv * 2 * (D / 8);
-  const int64_t blocks = (lanes + kThreads - 1) / kThreads;
+  const int threads = runs ? kRunThreads : kThreads;
+  const int64_t blocks = (lanes + threads - 1) / threads;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  return launch_pdl(runs ? kv4_runs_kernel<D, STORE> : kv4_rows_kernel<D, STORE>, dim3((unsigned)blocks), dim3(kThreads), 0, s,
+  return launch_pdl(runs ? kv4_runs_kernel<D, STORE> : kv4_rows_kernel<D, STORE>, dim3((unsigned)blocks), dim3(threads), 0, s,
                     static_cast<uint8_t*>(k), static_cast<uint8_t*>(v), static_cast<uint8_t*>(cache), p);
 }
 

@@ -176,7 +176,7 @@ def test_store_and_load(cb, hkv, d, n, page):
 
 @pytest.mark.parametrize("hkv,d,page", [(2, 64, 16), (3, 128, 48), (8, 128, 256)])
 def test_store_and_load_by_runs(cb, hkv, d, page):
-    # calls of 1,024 rows and more: whole records at any offset of the rows, broken runs, runs that begin
+    # calls of 4,096 rows and more: whole records at any offset of the rows, broken runs, runs that begin
     # or end inside a record, padding, rows that a quantiser meets seldom, the last record of the cache
     rng = np.random.default_rng(hkv + d + page)
     plan = _plan(cb, hkv, hkv, d)
@@ -192,11 +192,13 @@ def test_store_and_load_by_runs(cb, hkv, d, page):
     rest = np.arange(-(-at // 16) * 16, total - 16)
     pieces.append(rng.permutation(rest)[:150])
     pieces.append(np.arange(total - 16, total))
+    pieces.insert(4, np.full(1000, -1))  # padding among the rows and behind them
+    pieces.append(np.full(2100, -1))
     slots = np.concatenate(pieces)
-    slots[130], slots[300] = slots[131], -1
-    slots[131] = -1  # (a slot that was there is named once)
+    slots[1130], slots[1300] = slots[1131], -1
+    slots[1131] = -1  # (a slot that was there is named once)
     n = len(slots)
-    assert n >= 1024 and len(set(slots[slots >= 0])) == (slots >= 0).sum()
+    assert n >= 4096 and len(set(slots[slots >= 0])) == (slots >= 0).sum()
     k, v = _bits(rng, n, hkv, d), _bits(rng, n, hkv, d, scale=9.0)
     for x in (k, v):
         x[3], x[40], x[41, 0] = 0, f32_to_bf16_bits((rng.standard_normal((hkv, d)) * 1e-39).astype(np.float32)), 0x8000
@@ -217,10 +219,37 @@ def test_store_and_load_by_runs(cb, hkv, d, page):
         assert np.array_equal(np.isnan(g), np.isnan(w))
         assert np.array_equal(g[~np.isnan(w)], w[~np.isnan(w)])
     # one slot past the cache in a long call
-    slots[700] = total
+    slots[1700] = total
     cb.cb_kv4_load(plan, cache, page, _i32(slots), ok, ov)
     with pytest.raises(cb.CacheBlendError):
         plan.check()
+    plan.close()
+
+
+@pytest.mark.parametrize("padding", [0, 3100])
+def test_store_every_quotient(cb, padding):
+    """Every bf16 mantissa of a group's largest magnitude with every mantissa of its other values, ties among
+    them, from subnormal steps to the largest: scales and codes are those of exact arithmetic."""
+    plan, hkv, d = _plan(cb, 8, 8, 128), 8, 128
+    rng = np.random.default_rng(5)
+    exps = [0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 20, 60, 100, 126, 127, 128, 140, 200, 240, 252, 253, 254]
+    tops = (np.array(exps)[:, None] * 128 + np.arange(128)).astype(np.int64)  # bf16 bits
+    others = tops[:, :, None, None] // 128 * 128 - 128 * np.arange(5)[:, None] + np.arange(128)
+    others = np.minimum(np.maximum(others, 0), tops[:, :, None, None]).reshape(len(exps), 128, 640)
+    groups = np.broadcast_to(tops[:, :, None, None], (len(exps), 128, 21, 32)).copy()
+    groups[..., 1:] = np.concatenate((others, others[..., :11]), -1).reshape(len(exps), 128, 21, 31)
+    groups = rng.permuted(groups, axis=-1) | (rng.integers(0, 2, groups.shape) << 15)
+    kv = groups.astype(np.uint16).reshape(1050, 2, hkv, d)
+    cache = torch.zeros(66, hkv, cb.cb_kv4_page_bytes(plan, 16), dtype=torch.uint8, device="cuda")
+    k, v = (bf16_tensor(np.concatenate((kv[:, i], np.zeros((padding, hkv, d), np.uint16)))) for i in range(2))
+    slots = _i32(np.concatenate((np.arange(1050), np.full(padding, -1))))
+    cb.cb_kv4_store(plan, k, v, slots, cache, 16)
+    kk, vv = torch.empty_like(k), torch.empty_like(v)
+    cb.cb_kv4_load(plan, cache, 16, slots, kk, vv)
+    for i, got in enumerate((kk, vv)):
+        want = serving._to_bf16(serving.dequantise(*serving.quantise(bf16_bits_to_f64(kv[:, i]))))
+        assert np.array_equal(_f64(got)[:1050], want)
+    plan.check()
     plan.close()
 
 
