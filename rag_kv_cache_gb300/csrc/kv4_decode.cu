@@ -4,22 +4,24 @@
 //
 // with k and v = code * (scale of the row's group of 32 dims).
 //
-// Bound by HBM: a (key, kv head) is 18/16 D bytes. At 6.7 TB/s an SM receives 23 bytes per cycle, so
-// it has about 6 cycles per (key, kv head) at D = 128. Widening the codes to bf16 in shared memory for
-// tcgen05 would write and read 512 bytes per key there, 8 cycles at 128 bytes per cycle, more than the
-// bound; so the codes are widened in registers, straight into the operand layout of mma.sync, which
-// costs 7 instructions per 8 codes:
-//   (word >> 4 i & 0x000f000f) | 0x43004300 = two bf16 of value 128 + nibble = 136 + code (exact),
-// so that no subtraction or conversion is needed. The offset 136 leaves through the accumulators:
+// Floor: a (key, kv head) is 18/16 D bytes. At 6.7 TB/s an SM receives 23 bytes per cycle, so it has
+// about 6 cycles per (key, kv head) at D = 128. Widening the codes in shared memory for tcgen05 would write
+// and read 512 bytes per key there, 8 cycles at 128 bytes per cycle, more than the floor; so the codes
+// are widened in registers, straight into the operand layout of mma.sync:
+//   K   word & 0x000f000f and word & 0x00f000f0 are pairs of fp16 of value nibble * 2^-24 and * 2^-20
+//       (subnormals, exact): 5 instructions per 8 codes;
+//   V   (word >> 4 i & 0x000f000f) | 0x43004300 is a pair of bf16 of value 128 + nibble = 136 + code
+//       (exact): 7 per 8 codes. In bf16, since the weights times V's scales need its range.
+// No subtraction or conversion is needed. The offsets leave through the accumulators:
 //   scores   S^T = K Q^T (M = 16 keys, N = 8 heads, inner = dims), one accumulator per group of 32
-//            dims, times the key's scale, added to one more product of the keys' scales with
-//            -136 * (sum of q over the group), the latter as three bf16 terms;
+//            dims, times the key's scale, added to one more product of the keys' scales with -8 * (sum
+//            of q over the group), the latter as three bf16 terms; q is scaled into fp16's range;
 //   output   O^T += V^T P^T (M = 16 dims, N = 8 heads, inner = 16 keys) with P_g = bf16(p * scale of
 //            the key's group g), and one more product per group with ones in place of V, which sums
 //            the same rounded P_g: O - 136 * that sum is the result, so the offset adds no rounding.
 // P (keys x heads) becomes the second product's operand by an 8 x 8 transpose between lanes
-// (movmatrix). Products are bf16 x bf16 in fp32; softmax statistics and sums are fp32; rounding
-// p * scale to bf16 (2^-9 relative) is the one rounding before the output's.
+// (movmatrix). Sums of products, softmax statistics and sums are fp32; rounding p * scale to bf16 (2^-9
+// relative) is the one rounding before the output's.
 //
 // Work split: the records (16 keys of one request and kv head) of the whole batch, in the order
 // request, kv head, position, are dealt to the warps of one wave of CTAs in equal contiguous runs, so
@@ -27,7 +29,22 @@
 // inside a (request, kv head) leaves a partial result (max, sum, unnormalised O): the CTA merges those
 // of its warps in shared memory, and a (request, kv head) that spans CTAs is merged by the last of
 // them to finish, over partials in the plan's scratch (a ticket per CTA that begins one). The merge
-// order is fixed by position, so results do not change from run to run.
+// order is fixed by position, so results do not change from run to run. Small batches of short requests
+// take a CTA per (request, kv head), which spares that last merge: 4 requests of up to
+// 545 keys and 2 kv heads of 64 dims 6.8 against 11.2 us.
+//
+// Feeding: each warp asks for its own records by bulk copies into a ring of its own, five ahead (eight
+// with 8 warps), and waits for them alone; no warp waits for another one until the merge.
+//
+// Measured (8 kv heads of 128 dims): 64 requests of up to 8,449 keys, 64 query heads (308 MB, 46 us at
+// the copy rate) 87 us, 0.53 of that rate; one request of 32,897 keys, 32 query heads (38 MB, 5.7 us) 24 us,
+// of which about 8 us is fixed: the batch's prefix sums, the first copies, the merges. What bounds the
+// batch is the instructions: about 360 per record and warp, 175 of them on the integer pipe, which takes one
+// every other cycle, so 350 cycles per record for a scheduler, 0.9 of the bytes' time; three warps per
+// scheduler overlap them with the products and the exponentials to 1.6 times that. With 10 and 14 warps
+// (the latter with fewer registers) the batch took 101 and 102 us. Records two to a copy (92 us then), Q in
+// shared memory to make room for 16 warps (105), shifts as multiplications (96), and K in e4m3 with Q in two
+// terms (102; 3 instructions per 8 codes, but such a product costs more than two in fp16) were not faster.
 #include "common.cuh"
 #include "kernels.h"
 #include "attn_common.cuh"
@@ -41,7 +58,8 @@ constexpr float kHigh = 256.0f;           // a weight above it moves the referen
 constexpr float kLow = -3e38f;            // reference of a head that has seen nothing
 constexpr int kAlone = 6;                 // records per warp up to which a CTA takes a (request, kv head) alone
 constexpr int kMaxCtas = 160;             // of a launch (one wave: one per SM)
-constexpr float kOffset = 136.0f;         // value of a widened nibble of code 0
+constexpr float kOffset = 136.0f;         // value of a widened nibble of V for code 0
+constexpr float kKOffset = 8.0f / 16777216.0f;  // value of a nibble of K for code 0
 constexpr uint32_t kNibbles = 0x000f000fu;
 constexpr uint32_t kBias = 0x43004300u;   // two bf16 of 128: the last place is 1
 constexpr uint32_t kOnes = 0x3f803f80u;   // two bf16 of 1
@@ -51,7 +69,7 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 }
 
 struct Masks {
-  uint32_t nibbles, bias, ones;
+  uint32_t nibbles, higher, bias, ones;
 };
 
 struct Kv4DecodeParams {
@@ -89,6 +107,22 @@ __device__ __forceinline__ void mma_bf16_new(float (&d)[4], uint32_t a0, uint32_
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// The same in fp16.
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -141,34 +175,63 @@ __device__ __forceinline__ void reset(State<D, NT>& st) {
   }
 }
 
-// Query operand of one (request, kv head): pairs of dims 32 g + 8 c + .. of head 8 t + r; and the operand
-// of the correction, whose inner dimension is (term, group): -136 * (sum of the group's dims) in three
-// bf16 terms, which hold all 24 bits of it.
+// Query operand of one (request, kv head): pairs of dims 32 g + 8 c + .. of head 8 t + r in fp16. Each head's
+// q is scaled by a power of two that puts its largest magnitude into [2^14, 2^15), and every second pair by 2^-4
+// more (its codes lie four bits higher): exact down to 2^-27 of the largest, within 2^-35 of it below. `scale` takes
+// the power, and the 2^24 of the codes' value, out of the scores (NaN for a head that is not finite). `fix`
+// is the operand of the correction, whose inner dimension is (term, group): -8 * 2^-24 * (sum of the group's
+// dims) in three bf16 terms, which hold all 24 bits of it.
 template <int D, int NT>
 struct Query {
   static constexpr int NG = Kv4<D>::kGroups;
   uint32_t b[NT][NG][4];
   uint32_t fix[NT][2];
+  float scale[NT][2];  // of heads 8 t + 2 c and + 1, in log2 units
 };
 
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 .. 127
+
 template <int D, int NT>
-__device__ __forceinline__ void load_query(Query<D, NT>& qf, const uint8_t* q, int G, int lane) {
+__device__ __forceinline__ void load_query(Query<D, NT>& qf, const uint8_t* q, int G, float scale_log2, int lane) {
   constexpr int NG = Kv4<D>::kGroups;
   const int r = lane / 4, c = lane % 4;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
+    uint4 x[NG];
+    uint32_t top = 0;  // the head's largest magnitude, as bf16 bits
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      x[g] = make_uint4(0, 0, 0, 0);
+      if (8 * t + r < G) x[g] = __ldg(reinterpret_cast<const uint4*>(q + ((8 * t + r) * D + 32 * g + 8 * c) * 2));
+      const uint32_t w[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int up = 141 - max((int)(top >> 7), 1);  // the power: -114 .. 140, in two factors below
+    const float up0 = power_of_2(up >> 1), up1 = power_of_2(up - (up >> 1));
+    float scale = scale_log2 * power_of_2((24 - up) >> 1) * power_of_2(24 - up - ((24 - up) >> 1));
+    if (top >= 0x7f80u) scale = __uint_as_float(0x7fc00000u);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) qf.scale[t][e] = __shfl_sync(0xffffffffu, scale, 4 * (2 * c + e));
     float off[4] = {0.f, 0.f, 0.f, 0.f};  // of head 8 t + r
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (8 * t + r < G) x = __ldg(reinterpret_cast<const uint4*>(q + ((8 * t + r) * D + 32 * g + 8 * c) * 2));
-      qf.b[t][g][0] = x.x, qf.b[t][g][1] = x.y, qf.b[t][g][2] = x.z, qf.b[t][g][3] = x.w;
       float f[8];
-      unpack8(x, f);
+      unpack8(x[g], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = f[i] * up0 * up1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float low = i % 2 ? 0.0625f : 1.0f;
+        const __half2 h = __floats2half2_rn(f[2 * i] * low, f[2 * i + 1] * low);
+        qf.b[t][g][i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
       float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      off[g] = -kOffset * sum;
+      off[g] = -kKOffset * sum;
     }
     // inner index 2 c + {0, 1} (and + 8): term c / 2 (and 2, for c < 2), groups 2 (c % 2) + {0, 1}
     const float x0 = c % 2 ? off[2] : off[0], x1 = c % 2 ? off[3] : off[1];
@@ -187,8 +250,8 @@ __device__ __forceinline__ void load_query(Query<D, NT>& qf, const uint8_t* q, i
 
 // One record of up to 16 keys, the first `valid` of them in the request.
 template <int D, int NT, bool WHOLE>
-__device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, uint32_t rec, int valid, float scale_log2,
-                                     const Masks& mk, int lane) {
+__device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, uint32_t rec, int valid, const Masks& mk,
+                                     int lane) {
   constexpr int NG = Kv4<D>::kGroups;
   const int r = lane / 4;
   uint32_t sc[2][NG];  // scales of tokens r and r + 8: [K NG, V NG] bf16
@@ -209,7 +272,7 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
   for (int h = 0; h < 2; ++h) load_vec<NG>(w[h], rec + h * Kv4<D>::kPlane + lane * (4 * NG));
   float s[NT][4];
   {
-    // the offset's part of the scores first: -136 sum_g scale_g(key) (sum of q over g)
+    // the offset's part of the scores first: -8 sum_g scale_g(key) (sum of q over g)
     const bool odd = lane & 1;
     const uint32_t k0 = NG == 2 ? (odd ? 0u : sc[0][0]) : (odd ? sc[0][NG / 2 - 1] : sc[0][0]);
     const uint32_t k1 = NG == 2 ? (odd ? 0u : sc[1][0]) : (odd ? sc[1][NG / 2 - 1] : sc[1][0]);
@@ -223,15 +286,14 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
   for (int half = 0; half < 2; ++half)
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      uint32_t x[2], y[2];  // tokens r, r + 8
-      widen(w[0][g], 2 * half, mk, x);
-      widen(w[1][g], 2 * half, mk, y);
+      const uint32_t x = w[0][g] >> (8 * half), y = w[1][g] >> (8 * half);  // tokens r, r + 8
+      const uint32_t x0 = x & mk.nibbles, x1 = x & mk.higher, y0 = y & mk.nibbles, y1 = y & mk.higher;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (half == 0)
-          mma_bf16_new(acc[t][g], x[0], y[0], x[1], y[1], qf.b[t][g][0], qf.b[t][g][1]);
+          mma_f16_new(acc[t][g], x0, y0, x1, y1, qf.b[t][g][0], qf.b[t][g][1]);
         else
-          mma_bf16(acc[t][g], x[0], y[0], x[1], y[1], qf.b[t][g][2], qf.b[t][g][3]);
+          mma_f16(acc[t][g], x0, y0, x1, y1, qf.b[t][g][2], qf.b[t][g][3]);
       }
     }
 #pragma unroll
@@ -261,7 +323,7 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) pr[t][e] = ex2(fmaf(s[t][e], scale_log2, -st.m[t][e % 2]));
+    for (int e = 0; e < 4; ++e) pr[t][e] = ex2(fmaf(s[t][e], qf.scale[t][e % 2], -st.m[t][e % 2]));
     most = fmaxf(max3(most, pr[t][0], pr[t][1]), fmaxf(pr[t][2], pr[t][3]));
   }
   const bool high = most > kHigh;
@@ -274,7 +336,7 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
         float top = fmaxf(s[t][e], s[t][e + 2]);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) * scale_log2;
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) * qf.scale[t][e];
         const bool move = top > st.m[t][e];
         alpha[e] = move ? ex2(st.m[t][e] - top) : 1.0f;  // 0 where the head had nothing
         if (move) st.m[t][e] = top;
@@ -290,7 +352,7 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
         for (int e = 0; e < 4; ++e) st.ones[t][g][e] *= alpha[e % 2];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        pr[t][e] = ex2(fmaf(s[t][e], scale_log2, -st.m[t][e % 2]));
+        pr[t][e] = ex2(fmaf(s[t][e], qf.scale[t][e % 2], -st.m[t][e % 2]));
       }
     }
   }
@@ -549,7 +611,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
     while (rest > 0) {
       const int s = at.s, h = at.h;
       const int count = min(at.n - at.i, rest);
-      load_query<D, NT>(qf, p.q + ((int64_t)s * p.hkv + h) * p.G * D * 2, p.G, lane);
+      load_query<D, NT>(qf, p.q + ((int64_t)s * p.hkv + h) * p.G * D * 2, p.G, p.scale_log2, lane);
       reset(st);
       int keys = len_of(s) - at.i * kKv4Block;  // from the record on
       for (int i = 0; i < count; ++i, keys -= kKv4Block) {
@@ -557,9 +619,9 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
         __syncwarp();
         const uint32_t rec = ring + stage * kRecord;
         if (keys >= kKv4Block && !(bad >> stage & 1))
-          step<D, NT, true>(st, qf, rec, kKv4Block, p.scale_log2, p.masks, lane);
+          step<D, NT, true>(st, qf, rec, kKv4Block, p.masks, lane);
         else  // without its page, a stage holds an earlier record: weight 0
-          step<D, NT, false>(st, qf, rec, bad >> stage & 1 ? 0 : min(keys, kKv4Block), p.scale_log2, p.masks, lane);
+          step<D, NT, false>(st, qf, rec, bad >> stage & 1 ? 0 : min(keys, kKv4Block), p.masks, lane);
         __syncwarp();
         request();  // into the stage just read
         if (++stage == kStages) stage = 0, parity ^= 1;
@@ -828,7 +890,7 @@ cudaError_t launch_kv4_decode(const void* q, const void* cache, int32_t n_pages,
   p.hkv = hkv;
   p.G = hq / hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.masks = Masks{kNibbles, kBias, kOnes};
+  p.masks = Masks{kNibbles, kNibbles << 4, kBias, kOnes};
   p.part_o = ws.part_o;
   p.part_ml = ws.part_ml;
   p.tickets = ws.tickets;

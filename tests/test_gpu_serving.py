@@ -4,8 +4,8 @@ oracle, with the sizes, masks and contents where they can go wrong, and a run of
 Tolerances. Page tables, slots, codes and loaded rows are exact. Attention in 64 bits over the same
 rows, s = sum_j p_j |v_j|: the softmax weights (decode: times V's scale) are rounded to bf16 once,
 2^-8 relative each, so at most 2^-8 s; the output's rounding adds 2^-8 |out|. Scores are fp32 sums:
-of D products |q k| (prompt), or of groups of 32 products of |q| with 136 + code <= 143 and the offset
-136 |q| (decode), each of at most 40 roundings of 2^-23 (the matrix unit truncates); their error e
+of D products |q k| (prompt), or of groups of 32 products of |q| with 8 + code <= 15 and the offset
+8 |q| (decode), each of at most 40 roundings of 2^-23 (the matrix unit truncates); their error e
 changes a weight by a factor within exp(2 e).
 """
 
@@ -325,7 +325,7 @@ def _cache(cb, plan, rng, lens, page, spare=2, kscale=1.0, koffset=0.5):
 
 def _score_error(q, rows_scale, d, scale):
     """Bound of the fp32 error of a decode score (docstring of this file)."""
-    return scale * (d / 32) * 40 * 2.0**-23 * 32 * 143 * np.abs(q).max() * rows_scale
+    return scale * (d / 32) * 40 * 2.0**-23 * 32 * (15 + 8) * np.abs(q).max() * rows_scale
 
 
 def _check_decode(plan, q, out, ks, vs_rows, what, scale=None):
@@ -408,6 +408,42 @@ def test_decode_scores_that_jump_late(cb):
     cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32([n]), out)
     plan.check()
     _check_decode(plan, q, out, [qk], [qv], "late jumps")
+    plan.close()
+
+
+@pytest.mark.parametrize("q_power,spike", [(-100, 1), (100, 1), (0, 2**12), (-130, 2**6), (20, 2**20)])
+def test_decode_queries_far_from_one(cb, q_power, spike):
+    # magnitudes of q from 2^-130 to 2^120 with keys that bring the scores back to the order of one, heads of
+    # one group that lie far apart, and values beside one that is much larger, where K is much smaller
+    rng = np.random.default_rng(abs(q_power) + spike)
+    hq, hkv, d, page, lens = 8, 2, 128, 16, [37, 200]
+    plan = _plan(cb, hq, hkv, d)
+    n_pages = sum(-(-n // page) for n in lens)
+    table = np.full((2, 13), -1)
+    table[0, :3], table[1] = [5, 2, 9], np.setdiff1d(np.arange(n_pages), [5, 2, 9])
+    cache = torch.zeros(n_pages, hkv, cb.cb_kv4_page_bytes(plan, page), dtype=torch.uint8, device="cuda")
+    q, k = rng.standard_normal((2, hq, d)), rng.standard_normal((sum(lens), hkv, d))
+    q[:, :, 64:96] *= spike  # a group of dims: K's scale there is its own
+    k[:, :, 64:96] /= spike
+    q[:, :, 65:96] /= spike  # small values beside a large one: next to nothing
+    q[:, 1::4] *= 2.0**-10
+    q, k = (f32_to_bf16_bits((x * 2.0**p).astype(np.float32)) for x, p in ((q, q_power), (k, -max(q_power, -120))))
+    v = _bits(rng, sum(lens), hkv, d)
+    pos = [np.arange(n) for n in lens]
+    slots = np.concatenate([table[s][p // page] * page + p % page for s, p in enumerate(pos)])
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(slots), cache, page)
+    out = torch.empty(2, hq, d, dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32(lens), out)
+    plan.check()
+    qk, qv = (serving.dequantise(*serving.quantise(bf16_bits_to_f64(x))) for x in (k, v))
+    qf = bf16_bits_to_f64(q)
+    for s, (a, b) in enumerate(((0, 37), (37, 237))):
+        ref, vs = decode_attention(qf[s], qk[a:b], qv[a:b], return_vscale=True)
+        # per (head, group of dims), as in _score_error; q itself is within 2^-35 of its head's largest
+        top = np.abs(qk[a:b]).max(0).reshape(hkv, 4, 32).max(-1) / 7
+        sums = np.abs(qf[s]).reshape(hkv, hq // hkv, 4, 32).max(-1)
+        e = (sums * (32 * (15 + 8) * 40 * 2.0**-23) + 2.0**-35 * 32 * 7 * sums.max(-1, keepdims=True)) * top[:, None]
+        _close(_f64(out[s]), ref, vs, min(d**-0.5 * e.sum(-1).max(), 0.02), f"request {s}")
     plan.close()
 
 
