@@ -33,9 +33,9 @@
 //   registers or staged ones held the warps for 3,000 - 4,000 cycles per item, an SM's store path taking
 //   about 30 bytes per cycle). A warp whose rows pass the sequence's end, which belong to others, stores
 //   those inside itself. The query tiles' buffers stay free for the next item.
-//   Next scores. After an item's last P_i V the issuer forms the next item's first S_i as soon as its
-//   query tile is there, before the other tile's last product, so that the two softmax warpgroups keep
-//   their half-round distance from item to item.
+//   Next scores. Behind an item's last products the issuer forms the next item's first scores, while
+//   the softmax warps write their output. Boxes of 32 columns, two in flight, instead of the output's boxes
+//   of 64 held the warps longer: 306 against 293 us for the 40 prompts.
 // Roles, TMEM columns, register split and bounded waits are those of attention_pp.cu; "round" counts
 // the key tiles of all the CTA's items, and ring stage and parity follow from it. Item descriptions
 // pass from the producer to the other warps through a ring of eight: the producer
@@ -430,19 +430,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(sV0 + st * kKVBytes, &tm_v, vb, 0, row0 + j * kBN, 0, g);
             nv = r + 1;
           };
-          if (it > 0) load_v(0);  // (its stage is free before the query tiles' buffers are)
           // Query tile i: its buffer is free once S_i of the round before (the last of the item before)
           // is complete. Rows past the sequence's end are other sequences' (or the fill value).
-          for (int i = 0; i < kTiles && ok; ++i) {
+          auto load_q = [&](int i) {
             const int r = rounds - 1;
-            ok = r < 0 || mbar_wait_inl(smem_u32(&bars.s_full[i][r % kStages]), (r / kStages) & 1, abort_flag, p.err, 42);
-            if (!ok) break;
+            ok = ok && (r < 0 || mbar_wait_inl(smem_u32(&bars.s_full[i][r % kStages]), (r / kStages) & 1, abort_flag, p.err, 42));
+            if (!ok) return;
             const uint32_t qb = smem_u32(&bars.q_full[i]);
             mbar_expect_tx(qb, kQBytes);
             tma_load_5d(sQ + i * kQBytes, &tm_q, qb, 0, 0, row0 + t0 + i * p.tq, 0, g);
             ++nq;
-          }
-          for (int j = it > 0 ? 1 : 0; j < n_kv && ok; ++j) load_v(j);
+          };
+          // in the order in which the buffers become free
+          load_q(0);
+          if (ok) load_v(0);
+          load_q(1);
+          for (int j = 1; j < n_kv && ok; ++j) load_v(j);
         }
         __syncwarp();
         rounds += n_kv;
@@ -532,23 +535,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       int rounds = 0;
-      int n_kv = item_at(0);
       bool ok = true;
-      if (n_kv > 0) {
+      for (int it = 0;; ++it) {
+        const int n_kv = item_at(it);
+        if (n_kv == 0) break;
+        // Behind the item before's last products: its output takes the softmax warps longer than these scores.
+        // (Tile 0's before tile 1's last product would hold that one up until the query tile is there.)
 #pragma unroll 1
         for (int i = 0; i < kTiles; ++i) {
-          ok = ok && inputs(i, 0, 0);
-          if (ok) first_s(i, 0);
+          ok = ok && inputs(i, it, rounds);
+          if (ok) first_s(i, rounds);
         }
-      }
-      for (int it = 0; n_kv > 0; ++it) {
-        int next = 0;
         for (int j = 0; j < n_kv; ++j) {
           const int r = rounds + j;
           const bool last = j + 1 == n_kv;
           // Tile i's P is in TMEM; this round's V and the item's next K are loaded (the waiter meets
-          // tile 0's barrier). After the item's last P V come the next item's first scores, as soon as
-          // its query tile is there: its softmax then finds them when it is through with its output.
+          // tile 0's barrier).
 #pragma unroll
           for (int i = 0; i < kTiles; ++i) {
             __syncwarp();
@@ -567,15 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
             }
-            if (last) {
-              if (i == 0) next = item_at(it + 1);
-              if (next > 0) ok = ok && inputs(i, it + 1, r + 1);
-              if (ok && next > 0) first_s(i, r + 1);
-            }
           }
         }
         rounds += n_kv;
-        n_kv = next;
       }
       // All tensor-core work issued by this CTA completes before TMEM is freed.
       if (elect_one()) tc_commit(smem_u32(&bars.drain));
@@ -596,9 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)((warp % 4) * 32) << 16);
     int rounds = 0;
     bool ok = true;
-    for (int it = 0;; ++it) {
-      const int n_kv = item_at(it);
-      if (n_kv == 0) break;
+    int n_kv = item_at(0);
+    for (int it = 0; n_kv > 0; ++it) {
       // Position of this thread's row in the sequence; rows past its end repeat the last one and are
       // never stored.
       const int my_pos = min(items[it % kItems].t0 + ti * p.tq + (row >> p.lg), items[it % kItems].len - 1);
@@ -632,9 +627,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int lim = my_pos - j * kBN;  // columns c <= lim are visible to this row
         if (__any_sync(0xffffffffu, lim < kBN - 1)) {  // diagonal tiles only
+          // by 32 columns: only those that a row of the warp does not see (its first row sees the fewest)
+          const int first = __shfl_sync(0xffffffffu, lim, 0);
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            if (c > lim) sv[c] = 0xff800000u;  // -inf
+          for (int c0 = 0; c0 < kBN; c0 += 32) {
+            if (first < c0 + 31)
+#pragma unroll
+              for (int c = c0; c < c0 + 32; ++c)
+                if (c > lim) sv[c] = 0xff800000u;  // -inf
+          }
         }
         // As in attention_pp.cu, tiles run against a reference and take their max only where their P
         // sum shows that the reference is too low. The first tile's reference is the max of its first
@@ -709,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_sync(kBarTile1, 160);
       }
       rounds += n_kv;
+      n_kv = item_at(it + 1);  // while the last product runs
       if (ok) ok = wait_o(rounds - 1, 54 + ti);
       // Epilogue: out = O_ti / l, each thread its row.
       if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
