@@ -416,9 +416,9 @@ cb_status cb_kv4_load(cb_plan* plan, const void* cache, int32_t n_pages, int32_t
  * accumulation; the softmax weights times V's scales are rounded to bf16 before the product.
  * Recorded as CB_ERR_DEVICE_CHECK: a negative length (as 0), one past table_width * P (cut there), a
  * table entry outside [0, n_pages) (its keys are left out). n_seqs * hkv * table_width * P must stay below
- * 2^34 (CB_ERR_UNSUPPORTED). Partial results meet in the plan's
- * scratch: calls of this function on one plan must not overlap on the GPU; order them on one stream,
- * or give each stream its own plan. */
+ * 2^34 (CB_ERR_UNSUPPORTED). out must not be q. Partial results meet in the plan's scratch: calls of
+ * this function on one plan must not overlap on the GPU; order them on one stream, or give each
+ * stream its own plan. */
 cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,
                                   const int32_t* table, int32_t table_width, const int32_t* kv_lens, int32_t n_seqs,
                                   float scale, void* out, void* stream);
@@ -428,12 +428,14 @@ cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cach
  * and k, v [n_rows, hkv, D], and
  *   out[t, h] = sum_{j <= t, same sequence} softmax_j(scale * q[t, h] . k[j, g]) v[j, g],  g = h / (hq/hkv),
  * with q and k RoPE-encoded at their positions. cu_seqlens: device int32 [n_seqs + 1], ascending,
- * within [0, n_rows]; empty sequences are allowed, and rows in no sequence keep their out. Values of
+ * within [0, n_rows], n_seqs at most CB_PROMPT_MAX_SEQS (a block looks through the offsets once per 64
+ * tokens of the longest sequence or so); empty sequences are allowed, and rows in no sequence keep their out. Values of
  * keys that a row does not see (later ones, other sequences') do not reach it, whatever they are.
  * scale <= 0 selects 1/sqrt(D). fp32 accumulation and softmax, bf16 P, bf16 output; tcgen05 (TMEM
  * accumulators) fed by TMA. out must be none of the inputs. Offsets that fall or leave [0, n_rows] are
  * recorded as CB_ERR_DEVICE_CHECK (clipped, a falling pair read as empty). No scratch: calls on one
  * plan may overlap. A bounded wait that gives up records CB_ERR_TIMEOUT. */
+#define CB_PROMPT_MAX_SEQS 16384
 cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
                               int32_t n_seqs, int32_t n_rows, float scale, void* out, void* stream);
 

@@ -622,6 +622,7 @@ cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cach
   if (table_width > 0) CB_TRY(need_ptr(table, "table"));
   CB_TRY(need_ptr(kv_lens, "kv_lens"));
   CB_TRY(need_tensor(out, "out"));
+  if (out == q) return fail(CB_ERR_INVALID_ARG, "out must not be q");
   CB_TRY(check_device(plan));
   if (!(scale > 0.0f)) scale = 1.0f / std::sqrt((float)c.head_dim);
   return cuda_status(cb::launch_kv4_decode(q, cache, n_pages, page_size, table, table_width, kv_lens, n_seqs, c.hq,
@@ -636,6 +637,7 @@ cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const
   CB_TRY(check_plan(plan));
   const auto& c = plan->cfg;
   if (n_seqs < 0 || n_rows < 0) return fail(CB_ERR_INVALID_ARG, "negative size");
+  if (n_seqs > CB_PROMPT_MAX_SEQS) return fail(CB_ERR_UNSUPPORTED, "n_seqs above 16384");
   if (n_seqs == 0 || n_rows == 0) return CB_OK;
   if (cb::prompt_items(n_seqs, n_rows, c.hq, c.hkv) > (1 << 30))
     return fail(CB_ERR_INVALID_ARG, "n_rows and n_seqs make more than 2^30 work items");

@@ -20,7 +20,7 @@
 //            the key's group g), and one more product per group with ones in place of V, which sums
 //            the same rounded P_g: O - 136 * that sum is the result, so the offset adds no rounding.
 // P (keys x heads) becomes the second product's operand by an 8 x 8 transpose between lanes
-// (movmatrix). Sums of products, softmax statistics and sums are fp32; rounding p * scale to bf16 (2^-9
+// (movmatrix). Sums of products, softmax statistics and sums are fp32; rounding p * scale to bf16 (2^-8
 // relative) is the one rounding before the output's.
 //
 // Work split: the records (16 keys of one request and kv head) of the whole batch, in the order

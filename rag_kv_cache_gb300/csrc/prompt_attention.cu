@@ -171,6 +171,7 @@ __device__ __forceinline__ int row_at(const PromptParams& p, int s) {
 // sequence and kv head.
 struct Order {
   int level, count, first;  // current level, the sequences that have it, items of the levels above
+  int same, begin;          // they are the same down to this level; the first of them (a multiple of 32 at or before it)
   int s0, before;           // cursor: sequences before s0 hold `before` of them
   int latest;               // last index asked for
 
@@ -181,10 +182,20 @@ struct Order {
     return n > 0 ? (n + per - 1) >> (__ffs(per) - 1) : 0;
   }
   __device__ __forceinline__ void enter(const PromptParams& p, int lane) {
-    int n = 0;
-    for (int s = lane; s < p.n_seqs; s += 32) n += items_of(p, s) > level ? 1 : 0;
+    int n = 0, below = 0, at = p.n_seqs;
+#pragma unroll 4
+    for (int s = lane; s < p.n_seqs; s += 32) {
+      const int items = items_of(p, s);
+      const bool has = items > level;
+      n += has ? 1 : 0;
+      below = max(below, has ? 0 : items);
+      at = min(at, has ? s : p.n_seqs);
+    }
     count = __reduce_add_sync(0xffffffffu, n);
-    s0 = before = 0;
+    same = __reduce_max_sync(0xffffffffu, below);
+    begin = __reduce_min_sync(0xffffffffu, at) / 32 * 32;
+    s0 = begin;
+    before = 0;
   }
   __device__ __forceinline__ void start(const PromptParams& p, int lane) {
     int top = 0;
@@ -200,7 +211,12 @@ struct Order {
     while (level >= 0 && idx - first >= count * p.hkv) {
       first += count * p.hkv;
       --level;
-      if (level >= 0) enter(p, lane);
+      if (level >= same) {
+        s0 = begin;
+        before = 0;
+      } else if (level >= 0) {
+        enter(p, lane);
+      }
     }
     if (level < 0) return false;
     const uint32_t rel = idx - first, nth = rel / (uint32_t)p.hkv;  // 32 bits: a 64-bit division would be a call

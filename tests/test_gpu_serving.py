@@ -763,6 +763,102 @@ def test_calls_on_another_stream(cb):
     plan.close()
 
 
+def test_two_calls_of_one_plan_at_once(cb):
+    # page tables and packed prompts have no scratch: two streams, one plan, many calls in flight
+    rng = np.random.default_rng(42)
+    plan = _plan(cb, 8, 2, 64)
+    jobs = []
+    for lens in ([300, 7, 1000], [64] * 20):
+        n, rows = len(lens), sum(lens)
+        q, k, v = _bits(rng, rows, 8, 64), _bits(rng, rows, 2, 64), _bits(rng, rows, 2, 64)
+        table = np.full((n, 70), -1)
+        free = rng.permutation(200)
+        t = dict(ctx=_i32([0] * n), new=_i32(lens), free=_i32(free), table=_i32(table), cu=_i32(np.zeros(n + 1)), kv=_i32([0] * n),
+                 pos=_i32(np.zeros(rows)), slots=_i32(np.zeros(rows)), to=_i32([0]))
+        jobs.append((lens, free, table, (q, k, v), t, [bf16_tensor(x) for x in (q, k, v)],
+                     torch.empty(rows, 8, 64, dtype=torch.bfloat16, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for lens, free, table, _, t, dev, out, s in jobs:
+            cb.cb_page_tables(plan, t["ctx"], t["new"], 16, t["free"], t["table"], t["cu"], t["kv"], t["pos"], t["slots"], t["to"],
+                              stream=s)
+            cb.cb_prompt_attention(plan, *dev, t["cu"], out, stream=s)
+    torch.cuda.synchronize()
+    plan.check()
+    for lens, free, table, (q, k, v), t, _, out, _ in jobs:
+        want = serving.page_tables([0] * len(lens), lens, 16, free, table, sum(lens))
+        for w, name in zip(want, ("table", "cu", "kv", "pos", "slots", "to")):
+            assert np.array_equal(t[name].cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), name
+        _check_prompt(q, k, v, np.cumsum([0] + lens), out, "two at once")
+    plan.close()
+
+
+def test_decodes_of_two_plans_at_once_and_shared_pages(cb):
+    rng = np.random.default_rng(43)
+    jobs = []
+    for lens in ([5000, 40], [900] * 6):
+        plan = _plan(cb, 8, 2, 128)
+        cache, table, ks, vs = _cache(cb, plan, rng, lens, 16)
+        # a further request that shares the first one's pages, cut inside a record
+        table, lens = np.concatenate((table, table[:1])), lens + [lens[0] - 21]
+        ks, vs = ks + [ks[0][:lens[-1]]], vs + [vs[0][:lens[-1]]]
+        q = _bits(rng, len(lens), 8, 128)
+        jobs.append((plan, cache, _i32(table), _i32(lens), q, bf16_tensor(q), ks, vs,
+                     torch.empty(len(lens), 8, 128, dtype=torch.bfloat16, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for plan, cache, table, lens, _, q, _, _, out, s in jobs:
+            cb.cb_kv4_decode_attention(plan, q, cache, 16, table, lens, out, stream=s)
+    torch.cuda.synchronize()
+    for plan, _, _, _, q, _, ks, vs, out, _ in jobs:
+        plan.check()
+        _check_decode(plan, q, out, ks, vs, "two plans")
+        plan.close()
+
+
+def test_captured_prompts_of_other_lengths(cb):
+    # one graph, captured for 2,000 rows and 8 sequences, replayed for batches that leave most of them empty
+    rng = np.random.default_rng(44)
+    plan = _plan(cb, 8, 2, 128)
+    rows = 2000
+    q, k, v = _bits(rng, rows, 8, 128), _bits(rng, rows, 2, 128), _bits(rng, rows, 2, 128)
+    dev, cu = [bf16_tensor(x) for x in (q, k, v)], _i32(np.zeros(9))
+    out = torch.full((rows, 8, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    cb.cb_prompt_attention(plan, *dev, cu, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cb.cb_prompt_attention(plan, *dev, cu, out)
+    for lens in ([0] * 8, [1] + [0] * 7, [500, 0, 1, 64, 65, 0, 1300, 70], [0] * 7 + [2000], [3, 0, 0, 0, 0, 0, 0, 130]):
+        cu.copy_(_i32(np.cumsum([0] + lens)))
+        out.fill_(9.0)
+        graph.replay()
+        plan.check()
+        _check_prompt(q, k, v, np.cumsum([0] + lens), out, f"lengths {lens}")
+        assert (_f64(out)[sum(lens):] == 9.0).all()
+    plan.close()
+
+
+@pytest.mark.parametrize("n", [40, 4400])
+def test_store_of_one_slot_named_twice(cb, n):
+    # what that slot holds is open; every other slot is as it would be
+    rng = np.random.default_rng(45)
+    plan, page = _plan(cb, 2, 2, 64), 16
+    slots = np.arange(n)
+    slots[32:40], slots[17] = np.arange(8), 3
+    k, v = _bits(rng, n, 2, 64), _bits(rng, n, 2, 64)
+    cache = torch.zeros(n // page + 1, 2, cb.cb_kv4_page_bytes(plan, page), dtype=torch.uint8, device="cuda")
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(slots), cache, page)
+    ok, ov = (torch.empty((n, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cb.cb_kv4_load(plan, cache, page, _i32(slots), ok, ov)
+    plan.check()
+    once = slots > 7
+    for x, got in ((k, ok), (v, ov)):
+        want = serving._to_bf16(serving.dequantise(*serving.quantise(bf16_bits_to_f64(x))))
+        assert np.array_equal(_f64(got)[once], want[once])
+    plan.close()
+
+
 def test_binding_refuses_wrong_tensors(cb):
     plan = _plan(cb, 8, 2, 128)
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731

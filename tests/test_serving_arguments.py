@@ -84,7 +84,7 @@ def test_rows_refusals(lib, plan):
 
 
 def test_decode_refusals(lib, plan):
-    def call(plan_=plan, q=P, cache=P, pages=2, page=16, table=P, width=4, lens=P, n=3, out=P):
+    def call(plan_=plan, q=P, cache=P, pages=2, page=16, table=P, width=4, lens=P, n=3, out=P + 4096):
         return lib.cb_kv4_decode_attention(plan_, q, cache, pages, page, table, width, lens, n, 0.0, out, None)
 
     _refused(lib, call(plan_=None), "plan")
@@ -94,10 +94,13 @@ def test_decode_refusals(lib, plan):
         _refused(lib, call(**{name: -1}), "negative")
     _refused(lib, call(n=1 << 30), "2^31")
     _refused(lib, call(width=1 << 28), "2^31")
+    _refused(lib, call(n=1 << 11, width=1 << 18), "2^34", 2)  # 2^11 requests of 2 heads and 2^22 keys
+    _refused(lib, call(n=1 << 20, width=1 << 10, page=1024), "2^34", 2)
     for name, said in (("q", "q"), ("cache", "cache"), ("table", "table"), ("lens", "kv_lens"), ("out", "out")):
         _refused(lib, call(**{name: None}), said)
     for name in ("q", "cache", "out"):
         _refused(lib, call(**{name: P + 4}), "16-byte")
+    _refused(lib, call(q=P + 4096, out=P + 4096), "out must not be q")
     assert call(n=0, q=None) == 0
 
 
@@ -108,7 +111,7 @@ def test_prompt_refusals(lib, plan):
     _refused(lib, call(plan_=None), "plan")
     for name in ("n", "rows"):
         _refused(lib, call(**{name: -1}), "negative")
-    _refused(lib, call(n=1 << 30), "work items")
+    _refused(lib, call(n=16385), "n_seqs", 2)
     for name, said in (("q", "q"), ("k", "k"), ("v", "v"), ("cu", "cu_seqlens"), ("out", "out")):
         _refused(lib, call(**{name: None}), said)
     for name in ("q", "k", "v", "out"):
