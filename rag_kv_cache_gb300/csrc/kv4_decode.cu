@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   static_assert(kStages * kRecord >= kSlot * 4 && kSlot % 4 == 0, "a partial result fits a warp's ring");
   extern __shared__ __align__(16) uint8_t smem[];  // [kWarps] first partial result, ring
   __shared__ uint64_t full[kWarps][kStages];
-  __shared__ int s_abort;
+  __shared__ int s_abort[kWarps];
   constexpr int kSlots = 2 * kWarps, kHeads = 8 * NT;
   __shared__ SlotInfo info[kSlots];
   __shared__ float2 s_ml[kSlots][kHeads];     // (reference, sum) of the partial results
@@ -446,74 +446,95 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   __shared__ int s_last[2];
 
   pdl_launch_dependents();
-  if (threadIdx.x < kWarps * kStages) mbar_init(smem_u32(&full[0][threadIdx.x]), 1);
-  if (threadIdx.x == 0) s_abort = 0;
-  if (threadIdx.x < kSlots) info[threadIdx.x].pair = -1;
+  // What a warp uses until the merge is its own.
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  if (lane < kStages) mbar_init(smem_u32(&full[warp][lane]), 1);
+  if (lane < 2) info[2 * warp + lane].pair = -1;
+  if (lane == 0) s_abort[warp] = 0;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
   pdl_wait();
   auto slot_at = [&](int slot) -> float* {
     return reinterpret_cast<float*>(smem + (slot / 2) * kWarpBytes<D, NT> + (slot % 2) * kSlot * 4);
   };
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int r = lane / 4, c = lane % 4;
   const int32_t room = p.width * p.page_size;  // fits: the host checks
   auto len_of = [&](int s) -> int32_t { return min(max(__ldg(p.lens + s), 0), room); };
   auto records_of = [&](int s) -> int { return (int)(((int64_t)len_of(s) + kKv4Block - 1) / kKv4Block); };
 
   // The batch's records, and where each warp's run of them begins (32 bits hold them: the host checks).
-  const int run_s = (p.n_seqs + kThreads - 1) / kThreads;
-  const int q0 = min(tid * run_s, p.n_seqs), q1 = min(q0 + run_s, p.n_seqs);
-  int mine = 0, longest = 0;
-  for (int s = q0; s < q1; ++s) {
-    const int n = records_of(s);
-    mine += n * p.hkv;
-    longest = max(longest, n);
-  }
   const int warps = gridDim.x * kWarps;
   int quota, cta_records, cta0, cta1;  // records per warp, per CTA, this CTA's first and last
-  if (__syncthreads_and(p.n_seqs * p.hkv <= (int)gridDim.x && longest <= kAlone * kWarps)) {
-    // A small batch of short requests: a CTA for each (request, kv head), so that none is merged over CTAs.
+  int run_seq = 0, run_start = 0;      // the request that this warp's run begins in, that request's first record
+  auto alone = [&](int longest) -> bool { return p.n_seqs * p.hkv <= (int)gridDim.x && longest <= kAlone * kWarps; };
+  // A small batch of short requests: a CTA for each (request, kv head), so that none is merged over CTAs.
+  auto split_alone = [&]() {
     const int s = blockIdx.x / p.hkv, h = blockIdx.x - s * p.hkv;
     const int n = s < p.n_seqs ? records_of(s) : 0;
     quota = (n + kWarps - 1) / kWarps;
     cta_records = n;
     cta0 = h * n;  // counted from the request's first record
     cta1 = cta0 + n;
-    if (lane == 0) s_seq[warp] = s, s_start[warp] = 0;
-    __syncwarp();
-  } else {
-    int up = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, up, d);
-      if (lane >= d) up += x;
-    }
-    if (lane == 31) w_sum[warp] = up;
-    __syncthreads();
-    int sums = lane < kWarps ? w_sum[lane] : 0;
-#pragma unroll
-    for (int d = 1; d < kWarps; d <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, sums, d);
-      if (lane >= d) sums += x;
-    }
-    const int all = __shfl_sync(0xffffffffu, sums, kWarps - 1);
-    const int earlier = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
-    const int before = (warp > 0 ? earlier : 0) + up - mine;
+    run_seq = s;
+  };
+  auto split = [&](int all) {
     quota = (int)(((uint32_t)all + warps - 1) / (uint32_t)warps);
     cta_records = kWarps * quota;
     cta0 = (int)min((int64_t)blockIdx.x * cta_records, (int64_t)all);
     cta1 = (int)min((int64_t)cta0 + cta_records, (int64_t)all);
-    if (before < cta1 && before + mine > cta0)
-      for (int w = 0; w < kWarps; ++w) {
-        const int a = cta0 + w * quota;
-        if (a < before || a >= before + mine) continue;
-        int at = before, s = q0;
-        for (int n; a >= at + (n = records_of(s) * p.hkv); ++s) at += n;
-        s_seq[w] = s;
-        s_start[w] = at;
-      }
-    __syncthreads();
+  };
+  auto scan_up = [&](int x) -> int {  // inclusive, over the warp
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    return x;
+  };
+  if (p.n_seqs <= 32) {  // each warp for itself, a request per lane
+    const int n = lane < p.n_seqs ? records_of(lane) : 0;
+    if (alone(__reduce_max_sync(0xffffffffu, n))) {
+      split_alone();
+    } else {
+      const int end = scan_up(n * p.hkv), begin = end - n * p.hkv;
+      split(__shfl_sync(0xffffffffu, end, 31));
+      const int a = cta0 + warp * quota;
+      const uint32_t here = __ballot_sync(0xffffffffu, a >= begin && a < end);
+      run_seq = here ? __ffs(here) - 1 : 0;
+      run_start = __shfl_sync(0xffffffffu, begin, run_seq);
+    }
+  } else {
+    const int run_s = (p.n_seqs + kThreads - 1) / kThreads;
+    const int q0 = min(tid * run_s, p.n_seqs), q1 = min(q0 + run_s, p.n_seqs);
+    int mine = 0, longest = 0;
+    for (int s = q0; s < q1; ++s) {
+      const int n = records_of(s);
+      mine += n * p.hkv;
+      longest = max(longest, n);
+    }
+    const int up = scan_up(mine);
+    if (lane == 31) w_sum[warp] = up;
+    if (__syncthreads_and(alone(longest))) {
+      split_alone();
+    } else {
+      const int sums = scan_up(lane < kWarps ? w_sum[lane] : 0);
+      const int earlier = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+      const int before = (warp > 0 ? earlier : 0) + up - mine;
+      split(__shfl_sync(0xffffffffu, sums, 31));
+      if (before < cta1 && before + mine > cta0)
+        for (int w = 0; w < kWarps; ++w) {
+          const int a = cta0 + w * quota;
+          if (a < before || a >= before + mine) continue;
+          int at = before, s = q0;
+          for (int n; a >= at + (n = records_of(s) * p.hkv); ++s) at += n;
+          s_seq[w] = s;
+          s_start[w] = at;
+        }
+      __syncthreads();
+      run_seq = s_seq[warp];
+      run_start = s_start[warp];
+    }
   }
   // Requests without keys get zeros; lengths outside [0, room] are recorded.
   auto check_requests = [&]() {
@@ -534,13 +555,13 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   const int a0 = cta0 + warp * quota, a_end = min(a0 + quota, cta1);
   if (a0 < a_end) {
     int rest = a_end - a0;  // records still to take
-    volatile int* abort_flag = &s_abort;
+    volatile int* abort_flag = &s_abort[warp];
     const uint32_t ring = smem_u32(smem) + warp * kWarpBytes<D, NT> + kSlot * 4;
     Place at;
-    at.s = s_seq[warp];
+    at.s = run_seq;
     at.n = records_of(at.s);
-    at.h = (a0 - s_start[warp]) / at.n;
-    at.i = a0 - s_start[warp] - at.h * at.n;
+    at.h = (a0 - run_start) / at.n;
+    at.i = a0 - run_start - at.h * at.n;
     auto next = [&](Place& x) {
       if (++x.i < x.n) return;
       x.i = 0;
