@@ -30,7 +30,7 @@ def quantise(x):
     for g in range(x.shape[-1] // GROUP):
         part = x[..., g * GROUP:(g + 1) * GROUP]
         fine = np.isfinite(part).all(-1)
-        # the largest magnitude over 7 is rounded to fp32 first, as the library's division does
+        # (by way of fp32, which changes nothing: no quotient by 7 lies that near to a midpoint of two bf16s)
         scale = np.where(fine, _to_bf16((np.abs(np.where(fine[..., None], part, 0)).max(-1) / 7)
                                         .astype(np.float32).astype(np.float64)), np.nan)
         ok = fine & (scale > 0)

@@ -17,8 +17,9 @@
 //            dims, times the key's scale, added to one more product of the keys' scales with -8 * (sum
 //            of q over the group), the latter as three bf16 terms; q is scaled into fp16's range;
 //   output   O^T += V^T P^T (M = 16 dims, N = 8 heads, inner = 16 keys) with P_g = bf16(p * scale of
-//            the key's group g), and one more product per group with ones in place of V, which sums
-//            the same rounded P_g: O - 136 * that sum is the result, so the offset adds no rounding.
+//            the key's group g), and before it one more product with -136 in place of V. Record by
+//            record: a sum of the offsets over a long run taken off at its end (one product per group
+//            with ones) left 2^-24 of 136 times all weights, 0.0024 of the output at 70 records per warp.
 // P (keys x heads) becomes the second product's operand by an 8 x 8 transpose between lanes
 // (movmatrix). Sums of products, softmax statistics and sums are fp32; rounding p * scale to bf16 (2^-8
 // relative) is the one rounding before the output's.
@@ -58,18 +59,17 @@ constexpr float kHigh = 256.0f;           // a weight above it moves the referen
 constexpr float kLow = -3e38f;            // reference of a head that has seen nothing
 constexpr int kAlone = 6;                 // records per warp up to which a CTA takes a (request, kv head) alone
 constexpr int kMaxCtas = 160;             // of a launch (one wave: one per SM)
-constexpr float kOffset = 136.0f;         // value of a widened nibble of V for code 0
 constexpr float kKOffset = 8.0f / 16777216.0f;  // value of a nibble of K for code 0
 constexpr uint32_t kNibbles = 0x000f000fu;
 constexpr uint32_t kBias = 0x43004300u;   // two bf16 of 128: the last place is 1
-constexpr uint32_t kOnes = 0x3f803f80u;   // two bf16 of 1
+constexpr uint32_t kMinus = 0xc308c308u;  // two bf16 of -136, what a widened nibble of V is above its code
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 struct Masks {
-  uint32_t nibbles, higher, bias, ones;
+  uint32_t nibbles, higher, bias, minus;
 };
 
 struct Kv4DecodeParams {
@@ -153,8 +153,7 @@ __device__ __forceinline__ void load_vec(uint32_t (&w)[NG], uint32_t at) {
 template <int D, int NT>
 struct State {
   static constexpr int NG = Kv4<D>::kGroups;
-  float o[NT][2 * NG][4];   // O^T + 136 * sum, dims 32 g + 4 r + .. (r = lane / 4)
-  float ones[NT][NG][4];    // the sums of the rounded P_g (every row the same)
+  float o[NT][2 * NG][4];    // O^T, dims 32 g + 4 r + .. (r = lane / 4)
   float m[NT][2], l[NT][2];  // reference (log2 units, the same in all lanes of a head), this lane's share of the sum
 };
 
@@ -166,10 +165,6 @@ __device__ __forceinline__ void reset(State<D, NT>& st) {
     for (int i = 0; i < 2 * State<D, NT>::NG; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[t][i][e] = 0.0f;
-#pragma unroll
-    for (int g = 0; g < State<D, NT>::NG; ++g)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) st.ones[t][g][e] = 0.0f;
     st.m[t][0] = st.m[t][1] = kLow;
     st.l[t][0] = st.l[t][1] = 0.0f;
   }
@@ -347,10 +342,6 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.o[t][i][e] *= alpha[e % 2];
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st.ones[t][g][e] *= alpha[e % 2];
-#pragma unroll
       for (int e = 0; e < 4; ++e) {
         pr[t][e] = ex2(fmaf(s[t][e], qf.scale[t][e % 2], -st.m[t][e % 2]));
       }
@@ -374,6 +365,14 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
       pb[t][g][1] = transpose8x8(pack2(pr[t][2] * s1, pr[t][3] * s1));
     }
   }
+  // the offset first, for all groups, so that the two products of an accumulator stand apart
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        mma_bf16(st.o[t][2 * g + half], mk.minus, mk.minus, mk.minus, mk.minus, pb[t][g][0], pb[t][g][1]);
 #pragma unroll
   for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -384,7 +383,6 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         mma_bf16(st.o[t][2 * g + half], x[0], x[1], y[0], y[1], pb[t][g][0], pb[t][g][1]);
-        if (half == 0) mma_bf16(st.ones[t][g], mk.ones, mk.ones, mk.ones, mk.ones, pb[t][g][0], pb[t][g][1]);
       }
     }
 }
@@ -670,9 +668,8 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
           const float inv = inverse(st.l[t][e]);
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            const float off = kOffset * st.ones[t][g][e];
-            const float4 x = make_float4(st.o[t][2 * g][e] - off, st.o[t][2 * g][e + 2] - off,
-                                         st.o[t][2 * g + 1][e] - off, st.o[t][2 * g + 1][e + 2] - off);
+            const float4 x = make_float4(st.o[t][2 * g][e], st.o[t][2 * g][e + 2], st.o[t][2 * g + 1][e],
+                                         st.o[t][2 * g + 1][e + 2]);
             if (whole)
               write_out4(p.out, ((int64_t)s * p.hkv + h) * p.G + head, D, 8 * g + r, x, inv);
             else
@@ -911,7 +908,7 @@ cudaError_t launch_kv4_decode(const void* q, const void* cache, int32_t n_pages,
   p.hkv = hkv;
   p.G = hq / hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.masks = Masks{kNibbles, kNibbles << 4, kBias, kOnes};
+  p.masks = Masks{kNibbles, kNibbles << 4, kBias, kMinus};
   p.part_o = ws.part_o;
   p.part_ml = ws.part_ml;
   p.tickets = ws.tickets;

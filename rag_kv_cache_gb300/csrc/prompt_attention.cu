@@ -38,11 +38,17 @@
 //   of 64 held the warps longer: 306 against 293 us for the 40 prompts.
 // Roles, TMEM columns, register split and bounded waits are those of attention_pp.cu; "round" counts
 // the key tiles of all the CTA's items, and ring stage and parity follow from it. Item descriptions
-// pass from the producer to the other warps through a ring of eight: the producer
-// requests item i + 7's keys only once both tiles' scores of item i + 5 are formed, for which the softmax
-// warps are through with item i + 3. After a wait that gave up
-// (abort flag) every warp still walks through the rounds of the current item, without work, and the
-// producer ends the list, so no named barrier is left short.
+// pass from the producer to the other warps through a ring of eight: the producer requests item i + 7's
+// keys only once both tiles' scores of item i + 5 are formed, for which the softmax warps are through with
+// item i + 3. After a wait that gave up (abort flag) every warp still walks through the rounds of the
+// current item, without work, and the producer ends the list, so no named barrier is left short.
+//
+// Measured (8 kv heads of 128 dims): 16 chunks of 2,048 tokens, 32 query heads, 469 us with inputs that lie in
+// HBM and 421 with them in L2 (284 us at the tensor cores' rate, 100 of HBM); 40 prompts of 1 to 1,087
+// tokens, 64 query heads, 291 us (135 and 117); one prompt of 16,384 tokens 1.29 ms, 0.88 of that rate.
+// A round (a key tile against both query tiles) takes 2,750 - 2,850 cycles, of which the tensor cores need 2,504;
+// an item adds about 6,000: on its softmax warps' path the masks of the diagonal tile (600), the last product
+// (1,000), the output (2,000), the next item and the first maximum (600).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
