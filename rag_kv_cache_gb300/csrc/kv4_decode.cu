@@ -18,8 +18,9 @@
 //            of q over the group), the latter as three bf16 terms; q is scaled into fp16's range;
 //   output   O^T += V^T P^T (M = 16 dims, N = 8 heads, inner = 16 keys) with P_g = bf16(p * scale of
 //            the key's group g), and before it one more product with -136 in place of V. Record by
-//            record: a sum of the offsets over a long run taken off at its end (one product per group
-//            with ones) left 2^-24 of 136 times all weights, 0.0024 of the output at 70 records per warp.
+//            record: taken off at the end of a run (one product per group with ones, summing P_g), the
+//            offsets left their fp32 rounding, 2^-24 of 136 times all weights: 87 instead of 89 us for
+//            the batch below, but its output 0.0029 instead of 0.0023 off (relative, root mean square).
 // P (keys x heads) becomes the second product's operand by an 8 x 8 transpose between lanes
 // (movmatrix). Sums of products, softmax statistics and sums are fp32; rounding p * scale to bf16 (2^-8
 // relative) is the one rounding before the output's.
@@ -32,18 +33,19 @@
 // them to finish, over partials in the plan's scratch (a ticket per CTA that begins one). The merge
 // order is fixed by position, so results do not change from run to run. Small batches of short requests
 // take a CTA per (request, kv head), which spares that last merge: 4 requests of up to
-// 545 keys and 2 kv heads of 64 dims 6.8 against 11.2 us.
+// 545 keys and 2 kv heads of 64 dims 6.7 against 11.2 us. Up to 32 requests are dealt out by each
+// warp for itself, a request per lane, so that no barrier stands before its first copies (6.9 us with one).
 //
 // Feeding: each warp asks for its own records by bulk copies into a ring of its own, five ahead (eight
 // with 8 warps), and waits for them alone; no warp waits for another one until the merge.
 //
 // Measured (8 kv heads of 128 dims): 64 requests of up to 8,449 keys, 64 query heads (308 MB, 46 us at
-// the copy rate) 87 us, 0.53 of that rate; one request of 32,897 keys, 32 query heads (38 MB, 5.7 us) 24 us,
+// the copy rate) 89 us, 0.52 of that rate; one request of 32,897 keys, 32 query heads (38 MB, 5.7 us) 24 us,
 // of which about 8 us is fixed: the batch's prefix sums, the first copies, the merges. What bounds the
 // batch is the instructions: about 360 per record and warp, 175 of them on the integer pipe, which takes one
 // every other cycle, so 350 cycles per record for a scheduler, 0.9 of the bytes' time; three warps per
-// scheduler overlap them with the products and the exponentials to 1.6 times that. With 10 and 14 warps
-// (the latter with fewer registers) the batch took 101 and 102 us. Records two to a copy (92 us then), Q in
+// scheduler overlap them with the products and the exponentials to 1.6 times that. With 14 and 16 warps,
+// of fewer registers, the batch takes 96 and 94 us. Records two to a copy (92 us then), Q in
 // shared memory to make room for 16 warps (105), shifts as multiplications (96), and K in e4m3 with Q in two
 // terms (102; 3 instructions per 8 codes, but such a product costs more than two in fp16) were not faster.
 #include "common.cuh"
