@@ -428,11 +428,10 @@ cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cach
  * and k, v [n_rows, hkv, D], and
  *   out[t, h] = sum_{j <= t, same sequence} softmax_j(scale * q[t, h] . k[j, g]) v[j, g],  g = h / (hq/hkv),
  * with q and k RoPE-encoded at their positions. cu_seqlens: device int32 [n_seqs + 1], ascending,
- * within [0, n_rows], n_seqs at most CB_PROMPT_MAX_SEQS (a block looks through the offsets once per 64
- * tokens of the longest sequence or so); empty sequences are allowed, and rows in no sequence keep their out. Values of
- * keys that a row does not see (later ones, other sequences') do not reach it, whatever they are.
- * scale <= 0 selects 1/sqrt(D). fp32 accumulation and softmax, bf16 P, bf16 output; tcgen05 (TMEM
- * accumulators) fed by TMA. out must be none of the inputs. Offsets that fall or leave [0, n_rows] are
+ * within [0, n_rows], n_seqs at most CB_PROMPT_MAX_SEQS; empty sequences are allowed, and rows in no
+ * sequence keep their out. Values of keys that a row does not see (later ones, other sequences') do
+ * not reach it, whatever they are. scale <= 0 selects 1/sqrt(D). fp32 accumulation and softmax, bf16 P,
+ * bf16 output; tcgen05 (TMEM accumulators) fed by TMA. out must be none of the inputs. Offsets that fall or leave [0, n_rows] are
  * recorded as CB_ERR_DEVICE_CHECK (clipped, a falling pair read as empty). No scratch: calls on one
  * plan may overlap. A bounded wait that gives up records CB_ERR_TIMEOUT. */
 #define CB_PROMPT_MAX_SEQS 16384

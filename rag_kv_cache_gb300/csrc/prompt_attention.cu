@@ -15,13 +15,17 @@
 //   One CTA per SM takes items in turn; the rings of K and V run on across items, and the next
 //   item's first tiles load while the last softmax of the current one runs.
 //   No tile list. The lengths are known on the device only. The grid has a block for every item that
-//   the row count allows; blocks stand for the items in the order longest first, and a running CTA
-//   claims the next block that has not started (cluster launch control) when it has requested its last
-//   K tile. The producer warp finds a block's item by counting sequences. Taken in turn instead, by
-//   index modulo the number of CTAs in alternating direction, the items of 40 prompts of 1 to 1,087 tokens
-//   ended between 290 and 327 us on the various SMs; claimed they end between 298 and 302 us. Items
-//   that share K and V side by side (four or eight levels of a sequence as neighbours in the order) are
-//   slower, not faster: 498 and 513 against 438 us for 16 chunks of 2,048 tokens.
+//   the row count allows; blocks stand for the items in the order of `Order`, and a running CTA claims the
+//   next block that has not started (cluster launch control) when it has requested its last K tile. The
+//   producer warp finds a block's item by counting sequences. Taken in turn instead, by index modulo
+//   the number of CTAs in alternating direction, the items of 40 prompts of 1 to 1,087 tokens ended between
+//   290 and 327 us on the various SMs; claimed they end within 4 us of one another.
+//   Order. Longest first, so that the SMs end together, but by groups of sequences whose K and V (48 MB
+//   at the mean length) stay in L2: over all sequences at once, 16 chunks of 2,048 tokens read theirs
+//   from HBM again and again (64% of L2's reads missed): 472 us against 425, the 40 prompts 293 against
+//   282, 64 prompts of 512 tokens 186 against 172. Groups of 8, 16, 32 and 64 MB: 436, 438, 429 and 429 us for
+//   the chunks, 289, 283, 282 and 284 for the prompts; each sequence a group of its own 435, 299 and 204.
+//   Four or eight levels of a sequence as neighbours are slower too.
 //   Rows of other sequences. A key tile that reaches past its sequence's end holds the next one's
 //   rows, and one on the diagonal holds keys that some of the rows must not see; their weight is 0, but
 //   0 * V is NaN where V is infinite or NaN. In those tiles (the ones with a key that some row of the
@@ -43,14 +47,16 @@
 // item i + 3. After a wait that gave up (abort flag) every warp still walks through the rounds of the
 // current item, without work, and the producer ends the list, so no named barrier is left short.
 //
-// Measured (8 kv heads of 128 dims): 16 chunks of 2,048 tokens, 32 query heads, 469 us with inputs that lie in
-// HBM and 421 with them in L2 (284 us at the tensor cores' rate, 100 of HBM); 40 prompts of 1 to 1,087
-// tokens, 64 query heads, 291 us (135 and 117); one prompt of 16,384 tokens 1.29 ms, 0.88 of that rate.
+// Measured (8 kv heads of 128 dims): 16 chunks of 2,048 tokens, 32 query heads, 425 us with new inputs in each
+// call, 394 with the same (284 us at the tensor cores' rate, 100 of HBM); 40 prompts of 1 to 1,087 tokens,
+// 64 query heads, 282 us (135 and 117); one prompt of 16,384 tokens 1.29 ms, 0.88 of that rate.
 // A round (a key tile against both query tiles) takes 2,750 - 2,850 cycles, of which the tensor cores need 2,504;
 // an item adds about 6,000: on its softmax warps' path the masks of the diagonal tile (600), the last product
 // (1,000), the output (2,000), the next item and the first maximum (600).
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <algorithm>
 
 #include "attn_common.cuh"
 #include "attn_tile.cuh"
@@ -82,6 +88,7 @@ constexpr int kSoftmaxRegs = 216;  // per thread of WG0 / WG1 after setmaxnreg.i
 constexpr int kOtherRegs = 72;     // per thread of WG2 after setmaxnreg.dec
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only when the max grows by > 2^8
 constexpr float kTileSumLimit = 65536.0f;  // a later tile whose P sum exceeds 2^16 moves the reference
+constexpr int64_t kGroupBytes = 48 << 20;  // K and V of the sequences that are taken side by side
 constexpr unsigned long long kItemLimitNs = 5 * kTimeoutNs;  // the producer's own waits end well before
 
 __host__ __device__ constexpr uint32_t col_s(int i) { return (uint32_t)(i * kBN); }
@@ -122,6 +129,7 @@ struct PromptParams {
   int group;  // query heads per kv head, 1 << lg
   int lg;
   int tq;     // query tokens per tile = 128 / group
+  int seqs_per_group;  // of the items' order
   float scale_log2;
   int32_t* err;
 };
@@ -172,72 +180,52 @@ __device__ __forceinline__ int row_at(const PromptParams& p, int s) {
   return r < 0 ? 0 : min(r, p.n_rows);
 }
 
-// The launch's items in the order in which blocks stand for them, for a converged warp: by level (the
-// index of an item in its sequence) from the highest down, so the longest first, within a level by
-// sequence and kv head.
+// The launch's items in the order in which blocks stand for them, for a converged warp: by groups of
+// p.seqs_per_group sequences (at most 32, one per lane); in a group by level (the index of an item in its
+// sequence) from the highest down, so the longest first; in a level by sequence and kv head.
 struct Order {
-  int level, count, first;  // current level, the sequences that have it, items of the levels above
-  int same, begin;          // they are the same down to this level; the first of them (a multiple of 32 at or before it)
-  int s0, before;           // cursor: sequences before s0 hold `before` of them
-  int latest;               // last index asked for
+  int s0, group_end;   // the group's first sequence, index behind its last item
+  int items;           // per kv head, of this lane's sequence
+  int level, end;      // current level, index behind its last item
+  uint32_t has;        // the sequences that have it
+  int latest;          // last index asked for
 
   // Items per kv head of sequence s.
   __device__ __forceinline__ int items_of(const PromptParams& p, int s) const {
-    if (s >= p.n_seqs) return 0;
     const int n = row_at(p, s + 1) - row_at(p, s), per = kTiles * p.tq;
     return n > 0 ? (n + per - 1) >> (__ffs(per) - 1) : 0;
   }
-  __device__ __forceinline__ void enter(const PromptParams& p, int lane) {
-    int n = 0, below = 0, at = p.n_seqs;
-#pragma unroll 4
-    for (int s = lane; s < p.n_seqs; s += 32) {
-      const int items = items_of(p, s);
-      const bool has = items > level;
-      n += has ? 1 : 0;
-      below = max(below, has ? 0 : items);
-      at = min(at, has ? s : p.n_seqs);
-    }
-    count = __reduce_add_sync(0xffffffffu, n);
-    same = __reduce_max_sync(0xffffffffu, below);
-    begin = __reduce_min_sync(0xffffffffu, at) / 32 * 32;
-    s0 = begin;
-    before = 0;
+  // The group from sequence s on, whose first item has index `first`.
+  __device__ __forceinline__ void enter(const PromptParams& p, int s, int first, int lane) {
+    s0 = s;
+    items = lane < p.seqs_per_group && s + lane < p.n_seqs ? items_of(p, s + lane) : 0;
+    group_end = first + __reduce_add_sync(0xffffffffu, items) * p.hkv;
+    level = __reduce_max_sync(0xffffffffu, items);
+    end = first;
   }
   __device__ __forceinline__ void start(const PromptParams& p, int lane) {
-    int top = 0;
-    for (int s = lane; s < p.n_seqs; s += 32) top = max(top, items_of(p, s));
-    level = __reduce_max_sync(0xffffffffu, top) - 1;
-    first = latest = 0;
-    enter(p, lane);
+    latest = 0;
+    enter(p, 0, 0, lane);
   }
   // Item idx: false past the last one. Indices come in rising order but for rare cases, which begin anew.
   __device__ __forceinline__ bool find(const PromptParams& p, int idx, int lane, int& seq, int& head) {
     if (idx < latest) start(p, lane);
     latest = idx;
-    while (level >= 0 && idx - first >= count * p.hkv) {
-      first += count * p.hkv;
+    while (idx >= group_end) {
+      if (s0 + p.seqs_per_group >= p.n_seqs) return false;
+      enter(p, s0 + p.seqs_per_group, group_end, lane);
+    }
+    while (idx >= end) {
+      has = __ballot_sync(0xffffffffu, items >= level);
       --level;
-      if (level >= same) {
-        s0 = begin;
-        before = 0;
-      } else if (level >= 0) {
-        enter(p, lane);
-      }
+      end += __popc(has) * p.hkv;
     }
-    if (level < 0) return false;
-    const uint32_t rel = idx - first, nth = rel / (uint32_t)p.hkv;  // 32 bits: a 64-bit division would be a call
+    const uint32_t rel = idx - (end - __popc(has) * p.hkv), nth = rel / (uint32_t)p.hkv;
     head = (int)(rel - nth * p.hkv);
-    for (; s0 < p.n_seqs; s0 += 32) {
-      uint32_t has = __ballot_sync(0xffffffffu, items_of(p, s0 + lane) > level);
-      const int n = __popc(has);
-      if (before + n > (int)nth) {
-        for (int i = before; i < (int)nth; ++i) has &= has - 1;
-        seq = s0 + __ffs(has) - 1;
-        return true;
-      }
-      before += n;
-    }
-    return false;
+    uint32_t left = has;
+    for (uint32_t i = 0; i < nth; ++i) left &= left - 1;
+    seq = s0 + __ffs(left) - 1;
+    return true;
   }
 };
 
@@ -865,6 +853,8 @@ cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const i
   p.group = group;
   p.lg = 31 - __builtin_clz(group);
   p.tq = tq;
+  const int64_t seq_bytes = (int64_t)n_rows / n_seqs * hkv * D * 4 + 1;  // K and V of a sequence of the mean length
+  p.seqs_per_group = (int)std::min<int64_t>(std::max<int64_t>(kGroupBytes / seq_bytes, 1), 32);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.err = err;
   const size_t smem = 1024 + (size_t)(kTiles * kBM + 2 * kStages * kBN) * D * 2 + 2 * kSoftmaxThreads / 32 * kOutWarp;
