@@ -5,8 +5,8 @@ Tolerances. Page tables, slots, codes and loaded rows are exact. Attention in 64
 rows, s = sum_j p_j |v_j|: the softmax weights (decode: times V's scale) are rounded to bf16 once,
 2^-8 relative each, so at most 2^-8 s; the output's rounding adds 2^-8 |out|. Scores are fp32 sums:
 of D products |q k| (prompt), or of groups of 32 products of |q| with 8 + code <= 15 and the offset
-8 |q| (decode), each of at most 40 roundings of 2^-23 (the matrix unit truncates); their error e
-changes a weight by a factor within exp(2 e).
+8 |q| (decode; q scaled into fp16, within 2^-35 of its head's largest), each of at most 40 roundings of
+2^-23 (the matrix unit truncates); their error e changes a weight by a factor within exp(2 e).
 """
 
 import numpy as np
@@ -14,7 +14,7 @@ import pytest
 import torch
 
 from oracle import serving
-from oracle.attention import decode_attention
+from oracle.attention import causal_gqa_attention, decode_attention
 from oracle.deviation import bf16_bits_to_f64
 from workloads.generator import f32_to_bf16_bits
 from workloads.torch_io import bf16_bits, bf16_tensor
@@ -557,6 +557,26 @@ def test_prompt_many_sequences(cb):
     out = _prompt(cb, plan, q, k, v, cu)
     plan.check()
     _check_prompt(q, k, v, cu, out, "many sequences")
+    plan.close()
+
+
+def test_prompt_long_sequences_in_groups_of_two(cb):
+    # K and V of 20 MB at the mean length: the order of the work goes by two sequences at a time
+    rng = np.random.default_rng(46)
+    plan = _plan(cb, 16, 16, 128)
+    lens = [2600, 0, 3300, 2450, 3900, 2450]
+    cu, rows = np.cumsum([0] + lens), sum(lens)
+    q, k, v = (_bits(rng, rows, 16, 128) for _ in range(3))
+    out = torch.full((rows, 16, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    cb.cb_prompt_attention(plan, bf16_tensor(q), bf16_tensor(k), bf16_tensor(v), _i32(cu), out)
+    plan.check()
+    qf, kf, vf, got = bf16_bits_to_f64(q), bf16_bits_to_f64(k), bf16_bits_to_f64(v), _f64(out)
+    for a, b in zip(cu, cu[1:]):  # every 37th row of each, and its ends
+        at = np.unique(np.r_[np.arange(0, b - a, 37), b - a - 1]) if b > a else np.zeros(0, int)
+        if not len(at):
+            continue
+        ref, vs = causal_gqa_attention(qf[a + at], at, kf[a:b], vf[a:b], return_vscale=True)
+        _close(got[a + at], ref, vs, 40 * 2.0**-23 * 128**0.5 * np.abs(qf).max() * np.abs(kf).max(), f"rows from {a}")
     plan.close()
 
 
