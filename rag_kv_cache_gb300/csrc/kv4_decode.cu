@@ -209,6 +209,7 @@ __device__ __forceinline__ void load_query(Query<D, NT>& qf, const uint8_t* q, i
     const int up = 141 - max((int)(top >> 7), 1);  // the power: -114 .. 140, in two factors below
     const float up0 = power_of_2(up >> 1), up1 = power_of_2(up - (up >> 1));
     float scale = scale_log2 * power_of_2((24 - up) >> 1) * power_of_2(24 - up - ((24 - up) >> 1));
+    scale = fmaxf(scale, 1.2e-38f);  // not 0, which times -infinity (a masked key's score) is NaN
     if (top >= 0x7f80u) scale = __uint_as_float(0x7fc00000u);
 #pragma unroll
     for (int e = 0; e < 2; ++e) qf.scale[t][e] = __shfl_sync(0xffffffffu, scale, 4 * (2 * c + e));

@@ -6,7 +6,11 @@ rows, s = sum_j p_j |v_j|: the softmax weights (decode: times V's scale) are rou
 2^-8 relative each, so at most 2^-8 s; the output's rounding adds 2^-8 |out|. Scores are fp32 sums:
 of D products |q k| (prompt), or of groups of 32 products of |q| with 8 + code <= 15 and the offset
 8 |q| (decode; q scaled into fp16, within 2^-35 of its head's largest), each of at most 40 roundings of
-2^-23 (the matrix unit truncates); their error e changes a weight by a factor within exp(2 e).
+2^-23 (the matrix unit truncates); their error e changes a weight by a factor within exp(2 e). Decode sums V's codes with an offset of 136 that it takes
+off record by record: two products per record, each truncated within two units in the last place of partial sums that
+reach 143 times the record's weights times the row's steps, so over all records at most 4 * 2^-23 * 143 times
+the mean step, and as much again for the merges: 8 * 2^-23 * 143 of the largest step. It shows only where the keys
+that weigh something have code 0.
 """
 
 import numpy as np
@@ -40,9 +44,9 @@ def _i32(x):
     return torch.as_tensor(np.ascontiguousarray(np.asarray(x, dtype=np.int32))).cuda()
 
 
-def _close(got, ref, vs, e, what):
+def _close(got, ref, vs, e, what, least=1e-30):
     err = np.abs(got - ref)
-    lim = (2.0**-8 + 2 * e) * vs + (2.0**-8) * np.abs(ref) + 1e-30
+    lim = (2.0**-8 + 2 * e) * vs + (2.0**-8) * np.abs(ref) + least
     assert np.isfinite(got).all(), f"{what}: {int((~np.isfinite(got)).sum())} values are not finite"
     assert (err <= lim).all(), f"{what}: err/limit {float((err / lim).max()):.3f}"
 
@@ -336,7 +340,9 @@ def _check_decode(plan, q, out, ks, vs_rows, what, scale=None):
             continue
         ref, vs = decode_attention(bf16_bits_to_f64(q)[s], ks[s], vs_rows[s], scale=scale, return_vscale=True)
         e = _score_error(bf16_bits_to_f64(q)[s], np.abs(ks[s]).max() / 7, d, scale or d**-0.5)
-        _close(_f64(out[s]), ref, vs, min(e, 0.01), f"{what}, request {s} of {len(ks[s])} keys")
+        step = np.abs(vs_rows[s]).reshape(len(vs_rows[s]), -1, d // 32, 32).max((0, 3)) / 7  # [hkv, groups]
+        least = np.repeat(np.repeat(8 * 2.0**-23 * 143 * step, 32, axis=1), plan.hq // plan.hkv, axis=0) + 1e-30
+        _close(_f64(out[s]), ref, vs, min(e, 0.01), f"{what}, request {s} of {len(ks[s])} keys", least)
 
 
 @pytest.mark.parametrize("hq,hkv,d", HEADS)
@@ -444,6 +450,22 @@ def test_decode_queries_far_from_one(cb, q_power, spike):
         sums = np.abs(qf[s]).reshape(hkv, hq // hkv, 4, 32).max(-1)
         e = (sums * (32 * (15 + 8) * 40 * 2.0**-23) + 2.0**-35 * 32 * 7 * sums.max(-1, keepdims=True)) * top[:, None]
         _close(_f64(out[s]), ref, vs, min(d**-0.5 * e.sum(-1).max(), 0.02), f"request {s}")
+    plan.close()
+
+
+@pytest.mark.parametrize("scale", [1e-30, 0.02, 3.0])
+def test_decode_scales_and_a_zero_query(cb, scale):
+    # head 1 asks with zeros: every key weighs the same, also at a scale whose product with q's power underflows
+    rng = np.random.default_rng(47)
+    plan = _plan(cb, 8, 2, 64)
+    lens = [21, 300]
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, 16)
+    q = _bits(rng, 2, 8, 64)
+    q[:, 1] = 0
+    out = torch.empty((2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, 16, _i32(table), _i32(lens), out, scale=scale)
+    plan.check()
+    _check_decode(plan, q, out, ks, vs, f"scale {scale}", scale=scale)
     plan.close()
 
 
