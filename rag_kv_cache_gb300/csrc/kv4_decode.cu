@@ -70,6 +70,13 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// Adds one; the CTA's writes before it (behind a barrier) are seen by who reads the sum, whose reads come after.
+__device__ __forceinline__ int take_ticket(int32_t* at) {
+  int before;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(at) : "memory");
+  return before;
+}
+
 struct Masks {
   uint32_t nibbles, higher, bias, minus;
 };
@@ -792,86 +799,107 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
     if (reaches(tid)) {
       const SlotInfo& x = info[edge[tid]];
       const int c0 = x.p0 / cta_records, c1 = (x.p1 - 1) / cta_records;
-      __threadfence();
-      if (atomicAdd(&p.tickets[c0], 1) == c1 - c0) {
+      if (take_ticket(&p.tickets[c0]) == c1 - c0) {
         s_last[tid] = 1;
         p.tickets[c0] = 0;  // ready for the next call
       }
-      __threadfence();
     }
   }
   __syncthreads();
+  if (s_last[0] + s_last[1] == 0) return;
+  // Both, where this CTA is the last of both, side by side (one after the other they took 3 us longer).
   float* scratch = reinterpret_cast<float*>(smem);  // the partial results in it have been read
-  constexpr int kSums = kMaxCtas * kKv4MaxGroup, kTeams = kSums + kKv4MaxGroup;
-  static_assert(kWarps * kWarpBytes<D, NT> >= (kTeams + 4 * kThreads) * 4, "scratch of the merge over CTAs");
-#pragma unroll 1
+  constexpr int kSums = kMaxCtas * kKv4MaxGroup, kWeights = kSums + kKv4MaxGroup;  // of one of the two
+  static_assert(kWarps * kWarpBytes<D, NT> >= (2 * kWeights + 2 * 4 * kThreads) * 4, "scratch of the merge over CTAs");
+  int c0[2], parts[2], pair[2];
+#pragma unroll
   for (int e = 0; e < 2; ++e) {
+    c0[e] = parts[e] = pair[e] = 0;
     if (!s_last[e]) continue;
     const SlotInfo x = info[edge[e]];
-    const int c0 = x.p0 / cta_records, parts = (x.p1 - 1) / cta_records - c0 + 1;
-    auto part_of = [&](int k) -> int { return 2 * (c0 + k) + (k == 0 ? 1 : 0); };
-    // weights of the parts, a warp per head: scratch [part][head], then the heads' sums
-    for (int head = warp; head < p.G; head += kWarps) {
-      float2 ml[kMaxCtas / 32];  // parts lane, lane + 32, ...
-      float m = kLow, l = 0.0f;
+    c0[e] = x.p0 / cta_records;
+    parts[e] = (x.p1 - 1) / cta_records - c0[e] + 1;
+    pair[e] = x.pair;
+  }
+  auto part_of = [&](int e, int k) -> int { return (2 * (c0[e] + k) + (k == 0 ? 1 : 0)) * kKv4MaxGroup; };
+  // weights of the parts, a warp per head: scratch [part][head], then the heads' sums
 #pragma unroll
-      for (int u = 0; u < kMaxCtas / 32; ++u) {
-        ml[u] = make_float2(kLow, 0.0f);
-        if (lane + 32 * u < parts) ml[u] = __ldcg(&p.part_ml[part_of(lane + 32 * u) * kKv4MaxGroup + head]);
-      }
-#pragma unroll
-      for (int u = 0; u < kMaxCtas / 32; ++u) m = fmaxf(m, ml[u].x);
+  for (int e = 0; e < 2; ++e) {
+    float* weights = scratch + e * kWeights;
+    // the warps from the last one down take the second's heads
+    for (int head = e == 0 ? warp : kWarps - 1 - warp; head < p.G && parts[e] > 0; head += kWarps) {
+      // parts lane, lane + 32, ..; most launches have no more than 32
+      auto ml_of = [&](int k) -> float2 {
+        return k < parts[e] ? __ldcg(&p.part_ml[part_of(e, k) + head]) : make_float2(kLow, 0.0f);
+      };
+      const float2 ml = ml_of(lane);
+      float m = ml.x;
+#pragma unroll 1
+      for (int k = lane + 32; k < parts[e]; k += 32) m = fmaxf(m, ml_of(k).x);
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-#pragma unroll
-      for (int u = 0; u < kMaxCtas / 32; ++u) {
-        const float wk = ex2(ml[u].x - m);
-        l = fmaf(wk, ml[u].y, l);
-        if (lane + 32 * u < parts) scratch[(lane + 32 * u) * kKv4MaxGroup + head] = wk;
+      float wk = ex2(ml.x - m), l = wk * ml.y;
+      if (lane < parts[e]) weights[lane * kKv4MaxGroup + head] = wk;
+#pragma unroll 1
+      for (int k = lane + 32; k < parts[e]; k += 32) {
+        const float2 more = ml_of(k);
+        wk = ex2(more.x - m);
+        l = fmaf(wk, more.y, l);
+        weights[k * kKv4MaxGroup + head] = wk;
       }
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-      if (lane == 0) scratch[kSums + head] = l;
+      if (lane == 0) weights[kSums + head] = l;
     }
-    __syncthreads();
-    // the threads in teams of n4 (a power of two), each taking every (kThreads / n4)-th part
-    const int teams = kThreads >= n4 ? kThreads / n4 : 1;
-    if (tid < teams * n4 || teams == 1)
-      for (int at = tid & (n4 - 1), team = teams > 1 ? tid / n4 : 0; at < n4; at += kThreads) {
-        const int head = at * 4 / D;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = team; k < parts; k += 4 * teams) {
-          float4 v[4];
+  }
+  __syncthreads();
+  // the threads in teams of n4 (a power of two), each taking every (kThreads / n4)-th part
+  const int teams = kThreads >= n4 ? kThreads / n4 : 1;
+  if (tid < teams * n4 || teams == 1)
+    for (int at = tid & (n4 - 1), team = teams > 1 ? tid / n4 : 0; at < n4; at += kThreads) {
+      const int head = at * 4 / D;
+      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      for (int k = team; k < max(parts[0], parts[1]); k += 4 * teams) {
+        float4 v[2][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (k + u * teams < parts)
-              v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + part_of(k + u * teams) * kKv4MaxGroup * D + at * 4));
+            if (k + u * teams < parts[e])
+              v[e][u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + part_of(e, k + u * teams) * D + at * 4));
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            if (k + u * teams >= parts) continue;
-            const float wk = scratch[(k + u * teams) * kKv4MaxGroup + head];
-            acc.x = fmaf(wk, v[u].x, acc.x);
-            acc.y = fmaf(wk, v[u].y, acc.y);
-            acc.z = fmaf(wk, v[u].z, acc.z);
-            acc.w = fmaf(wk, v[u].w, acc.w);
+            if (k + u * teams >= parts[e]) continue;
+            const float wk = scratch[e * kWeights + (k + u * teams) * kKv4MaxGroup + head];
+            acc[e].x = fmaf(wk, v[e][u].x, acc[e].x);
+            acc[e].y = fmaf(wk, v[e][u].y, acc[e].y);
+            acc[e].z = fmaf(wk, v[e][u].z, acc[e].z);
+            acc[e].w = fmaf(wk, v[e][u].w, acc[e].w);
           }
-        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (parts[e] == 0) continue;
         if (teams > 1)
-          *reinterpret_cast<float4*>(scratch + kTeams + 4 * (team * n4 + at)) = acc;
+          *reinterpret_cast<float4*>(scratch + 2 * kWeights + 4 * (e * kThreads + team * n4 + at)) = acc[e];
         else
-          write_out4(p.out, (int64_t)x.pair * p.G + head, D, at % (D / 4), acc, inverse(scratch[kSums + head]));
+          write_out4(p.out, (int64_t)pair[e] * p.G + head, D, at % (D / 4), acc[e], inverse(scratch[e * kWeights + kSums + head]));
       }
-    __syncthreads();
-    if (teams > 1 && tid < n4) {
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int team = 0; team < teams; ++team) {
-        const float4 v = *reinterpret_cast<const float4*>(scratch + kTeams + 4 * (team * n4 + tid));
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-      }
-      write_out4(p.out, (int64_t)x.pair * p.G + tid * 4 / D, D, tid % (D / 4), acc,
-                 inverse(scratch[kSums + tid * 4 / D]));
     }
-    __syncthreads();  // the scratch is used again
+  if (teams == 1) return;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (parts[e] == 0 || tid >= n4) continue;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int team = 0; team < teams; ++team) {
+      const float4 v = *reinterpret_cast<const float4*>(scratch + 2 * kWeights + 4 * (e * kThreads + team * n4 + tid));
+      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
+    write_out4(p.out, (int64_t)pair[e] * p.G + tid * 4 / D, D, tid % (D / 4), acc,
+               inverse(scratch[e * kWeights + kSums + tid * 4 / D]));
   }
 }
 
