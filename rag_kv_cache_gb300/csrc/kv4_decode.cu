@@ -19,7 +19,7 @@
 //   output   O^T += V^T P^T (M = 16 dims, N = 8 heads, inner = 16 keys) with P_g = bf16(p * scale of
 //            the key's group g), and before it one more product with -136 in place of V. Record by
 //            record: taken off at the end of a run (one product per group with ones, summing P_g), the
-//            offsets left their fp32 rounding, 2^-24 of 136 times all weights: 87 instead of 89 us for
+//            offsets left their fp32 rounding, 2^-24 of 136 times all weights: 2 us less for
 //            the batch below, but its output 0.0029 instead of 0.0023 off (relative, root mean square).
 // P (keys x heads) becomes the second product's operand by an 8 x 8 transpose between lanes
 // (movmatrix). Sums of products, softmax statistics and sums are fp32; rounding p * scale to bf16 (2^-8
@@ -40,14 +40,16 @@
 // with 8 warps), and waits for them alone; no warp waits for another one until the merge.
 //
 // Measured (8 kv heads of 128 dims): 64 requests of up to 8,449 keys, 64 query heads (308 MB, 46 us at
-// the copy rate) 89 us, 0.52 of that rate; one request of 32,897 keys, 32 query heads (38 MB, 5.7 us) 24 us,
-// of which about 8 us is fixed: the batch's prefix sums, the first copies, the merges. What bounds the
-// batch is the instructions: about 360 per record and warp, 175 of them on the integer pipe, which takes one
-// every other cycle, so 350 cycles per record for a scheduler, 0.9 of the bytes' time; three warps per
-// scheduler overlap them with the products and the exponentials to 1.6 times that. With 14 and 16 warps,
-// of fewer registers, the batch takes 96 and 94 us. Records two to a copy (92 us then), Q in
-// shared memory to make room for 16 warps (105), shifts as multiplications (96), and K in e4m3 with Q in two
-// terms (102; 3 instructions per 8 codes, but such a product costs more than two in fp16) were not faster.
+// the copy rate) 88 us, 0.52 of that rate; one request of 32,897 keys, 32 query heads (38 MB, 5.7 us) 22 us:
+// the first records arrive after 3.3 us, a warp's ten take 9, the merges 5 (a CTA's own, the ticket, the parts).
+// Runs of equal length by CTA instead of by warp are slower, 92 us for the batch. What bounds the batch
+// is the instructions: about 360 per record and warp, 175 of them on the integer pipe, which takes one every
+// other cycle, so 350 cycles per record for a scheduler, 0.9 of the bytes' time; three warps per scheduler
+// overlap them with the products and the exponentials to 1.6 times that. With 14 and 16 warps, of fewer
+// registers, the batch takes 96 and 94 us. Records two to a copy (92 us then) or two at a time through the
+// registers (88 against 89), Q in shared memory to make room for 16 warps (105), shifts as multiplications (96),
+// and K in e4m3 with Q in two terms (102; 3 instructions per 8 codes, but such a product costs more than
+// two in fp16) were slower or no gain.
 #include "common.cuh"
 #include "kernels.h"
 #include "attn_common.cuh"
