@@ -87,6 +87,30 @@ def test_page_tables(cb, n, most_ctx, most_new, page, pad):
     plan.close()
 
 
+@pytest.mark.parametrize("shift", [0, 1, 2])
+def test_page_tables_rows_at_any_address(cb, shift):
+    # rows that are no multiple of four, in buffers off a 16-byte boundary, with rows before and behind them kept
+    rng = np.random.default_rng(48)
+    plan = _plan(cb, 4, 2, 64)
+    ctx, new = rng.integers(0, 90, 9), rng.integers(0, 60, 9)
+    new[3] = 0
+    rows = int(new.sum()) + 6
+    free, width = rng.permutation(99), 12
+    have = -(-ctx // 16)
+    table = np.where(np.arange(width) < have[:, None], 100 + np.arange(9 * width).reshape(9, width), -1)
+    t, pos, slots = _i32(table), _i32(np.full(rows + 8, -7)), _i32(np.full(rows + 8, -7))
+    cu, kv, to = _i32([0] * 10), _i32([0] * 9), _i32([0])
+    cb.cb_page_tables(plan, _i32(ctx), _i32(new), 16, _i32(free), t, cu, kv, pos[shift:shift + rows], slots[shift:shift + rows], to)
+    plan.check()
+    want = serving.page_tables(ctx.tolist(), new.tolist(), 16, free, table, rows)
+    for got, w in ((pos, want[3]), (slots, want[4])):
+        got = got.cpu().numpy()
+        assert np.array_equal(got[shift:shift + rows], w)
+        assert (got[:shift] == -7).all() and (got[shift + rows:] == -7).all()
+    assert np.array_equal(t.cpu().numpy(), want[0])
+    plan.close()
+
+
 def test_page_tables_without_requests_or_rows(cb):
     plan = _plan(cb, 4, 2, 64)
     t, cu, kv, pos, slots, to = _tables(cb, plan, [], [], 16, [1, 2], np.zeros((0, 4)), 5, free_from=1)
