@@ -263,12 +263,15 @@ def cb_page_tables(plan, ctx_lens, new_lens, page_size, free_pages, table, cu_se
     positions and slots [n_rows], free_from and free_to [1]; all int32 on the device."""
     n, rows, free = _size(ctx_lens, "ctx_lens"), _size(slots, "slots"), _size(free_pages, "free_pages")
     width = _size(table, "table", 1, 2)
-    arg = lambda t, name, *shape: _arg(plan, t, torch.int32, shape, name)  # noqa: E731
+    i32, per_request, per_row, one = torch.int32, (n,), (rows,), (1,)
     check(_lib.load().cb_page_tables(
-        plan.handle, arg(ctx_lens, "ctx_lens", n), arg(new_lens, "new_lens", n), n, page_size,
-        arg(free_pages, "free_pages", free), free, arg(free_from, "free_from", 1), arg(table, "table", n, width), width,
-        arg(cu_seqlens, "cu_seqlens", n + 1), arg(kv_lens, "kv_lens", n), arg(positions, "positions", rows),
-        arg(slots, "slots", rows), rows, arg(free_to, "free_to", 1), _plan_stream(plan, stream)))
+        plan.handle, _arg(plan, ctx_lens, i32, per_request, "ctx_lens"), _arg(plan, new_lens, i32, per_request, "new_lens"),
+        n, page_size, _arg(plan, free_pages, i32, (free,), "free_pages"), free,
+        None if free_from is None else _arg(plan, free_from, i32, one, "free_from"),
+        _arg(plan, table, i32, (n, width), "table"), width, _arg(plan, cu_seqlens, i32, (n + 1,), "cu_seqlens"),
+        _arg(plan, kv_lens, i32, per_request, "kv_lens"), _arg(plan, positions, i32, per_row, "positions"),
+        _arg(plan, slots, i32, per_row, "slots"), rows, _arg(plan, free_to, i32, one, "free_to"),
+        _plan_stream(plan, stream)))
 
 
 def _kv4_rows(plan, k, v, slots):
