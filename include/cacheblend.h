@@ -416,9 +416,9 @@ cb_status cb_kv4_load(cb_plan* plan, const void* cache, int32_t n_pages, int32_t
  * accumulation; the softmax weights times V's scales are rounded to bf16 before the product.
  * Recorded as CB_ERR_DEVICE_CHECK: a negative length (as 0), one past table_width * P (cut there), a
  * table entry outside [0, n_pages) (its keys are left out). n_seqs * hkv * table_width * P must stay below
- * 2^34 (CB_ERR_UNSUPPORTED). out must not be q. Partial results meet in the plan's scratch: calls of
- * this function on one plan must not overlap on the GPU; order them on one stream, or give each
- * stream its own plan. */
+ * 2^34 (CB_ERR_UNSUPPORTED). out must not be q. A bounded wait that gives up records CB_ERR_TIMEOUT.
+ * Partial results meet in the plan's scratch: calls of this function on one plan must not overlap on
+ * the GPU; order them on one stream, or give each stream its own plan. */
 cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,
                                   const int32_t* table, int32_t table_width, const int32_t* kv_lens, int32_t n_seqs,
                                   float scale, void* out, void* stream);

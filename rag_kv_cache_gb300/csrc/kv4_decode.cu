@@ -79,6 +79,13 @@ __device__ __forceinline__ int take_ticket(int32_t* at) {
   return before;
 }
 
+// The wait for a record's copy. One that takes longer than the limit is recorded (the call's result is void),
+// but the copy is waited for all the same, with the limit again: no copy may be in flight when its stage is asked
+// for anew or the CTA ends.
+__device__ __noinline__ void wait_record(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* err) {
+  if (!mbar_spin_slow_body(bar, parity, abort_flag, err, 80, kTimeoutNs)) mbar_wait(bar, parity, abort_flag, err, 81, false);
+}
+
 struct Masks {
   uint32_t nibbles, higher, bias, minus;
 };
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
       reset(st);
       int keys = len_of(s) - at.i * kKv4Block;  // from the record on
       for (int i = 0; i < count; ++i, keys -= kKv4Block) {
-        mbar_spin(bar0 + 8 * stage, parity, abort_flag, p.err, 80);
+        if (!mbar_test(bar0 + 8 * stage, parity)) wait_record(bar0 + 8 * stage, parity, abort_flag, p.err);
         __syncwarp();
         const uint32_t rec = ring + stage * kRecord;
         if (keys >= kKv4Block && !(bad >> stage & 1))
