@@ -764,19 +764,21 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
     const int g1 = group_end(g0);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (uint32_t some = held & (0xffffffffu >> (32 - g1)) & ~((1u << g0) - 1); some != 0;) {
-      int k[4];  // up to four slots at a time
+      // Up to four slots at a time. A slot that holds something is added whatever its weight: 0 times a NaN is
+      // NaN here as within a warp's run and over CTAs, so a value that is not finite shows however the batch was split.
+      const int here = __popc(some);
       float wk[4];
       float4 v[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        k[u] = some ? __ffs(some) - 1 : g0;
-        wk[u] = some ? s_weight[k[u]][head] : 0.0f;
+        const int k = u < here ? __ffs(some) - 1 : g0;
+        wk[u] = s_weight[k][head];
         some &= some - 1;
-        v[u] = *reinterpret_cast<const float4*>(slot_at(k[u]) + at * 4);
+        v[u] = *reinterpret_cast<const float4*>(slot_at(k) + at * 4);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if (wk[u] == 0.0f) continue;  // (a slot of no keys, or none: 0 times what is not finite)
+        if (u >= here) continue;
         acc.x = fmaf(wk[u], v[u].x, acc.x);
         acc.y = fmaf(wk[u], v[u].y, acc.y);
         acc.z = fmaf(wk[u], v[u].z, acc.z);

@@ -959,3 +959,39 @@ def test_binding_refuses_wrong_tensors(cb):
         cb.cb_page_tables(plan, i32(3), i32(3), 16, i32(9), i32(3, 4), i32(4), i32(3), i32(5), i32(5), None)
     plan.check()
     plan.close()
+
+
+# ---- values that are not finite, however the batch is split --------------------------------------
+
+
+@pytest.mark.parametrize("others", [[], [0] * 3 + [7000], [30, 9000, 9000, 9000], [600] * 60])
+def test_decode_value_that_is_not_finite_under_a_weight_of_nothing(cb, others):
+    # Keys 96 to 511 of request 0 score 180 below the others: e^-180 is 0 in 32 bits. One of their values is NaN, which
+    # every split of the batch (runs of 1 to 4 records per warp, within one CTA or over several) has to show, in its group
+    # alone.
+    rng = np.random.default_rng(50 + len(others))
+    hq, hkv, d, page = 8, 2, 128, 32
+    plan = _plan(cb, hq, hkv, d)
+    lens = [640] + others
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, page)
+    base = np.sign(rng.standard_normal((hkv, d)))
+    q = _bits(rng, len(lens), hq, d)
+    q[0] = f32_to_bf16_bits(np.repeat(base, hq // hkv, 0).astype(np.float32))
+    low = (np.arange(640) >= 96) & (np.arange(640) < 512)
+    k = f32_to_bf16_bits((np.where(low, -8.0, 8.0)[:, None, None] * base + 0.1 * rng.standard_normal((640, hkv, d)))
+                         .astype(np.float32))
+    v = _bits(rng, 640, hkv, d)
+    slots = _i32(table[0][np.arange(640) // page] * page + np.arange(640) % page)
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), slots, cache, page)
+    bad = v[300:301].copy()
+    bad[0, 0, 33] = 0x7F80  # its group of 32 dims of kv head 0 stands for NaN
+    cb.cb_kv4_store(plan, bf16_tensor(k[300:301].copy()), bf16_tensor(bad), slots[300:301], cache, page)
+    out = torch.empty((len(lens), hq, d), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32(lens), out)
+    plan.check()
+    got = _f64(out)
+    assert np.isnan(got[0, :4, 32:64]).all()
+    ks[0], vs[0] = (serving.dequantise(*serving.quantise(bf16_bits_to_f64(x))) for x in (k, v))
+    got[0, :4, 32:64] = decode_attention(bf16_bits_to_f64(q)[0], ks[0], vs[0])[:4, 32:64]
+    _check_decode(plan, q, bf16_tensor(f32_to_bf16_bits(got.astype(np.float32))), ks, vs, "beside it")
+    plan.close()
