@@ -382,8 +382,8 @@ int32_t cb_kv4_page_bytes(const cb_plan* plan, int32_t page_size);
  *   positions  [n_rows]      position of each packed new token, 0 behind the last one
  *   slots      [n_rows]      its slot (for cb_kv4_store), -1 behind the last one
  *   free_to    [1]           free_from + the pages taken
- * free_from: device int32, NULL = 0. kv_lens must be another buffer than the lengths, free_to another
- * than free_from. n_seqs is at most CB_PAGE_TABLES_MAX_SEQS. Recorded as CB_ERR_DEVICE_CHECK: a
+ * free_from: device int32, NULL = 0. The six outputs (the table among them) must overlap neither one of
+ * the four inputs nor one another (CB_ERR_INVALID_ARG). n_seqs is at most CB_PAGE_TABLES_MAX_SEQS. Recorded as CB_ERR_DEVICE_CHECK: a
  * negative length (taken as 0); a request past table_width * P tokens (its kv_lens is cut there, the
  * tokens behind get slot -1); a free list that runs out or holds an id below 0 or whose slots would
  * pass 2^31 - 1 (table entry and slots -1); a token that falls in a held page whose table entry is no

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <string>
 #include <vector>
 
@@ -107,6 +108,28 @@ cb_status check_kv4_cache(int32_t n_pages, int32_t page_size) {
     return fail(CB_ERR_INVALID_ARG, "page_size %d: a multiple of 16 up to %d is required", page_size, CB_KV4_MAX_PAGE);
   if ((int64_t)n_pages * page_size > 0x7fffffffll)
     return fail(CB_ERR_INVALID_ARG, "n_pages * page_size above 2^31 - 1");
+  return CB_OK;
+}
+
+// A buffer of a call, for the check that what it writes lies apart from what it reads.
+struct Span {
+  const void* at;
+  int64_t bytes;
+  const char* name;
+};
+bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at != nullptr && b.at != nullptr && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes &&
+         y < x + (uintptr_t)a.bytes;
+}
+// No output may overlap an input or another output, not in part either.
+cb_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (meet(*o, i)) return fail(CB_ERR_INVALID_ARG, "%s overlaps %s", o->name, i.name);
+    for (const Span* other = outs.begin(); other != o; ++other)
+      if (meet(*o, *other)) return fail(CB_ERR_INVALID_ARG, "%s overlaps %s", o->name, other->name);
+  }
   return CB_OK;
 }
 
@@ -564,10 +587,22 @@ cb_status cb_page_tables(cb_plan* plan, const int32_t* ctx_lens, const int32_t* 
   }
   CB_TRY(need_ptr(cu_seqlens, "cu_seqlens"));
   CB_TRY(need_ptr(free_to, "free_to"));
-  // every block reads all lengths and the start of the free list, so no block may write over them
+  // Every block reads all lengths, the start of the free list and the pages that it gives out, each at a time of its
+  // own, so no block may write over them.
   if (n_seqs > 0 && (kv_lens == ctx_lens || kv_lens == new_lens))
     return fail(CB_ERR_INVALID_ARG, "kv_lens must not be ctx_lens or new_lens");
   if (free_to == free_from) return fail(CB_ERR_INVALID_ARG, "free_to must not be free_from");
+  const int64_t per_request = 4 * (int64_t)n_seqs, per_row = 4 * (int64_t)n_rows;
+  CB_TRY(check_apart({{table, per_request * table_width, "table"},
+                      {cu_seqlens, per_request + 4, "cu_seqlens"},
+                      {kv_lens, per_request, "kv_lens"},
+                      {positions, per_row, "positions"},
+                      {slots, per_row, "slots"},
+                      {free_to, 4, "free_to"}},
+                     {{ctx_lens, per_request, "ctx_lens"},
+                      {new_lens, per_request, "new_lens"},
+                      {free_pages, 4 * (int64_t)n_free, "free_pages"},
+                      {free_from, 4, "free_from"}}));
   CB_TRY(check_device(plan));
   return cuda_status(cb::launch_page_tables(ctx_lens, new_lens, n_seqs, page_size, free_pages, n_free, free_from, table,
                                             table_width, cu_seqlens, kv_lens, positions, slots, n_rows, free_to,

@@ -995,3 +995,27 @@ def test_decode_value_that_is_not_finite_under_a_weight_of_nothing(cb, others):
     got[0, :4, 32:64] = decode_attention(bf16_bits_to_f64(q)[0], ks[0], vs[0])[:4, 32:64]
     _check_decode(plan, q, bf16_tensor(f32_to_bf16_bits(got.astype(np.float32))), ks, vs, "beside it")
     plan.close()
+
+
+def test_page_tables_in_one_buffer(cb):
+    # every array a slice of one buffer, each right behind the one before: neighbours are no overlap
+    rng = np.random.default_rng(51)
+    plan, n, width, rows = _plan(cb, 4, 2, 64), 7, 5, 90
+    ctx, new = rng.integers(0, 40, n), rng.integers(0, 13, n)
+    have = -(-ctx // 16)
+    table = np.where(np.arange(width) < have[:, None], 50 + np.arange(n * width).reshape(n, width), -1)
+    free = rng.permutation(30)
+    parts = [ctx, new, free, [2], table, np.full(n + 1, -7), np.full(n, -7), np.full(rows, -7), np.full(rows, -7), [-7]]
+    whole = _i32(np.concatenate([np.ravel(x) for x in parts]))
+    t = list(whole.split([np.size(x) for x in parts]))
+    t[4] = t[4].view(n, width)
+    cb.cb_page_tables(plan, t[0], t[1], 16, t[2], *t[4:], free_from=t[3])
+    plan.check()
+    want = serving.page_tables(ctx.tolist(), new.tolist(), 16, free, table, rows, 2)
+    for got, w in zip(t[4:], want):
+        assert np.array_equal(got.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+    assert np.array_equal(torch.cat(t[:4]).cpu().numpy(), np.concatenate([ctx, new, free, [2]]))
+    # a decode step whose positions would be written over its lengths
+    with pytest.raises(cb.CacheBlendError, match="positions overlaps ctx_lens"):
+        cb.cb_page_tables(plan, t[0], t[1], 16, t[2], t[4], t[5], t[6], t[0][:n], t[8][:n], t[9])
+    plan.close()

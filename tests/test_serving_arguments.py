@@ -156,3 +156,22 @@ def test_binding_checks_shapes_before_the_library(lib, plan):
         cb.cb_page_tables(p, i32(3), i32(2), 16, i32(9), i32(3, 4), i32(4), i32(3), i32(5), i32(5), i32(1))
     with pytest.raises(ValueError, match="free_pages must have 1 dim"):
         cb.cb_page_tables(p, i32(3), i32(3), 16, i32(9, 1), i32(3, 4), i32(4), i32(3), i32(5), i32(5), i32(1))
+
+
+TABLES = {"ctx_lens": 16, "new_lens": 16, "free_pages": 36, "free_from": 4, "table": 128, "cu_seqlens": 20, "kv_lens": 16,
+          "positions": 20, "slots": 20, "free_to": 4}  # bytes: 4 requests, 9 free pages, 8 pages a row, 5 rows
+
+
+@pytest.mark.parametrize("out", ["table", "cu_seqlens", "kv_lens", "positions", "slots", "free_to"])
+@pytest.mark.parametrize("other", list(TABLES))
+@pytest.mark.parametrize("where", ["first bytes", "last bytes"])
+def test_page_tables_outputs_lie_apart(lib, plan, out, other, where):
+    if out == other:
+        return
+    at = {name: P + 4096 * i for i, name in enumerate(TABLES)}
+    # the output ends one element inside the other buffer, or begins on its last one
+    at[out] = at[other] - TABLES[out] + 4 if where == "first bytes" else at[other] + TABLES[other] - 4
+    a = [at[name] for name in TABLES]
+    got = lib.cb_page_tables(plan, a[0], a[1], 4, 16, a[2], 9, a[3], a[4], 8, a[5], a[6], a[7], a[8], 5, a[9], None)
+    said = lib.cb_last_error_string().decode()
+    assert got == 1 and out in said and other in said and ("overlaps" in said or "must not be" in said), said
