@@ -397,13 +397,14 @@ cb_status cb_page_tables(cb_plan* plan, const int32_t* ctx_lens, const int32_t* 
 
 /* Quantise rows k, v [n, hkv, D] (as attention reads them: keys RoPE-encoded) into the cache at
  * slots[i]. A negative slot skips its row (padding); one past the cache is skipped and recorded.
- * Slots of one call must differ (the content of a slot named twice is a mix of its rows). */
+ * Slots of one call must differ (the content of a slot named twice is a mix of its rows). The cache must
+ * not overlap k, v or slots. */
 cb_status cb_kv4_store(cb_plan* plan, const void* k, const void* v, const int32_t* slots, int32_t n, void* cache,
                        int32_t n_pages, int32_t page_size, void* stream);
 
 /* Read rows back: k[i], v[i] [n, hkv, D] = bf16(scale * code) of slots[i], e.g. a stored chunk's
  * k_old / v_old for cb_blend_layer. A negative slot leaves its rows as they are; one past the cache
- * too, and is recorded. */
+ * too, and is recorded. k and v must overlap neither one another nor the cache or slots. */
 cb_status cb_kv4_load(cb_plan* plan, const void* cache, int32_t n_pages, int32_t page_size, const int32_t* slots,
                       int32_t n, void* k, void* v, void* stream);
 
@@ -416,7 +417,7 @@ cb_status cb_kv4_load(cb_plan* plan, const void* cache, int32_t n_pages, int32_t
  * accumulation; the softmax weights times V's scales are rounded to bf16 before the product.
  * Recorded as CB_ERR_DEVICE_CHECK: a negative length (as 0), one past table_width * P (cut there), a
  * table entry outside [0, n_pages) (its keys are left out). n_seqs * hkv * table_width * P must stay below
- * 2^34 (CB_ERR_UNSUPPORTED). out must not be q. A bounded wait that gives up records CB_ERR_TIMEOUT.
+ * 2^34 (CB_ERR_UNSUPPORTED). out must overlap no input. A bounded wait that gives up records CB_ERR_TIMEOUT.
  * Partial results meet in the plan's scratch: calls of this function on one plan must not overlap on
  * the GPU; order them on one stream, or give each stream its own plan. */
 cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,
@@ -431,7 +432,7 @@ cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cach
  * within [0, n_rows], n_seqs at most CB_PROMPT_MAX_SEQS; empty sequences are allowed, and rows in no
  * sequence keep their out. Values of keys that a row does not see (later ones, other sequences') do
  * not reach it, whatever they are. scale <= 0 selects 1/sqrt(D). fp32 accumulation and softmax, bf16 P,
- * bf16 output; tcgen05 (TMEM accumulators) fed by TMA. out must be none of the inputs. Offsets that fall or leave [0, n_rows] are
+ * bf16 output; tcgen05 (TMEM accumulators) fed by TMA. out must overlap no input. Offsets that fall or leave [0, n_rows] are
  * recorded as CB_ERR_DEVICE_CHECK (clipped, a falling pair read as empty). No scratch: calls on one
  * plan may overlap. A bounded wait that gives up records CB_ERR_TIMEOUT. */
 #define CB_PROMPT_MAX_SEQS 16384

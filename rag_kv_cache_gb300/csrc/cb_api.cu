@@ -133,6 +133,10 @@ cb_status check_apart(std::initializer_list<Span> outs, std::initializer_list<Sp
   return CB_OK;
 }
 
+Span cache_span(const cb_plan* plan, const void* cache, int32_t n_pages, int32_t page_size) {
+  return Span{cache, (int64_t)n_pages * plan->cfg.hkv * (page_size / 16 * 18 * plan->cfg.head_dim), "cache"};
+}
+
 cb::RopeTable table(const cb_plan* p) { return cb::RopeTable{p->rope_tab, p->n_tokens}; }
 
 int32_t k_for_ratio(int32_t r_pct, int32_t n_ctx) {
@@ -620,6 +624,9 @@ static cb_status kv4_rows(const char* fn, bool store, cb_plan* plan, void* k, vo
   CB_TRY(need_tensor(v, "v"));
   CB_TRY(need_ptr(slots, "slots"));
   if (n_pages > 0) CB_TRY(need_tensor(cache, "cache"));
+  const int64_t rows = (int64_t)n * plan->cfg.hkv * plan->cfg.head_dim * 2;
+  const Span ks{k, rows, "k"}, vs{v, rows, "v"}, ss{slots, 4 * (int64_t)n, "slots"}, cs = cache_span(plan, cache, n_pages, page_size);
+  CB_TRY(store ? check_apart({cs}, {ks, vs, ss}) : check_apart({ks, vs}, {cs, ss}));
   CB_TRY(check_device(plan));
   return cuda_status(cb::launch_kv4_rows(store, k, v, slots, n, cache, n_pages, page_size, plan->cfg.hkv,
                                          plan->cfg.head_dim, plan->err, static_cast<cudaStream_t>(stream)),
@@ -658,6 +665,11 @@ cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cach
   CB_TRY(need_ptr(kv_lens, "kv_lens"));
   CB_TRY(need_tensor(out, "out"));
   if (out == q) return fail(CB_ERR_INVALID_ARG, "out must not be q");
+  const int64_t rows = (int64_t)n_seqs * c.hq * c.head_dim * 2;
+  CB_TRY(check_apart({{out, rows, "out"}}, {{q, rows, "q"},
+                                            cache_span(plan, cache, n_pages, page_size),
+                                            {table, 4 * (int64_t)n_seqs * table_width, "table"},
+                                            {kv_lens, 4 * (int64_t)n_seqs, "kv_lens"}}));
   CB_TRY(check_device(plan));
   if (!(scale > 0.0f)) scale = 1.0f / std::sqrt((float)c.head_dim);
   return cuda_status(cb::launch_kv4_decode(q, cache, n_pages, page_size, table, table_width, kv_lens, n_seqs, c.hq,
@@ -682,6 +694,11 @@ cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const
   CB_TRY(need_ptr(cu_seqlens, "cu_seqlens"));
   CB_TRY(need_tensor(out, "out"));
   if (out == q || out == k || out == v) return fail(CB_ERR_INVALID_ARG, "out must not be q, k or v");
+  const int64_t q_row = (int64_t)c.hq * c.head_dim * 2, kv_row = (int64_t)c.hkv * c.head_dim * 2;
+  CB_TRY(check_apart({{out, n_rows * q_row, "out"}}, {{q, n_rows * q_row, "q"},
+                                                      {k, n_rows * kv_row, "k"},
+                                                      {v, n_rows * kv_row, "v"},
+                                                      {cu_seqlens, 4 * ((int64_t)n_seqs + 1), "cu_seqlens"}}));
   CB_TRY(check_device(plan));
   if (!(scale > 0.0f)) scale = 1.0f / std::sqrt((float)c.head_dim);
   return cuda_status(cb::launch_prompt_attention(q, k, v, cu_seqlens, n_seqs, n_rows, c.hq, c.hkv, c.head_dim, scale,

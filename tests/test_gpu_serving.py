@@ -1019,3 +1019,20 @@ def test_page_tables_in_one_buffer(cb):
     with pytest.raises(cb.CacheBlendError, match="positions overlaps ctx_lens"):
         cb.cb_page_tables(plan, t[0], t[1], 16, t[2], t[4], t[5], t[6], t[0][:n], t[8][:n], t[9])
     plan.close()
+
+
+def test_prompt_over_neighbouring_buffers(cb):
+    # q, k, v and out as neighbours in one buffer are no overlap; out half a batch into q is
+    rng = np.random.default_rng(52)
+    plan, n = _plan(cb, 8, 2, 64), 70
+    q, k, v = _bits(rng, n, 8, 64), _bits(rng, n, 2, 64), _bits(rng, n, 2, 64)
+    whole = torch.cat([bf16_tensor(x).view(-1) for x in (q, k, v)] + [torch.full((n * 512,), 9.0, dtype=torch.bfloat16, device="cuda")])
+    dq, dk, dv, out = (x.view(n, -1, 64) for x in whole.split([n * 512, n * 128, n * 128, n * 512]))
+    cb.cb_prompt_attention(plan, dq, dk, dv, _i32([0, 40, 70]), out)
+    plan.check()
+    _check_prompt(q, k, v, [0, 40, 70], out, "neighbours")
+    assert torch.equal(dq.contiguous().view(torch.int16), bf16_tensor(q).view(torch.int16))
+    half = whole[n * 256:n * 768].view(n, 8, 64)
+    with pytest.raises(cb.CacheBlendError, match="out overlaps q"):
+        cb.cb_prompt_attention(plan, dq, dk, dv, _i32([0, 40, 70]), half)
+    plan.close()

@@ -175,3 +175,35 @@ def test_page_tables_outputs_lie_apart(lib, plan, out, other, where):
     got = lib.cb_page_tables(plan, a[0], a[1], 4, 16, a[2], 9, a[3], a[4], 8, a[5], a[6], a[7], a[8], 5, a[9], None)
     said = lib.cb_last_error_string().decode()
     assert got == 1 and out in said and other in said and ("overlaps" in said or "must not be" in said), said
+
+
+@pytest.mark.parametrize("where", ["first bytes", "last bytes"])
+def test_rows_and_attention_outputs_lie_apart(lib, plan, where):
+    row, kv = 8 * 128 * 2, 2 * 128 * 2  # bytes of a row of q and out, of k and v
+    cache = 4 * 2 * 18 * 128  # four pages of 16 tokens, two kv heads
+
+    def place(sizes, out, other):
+        at = {name: P + (i << 16) for i, name in enumerate(sizes)}
+        at[out] = at[other] - sizes[out] + 16 if where == "first bytes" else at[other] + (sizes[other] - 1) // 16 * 16
+        return at
+
+    def overlaps(got, out, other):
+        said = lib.cb_last_error_string().decode()
+        assert got == 1 and "overlaps" in said and out in said and other in said, said
+
+    sizes = {"k": 3 * kv, "v": 3 * kv, "slots": 12, "cache": cache}
+    for other in ("k", "v", "slots"):
+        a = place(sizes, "cache", other)
+        overlaps(lib.cb_kv4_store(plan, a["k"], a["v"], a["slots"], 3, a["cache"], 4, 16, None), "cache", other)
+    for out, other in (("k", "v"), ("k", "cache"), ("k", "slots"), ("v", "k"), ("v", "cache"), ("v", "slots")):
+        a = place(sizes, out, other)
+        overlaps(lib.cb_kv4_load(plan, a["cache"], 4, 16, a["slots"], 3, a["k"], a["v"], None), out, other)
+    sizes = {"q": 3 * row, "cache": cache, "table": 24, "kv_lens": 12, "out": 3 * row}
+    for other in ("q", "cache", "table", "kv_lens"):
+        a = place(sizes, "out", other)
+        overlaps(lib.cb_kv4_decode_attention(plan, a["q"], a["cache"], 4, 16, a["table"], 2, a["kv_lens"], 3, 0.0, a["out"], None),
+                 "out", other)
+    sizes = {"q": 9 * row, "k": 9 * kv, "v": 9 * kv, "cu_seqlens": 12, "out": 9 * row}
+    for other in ("q", "k", "v", "cu_seqlens"):
+        a = place(sizes, "out", other)
+        overlaps(lib.cb_prompt_attention(plan, a["q"], a["k"], a["v"], a["cu_seqlens"], 2, 9, 0.0, a["out"], None), "out", other)
