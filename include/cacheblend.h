@@ -486,6 +486,20 @@ cb_status cb_test_decode_wait_timeout(cb_plan* plan, const void* q, const void* 
 cb_status cb_test_projection_wait_timeout(cb_plan* plan, const void* x, int32_t d_model, int32_t m,
                                           const void* w_qkv, void* q, void* k, void* v, void* stream);
 
+/* Test support for the failure path, not part of the blend (the pages have no
+ * counterpart). Runs cb_kv4_decode_attention's kernel (head_dim 128, hq / hkv at
+ * most 8) in a form where every warp waits for a second record that it never
+ * copies, and every bounded wait gives up after 100 us instead of 2 s: each warp
+ * whose share of the batch is two records (16 keys of one kv head) or more records
+ * CB_ERR_TIMEOUT in the plan's error word, asks for no more records, waits (again
+ * bounded) for those in flight and still takes part in the merges, so the ticket
+ * counters stay consistent; the contents of `out` are undefined. The next cb_check
+ * reports CB_ERR_TIMEOUT and clears the word, and the device and the plan stay
+ * usable. Arguments as cb_kv4_decode_attention (scale 1/sqrt(D)). */
+cb_status cb_test_kv4_decode_wait_timeout(cb_plan* plan, const void* q, const void* cache, int32_t n_pages,
+                                          int32_t page_size, const int32_t* table, int32_t table_width,
+                                          const int32_t* kv_lens, int32_t n_seqs, void* out, void* stream);
+
 /* Synchronise the plan's device, read and clear its error word. Returns
  * CB_OK, CB_ERR_TIMEOUT or CB_ERR_DEVICE_CHECK (detail in
  * cb_last_error_string). Off the hot path. */

@@ -21,7 +21,7 @@ __all__ = ["Plan", "CacheBlendError", "cb_rope_rerotate", "cb_kv_deviation", "cb
            "cb_blend_request", "cb_hkvd_select_noalloc", "cb_kv4_page_bytes", "cb_page_tables", "cb_kv4_store",
            "cb_kv4_load", "cb_kv4_decode_attention", "cb_prompt_attention", "cb_attention_uses_paired_tiles",
            "cb_test_attention_wait_timeout", "cb_test_decode_wait_timeout", "cb_test_projection_wait_timeout",
-           "cb_check", "cb_version",
+           "cb_test_kv4_decode_wait_timeout", "cb_check", "cb_version",
            "LayerBuffers"]
 
 
@@ -295,16 +295,22 @@ def cb_kv4_load(plan, cache, page_size, slots, k, v, stream=None):
     check(_lib.load().cb_kv4_load(plan.handle, pc, n_pages, page_size, ps, n, pk, pv, _plan_stream(plan, stream)))
 
 
-def cb_kv4_decode_attention(plan, q, cache, page_size, table, kv_lens, out, scale=0.0, stream=None):
-    """One decode step of a batch: q, out [n, Hq, D] over the pages table [n, width] of the 4-bit cache,
-    kv_lens [n] keys each (0: zeros)."""
+def _kv4_decode_args(plan, q, cache, page_size, table, kv_lens):
+    """The batch's arguments from q to n_seqs, and the shape of q and out."""
     n, width = _size(kv_lens, "kv_lens"), _size(table, "table", 1, 2)
     shape = (n, plan.hq, plan.head_dim)
     pc, n_pages = _kv4_cache(plan, cache, page_size)
-    check(_lib.load().cb_kv4_decode_attention(
-        plan.handle, _arg(plan, q, torch.bfloat16, shape, "q"), pc, n_pages, page_size,
-        _arg(plan, table, torch.int32, (n, width), "table"), width, _arg(plan, kv_lens, torch.int32, (n,), "kv_lens"), n,
-        float(scale), _arg(plan, out, torch.bfloat16, shape, "out"), _plan_stream(plan, stream)))
+    return shape, (_arg(plan, q, torch.bfloat16, shape, "q"), pc, n_pages, page_size,
+                   _arg(plan, table, torch.int32, (n, width), "table"), width,
+                   _arg(plan, kv_lens, torch.int32, (n,), "kv_lens"), n)
+
+
+def cb_kv4_decode_attention(plan, q, cache, page_size, table, kv_lens, out, scale=0.0, stream=None):
+    """One decode step of a batch: q, out [n, Hq, D] over the pages table [n, width] of the 4-bit cache,
+    kv_lens [n] keys each (0: zeros)."""
+    shape, args = _kv4_decode_args(plan, q, cache, page_size, table, kv_lens)
+    check(_lib.load().cb_kv4_decode_attention(plan.handle, *args, float(scale), _arg(plan, out, torch.bfloat16, shape, "out"),
+                                              _plan_stream(plan, stream)))
 
 
 def cb_prompt_attention(plan, q, k, v, cu_seqlens, out, scale=0.0, stream=None):
@@ -330,6 +336,13 @@ def cb_test_decode_wait_timeout(plan, q, k, v, n_keys, out, stream=None):
     check(_lib.load().cb_test_decode_wait_timeout(
         plan.handle, _ptr(q, torch.bfloat16, "q"), _ptr(k, torch.bfloat16, "k"), _ptr(v, torch.bfloat16, "v"),
         n_keys, _ptr(out, torch.bfloat16, "out"), _stream(stream)))
+
+
+def cb_test_kv4_decode_wait_timeout(plan, q, cache, page_size, table, kv_lens, out, stream=None):
+    """The batch decode over 4-bit pages in a form whose bounded waits run out (see cacheblend.h; test support)."""
+    shape, args = _kv4_decode_args(plan, q, cache, page_size, table, kv_lens)
+    check(_lib.load().cb_test_kv4_decode_wait_timeout(plan.handle, *args, _arg(plan, out, torch.bfloat16, shape, "out"),
+                                                      _plan_stream(plan, stream)))
 
 
 def cb_test_projection_wait_timeout(plan, x, m, w_qkv, q, k, v, stream=None):

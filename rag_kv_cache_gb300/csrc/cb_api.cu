@@ -646,10 +646,9 @@ cb_status cb_kv4_load(cb_plan* plan, const void* cache, int32_t n_pages, int32_t
   return kv4_rows("cb_kv4_load", false, plan, k, v, slots, n, const_cast<void*>(cache), n_pages, page_size, stream);
 }
 
-cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,
-                                  const int32_t* table, int32_t table_width, const int32_t* kv_lens, int32_t n_seqs,
-                                  float scale, void* out, void* stream) {
-  CB_NVTX_RANGE();
+static cb_status kv4_decode(const char* fn, bool probe, cb_plan* plan, const void* q, const void* cache, int32_t n_pages,
+                            int32_t page_size, const int32_t* table, int32_t table_width, const int32_t* kv_lens,
+                            int32_t n_seqs, float scale, void* out, void* stream) {
   CB_TRY(check_plan(plan));
   CB_TRY(check_kv4_cache(n_pages, page_size));
   const auto& c = plan->cfg;
@@ -672,10 +671,31 @@ cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cach
                                             {kv_lens, 4 * (int64_t)n_seqs, "kv_lens"}}));
   CB_TRY(check_device(plan));
   if (!(scale > 0.0f)) scale = 1.0f / std::sqrt((float)c.head_dim);
-  return cuda_status(cb::launch_kv4_decode(q, cache, n_pages, page_size, table, table_width, kv_lens, n_seqs, c.hq,
-                                           c.hkv, c.head_dim, scale, out, plan->kv4, plan->err,
-                                           static_cast<cudaStream_t>(stream)),
-                     "cb_kv4_decode_attention");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(probe ? cb::launch_kv4_decode_timeout_probe(q, cache, n_pages, page_size, table, table_width, kv_lens,
+                                                                 n_seqs, c.hq, c.hkv, scale, out, plan->kv4, plan->err, s)
+                           : cb::launch_kv4_decode(q, cache, n_pages, page_size, table, table_width, kv_lens, n_seqs, c.hq,
+                                                   c.hkv, c.head_dim, scale, out, plan->kv4, plan->err, s),
+                     fn);
+}
+
+cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,
+                                  const int32_t* table, int32_t table_width, const int32_t* kv_lens, int32_t n_seqs,
+                                  float scale, void* out, void* stream) {
+  CB_NVTX_RANGE();
+  return kv4_decode("cb_kv4_decode_attention", false, plan, q, cache, n_pages, page_size, table, table_width, kv_lens,
+                    n_seqs, scale, out, stream);
+}
+
+cb_status cb_test_kv4_decode_wait_timeout(cb_plan* plan, const void* q, const void* cache, int32_t n_pages,
+                                          int32_t page_size, const int32_t* table, int32_t table_width,
+                                          const int32_t* kv_lens, int32_t n_seqs, void* out, void* stream) {
+  CB_NVTX_RANGE();
+  CB_TRY(check_plan(plan));
+  if (plan->cfg.head_dim != 128 || plan->cfg.hq > 8 * plan->cfg.hkv)
+    return fail(CB_ERR_UNSUPPORTED, "the wait-timeout probe needs head_dim 128 and hq / hkv of at most 8");
+  return kv4_decode("cb_test_kv4_decode_wait_timeout", true, plan, q, cache, n_pages, page_size, table, table_width,
+                    kv_lens, n_seqs, 0.0f, out, stream);
 }
 
 cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const void* v, const int32_t* cu_seqlens,

@@ -177,6 +177,13 @@ cudaError_t launch_kv4_decode(const void* q, const void* cache, int32_t n_pages,
                               int32_t hkv, int32_t head_dim, float scale, void* out, const Kv4Scratch& ws,
                               int32_t* err, cudaStream_t s);
 
+// Test support: the same kernel (head_dim 128, at most 8 query heads per kv head) in a form where the second record of
+// every warp never arrives and whose waits give up after kProbeTimeoutNs.
+cudaError_t launch_kv4_decode_timeout_probe(const void* q, const void* cache, int32_t n_pages, int32_t page_size,
+                                            const int32_t* table, int32_t width, const int32_t* lens, int32_t n_seqs,
+                                            int32_t hq, int32_t hkv, float scale, void* out, const Kv4Scratch& ws,
+                                            int32_t* err, cudaStream_t s);
+
 // Causal attention of packed prompts; prompt_items is the most work items a launch can have.
 int64_t prompt_items(int32_t n_seqs, int32_t n_rows, int32_t hq, int32_t hkv);
 cudaError_t launch_prompt_attention(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,

@@ -40,7 +40,7 @@
 // with 8 warps), and waits for them alone; no warp waits for another one until the merge.
 //
 // Measured (8 kv heads of 128 dims): 64 requests of up to 8,449 keys, 64 query heads (308 MB, 46 us at
-// the copy rate) 88 us, 0.52 of that rate; one request of 32,897 keys, 32 query heads (38 MB, 5.7 us) 22 us:
+// the copy rate) 89 us, 0.52 of that rate; one request of 32,897 keys, 32 query heads (38 MB, 5.7 us) 22 us:
 // the first records arrive after 3.3 us, a warp's ten take 9, the merges 5 (a CTA's own, the ticket, the parts).
 // Runs of equal length by CTA instead of by warp are slower, 92 us for the batch. What bounds the batch
 // is the instructions: about 360 per record and warp, 175 of them on the integer pipe, which takes one every
@@ -79,11 +79,26 @@ __device__ __forceinline__ int take_ticket(int32_t* at) {
   return before;
 }
 
-// The wait for a record's copy. One that takes longer than the limit is recorded (the call's result is void),
-// but the copy is waited for all the same, with the limit again: no copy may be in flight when its stage is asked
-// for anew or the CTA ends.
-__device__ __noinline__ void wait_record(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* err) {
-  if (!mbar_spin_slow_body(bar, parity, abort_flag, err, 80, kTimeoutNs)) mbar_wait(bar, parity, abort_flag, err, 81, false);
+// The wait for a record's copy; false if the limit ran out: the timeout is recorded and the warp's abort flag raised,
+// so that its later waits return at once; the call's result is void.
+__device__ __noinline__ bool wait_record(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* err,
+                                         uint64_t limit_ns) {
+  return !*abort_flag && mbar_spin_slow_body(bar, parity, abort_flag, err, 80, limit_ns);
+}
+// After it: the lane that asks for the records waits once more for those in flight, from stage `stage` of the ring on,
+// for as long as the limit again for all of them together, and asks for no more (returns false): a barrier whose phase
+// has not completed must not be armed again. So no copy is under way when the ring is used for something else or
+// the CTA ends, unless it takes longer than both limits. (A flag that the lane tests before each request and the wait's
+// result cost 1 us of 88; asking on after the second limit, as it was without them, armed such a barrier.)
+__device__ __noinline__ bool stop_requests(uint32_t bar0, int stage, uint32_t parity, int stages, int in_flight,
+                                           uint64_t limit_ns) {
+  const uint64_t t0 = global_timer();
+  for (int k = 0; k < in_flight; ++k) {
+    while (!mbar_try_wait_sleep(bar0 + 8 * stage, parity) && global_timer() - t0 <= limit_ns) {
+    }
+    if (++stage == stages) stage = 0, parity ^= 1;
+  }
+  return false;
 }
 
 struct Masks {
@@ -441,8 +456,12 @@ __device__ __forceinline__ void write_out4(uint8_t* out, int64_t row, int D, int
 // 1 / l, and 0 for a sum over nothing.
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
-template <int D, int NT>
+// PROBE: the wait-timeout probe (test support only): every warp arms the barrier of its second record but never
+// copies it, and the waits give up after kProbeTimeoutNs, so each warp with two records or more takes its failure
+// path. The kernel itself has no part of it.
+template <int D, int NT, bool PROBE = false>
 __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const Kv4DecodeParams p) {
+  constexpr uint64_t kLimit = PROBE ? kProbeTimeoutNs : kTimeoutNs;
   constexpr int NG = Kv4<D>::kGroups;
   constexpr int kWarps = kWarpsOf<NT>, kThreads = kWarps * 32;
   constexpr int kSlot = kSlotFloats<D, NT>;
@@ -591,7 +610,9 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
     };
     // The warp's own producer: records in the order of its run, kStages ahead. `run` records from src on
     // are neighbours in a page; behind them the next page's id comes from lane (page index - w0) of a
-    // window of 32 entries of the table's row. All lanes keep the producer's state, lane 0 acts.
+    // window of 32 entries of the table's row. All lanes keep the producer's state, the leader (lane 0, until a
+    // wait of its own gives up) acts.
+    bool leader = lane == 0;
     Place to = at;       // first record behind the neighbours
     int left = rest;     // records still to request
     int run = 0, w0 = 0, ws = -1;
@@ -621,16 +642,17 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
       if (run == 0) next_page();
       if (page_ok) {
         bad &= ~fill_bit;
-        if (lane == 0) {
+        if (leader) {
           mbar_expect_tx(fill_bar, kRecord);
-          asm volatile(
-              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(fill_dst),
-              "l"(src), "r"(kRecord), "r"(fill_bar)
-              : "memory");
+          if (!(PROBE && left == a_end - a0 - 1))
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(fill_dst),
+                "l"(src), "r"(kRecord), "r"(fill_bar)
+                : "memory");
         }
       } else {
         bad |= fill_bit;
-        if (lane == 0) mbar_arrive(fill_bar);  // the phase passes without a copy
+        if (leader) mbar_arrive(fill_bar);  // the phase passes without a copy
       }
       src += kRecord;
       --run;
@@ -653,7 +675,10 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
       reset(st);
       int keys = len_of(s) - at.i * kKv4Block;  // from the record on
       for (int i = 0; i < count; ++i, keys -= kKv4Block) {
-        if (!mbar_test(bar0 + 8 * stage, parity)) wait_record(bar0 + 8 * stage, parity, abort_flag, p.err);
+        // (after a wait that gave up, the rest of the run goes over whatever the stages hold)
+        if (!mbar_test(bar0 + 8 * stage, parity) &&
+            !wait_record(bar0 + 8 * stage, parity, abort_flag, p.err, kLimit) && leader)
+          leader = stop_requests(bar0, stage, parity, kStages, rest - i - left, kLimit);
         __syncwarp();
         const uint32_t rec = ring + stage * kRecord;
         if (keys >= kKv4Block && !(bad >> stage & 1))
@@ -914,7 +939,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool PROBE = false>
 cudaError_t launch_t(const Kv4DecodeParams& p, int32_t sms, cudaStream_t s) {
   constexpr int kWarps = kWarpsOf<NT>;
   const int64_t most = (int64_t)p.n_seqs * p.hkv * p.width * (p.page_size / kKv4Block);  // records at most
@@ -926,17 +951,14 @@ cudaError_t launch_t(const Kv4DecodeParams& p, int32_t sms, cudaStream_t s) {
   if (grid < 1) grid = 1;
   const size_t smem = (size_t)kWarps * kWarpBytes<D, NT>;
   static std::atomic<uint64_t> configured{0};
-  const cudaError_t e = set_smem_limit_once(kv4_decode_kernel<D, NT>, (int)smem, configured);
+  const cudaError_t e = set_smem_limit_once(kv4_decode_kernel<D, NT, PROBE>, (int)smem, configured);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_decode_kernel<D, NT>, dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p);
+  return launch_pdl(kv4_decode_kernel<D, NT, PROBE>, dim3((unsigned)grid), dim3(kWarps * 32), smem, s, p);
 }
 
-}  // namespace
-
-cudaError_t launch_kv4_decode(const void* q, const void* cache, int32_t n_pages, int32_t page_size,
-                              const int32_t* table, int32_t width, const int32_t* lens, int32_t n_seqs, int32_t hq,
-                              int32_t hkv, int32_t head_dim, float scale, void* out, const Kv4Scratch& ws,
-                              int32_t* err, cudaStream_t s) {
+Kv4DecodeParams params_of(const void* q, const void* cache, int32_t n_pages, int32_t page_size, const int32_t* table,
+                          int32_t width, const int32_t* lens, int32_t n_seqs, int32_t hq, int32_t hkv, float scale,
+                          void* out, const Kv4Scratch& ws, int32_t* err) {
   Kv4DecodeParams p;
   p.q = static_cast<const uint8_t*>(q);
   p.cache = static_cast<const uint8_t*>(cache);
@@ -955,10 +977,30 @@ cudaError_t launch_kv4_decode(const void* q, const void* cache, int32_t n_pages,
   p.part_ml = ws.part_ml;
   p.tickets = ws.tickets;
   p.err = err;
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_decode(const void* q, const void* cache, int32_t n_pages, int32_t page_size,
+                              const int32_t* table, int32_t width, const int32_t* lens, int32_t n_seqs, int32_t hq,
+                              int32_t hkv, int32_t head_dim, float scale, void* out, const Kv4Scratch& ws,
+                              int32_t* err, cudaStream_t s) {
+  const Kv4DecodeParams p =
+      params_of(q, cache, n_pages, page_size, table, width, lens, n_seqs, hq, hkv, scale, out, ws, err);
   const bool wide = p.G > 8;
   if (head_dim == 128) return wide ? launch_t<128, 2>(p, ws.sms, s) : launch_t<128, 1>(p, ws.sms, s);
   if (head_dim == 64) return wide ? launch_t<64, 2>(p, ws.sms, s) : launch_t<64, 1>(p, ws.sms, s);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_kv4_decode_timeout_probe(const void* q, const void* cache, int32_t n_pages, int32_t page_size,
+                                            const int32_t* table, int32_t width, const int32_t* lens, int32_t n_seqs,
+                                            int32_t hq, int32_t hkv, float scale, void* out, const Kv4Scratch& ws,
+                                            int32_t* err, cudaStream_t s) {
+  const Kv4DecodeParams p =
+      params_of(q, cache, n_pages, page_size, table, width, lens, n_seqs, hq, hkv, scale, out, ws, err);
+  return launch_t<128, 1, true>(p, ws.sms, s);
 }
 
 }  // namespace cb

@@ -130,3 +130,50 @@ def test_projection_wait_timeout_is_reported_and_the_device_stays_usable(cb):
                                            q, k, v)  # d_model 64: no K step 1 to miss
     assert e.value.status == 1
     plan.close()
+
+
+@pytest.mark.parametrize("lens", [[33000, 700, 40], [900, 0, 17]])
+def test_kv4_decode_wait_timeout_is_reported_and_the_plan_stays_usable(cb, lens):
+    # cb_test_kv4_decode_wait_timeout: every warp waits for a second record that it never copies, for 100 us. Each warp
+    # with two records or more records the timeout, asks for no more, waits for the copies in flight and joins the
+    # merges (over CTAs in the first batch, a CTA per kv head in the second); a normal decode on the same plan right
+    # after (the same tickets and partial results) must match the oracle.
+    from oracle import serving
+    from oracle.attention import decode_attention
+
+    hq, hkv, d, page = 16, 2, 128, 64
+    plan = cb.Plan(1, 1, 0, hq, hkv, d, 1e4)
+    rng = np.random.default_rng(406 + sum(lens))
+    q = f32_to_bf16_bits(rng.standard_normal((len(lens), hq, d)).astype(np.float32))
+    k, v = (f32_to_bf16_bits(rng.standard_normal((sum(lens), hkv, d)).astype(np.float32)) for _ in range(2))
+    need = [-(-n // page) for n in lens]
+    table = np.full((len(lens), max(need)), -1, dtype=np.int32)
+    ids = rng.permutation(sum(need))
+    for s, n in enumerate(need):
+        table[s, :n] = ids[sum(need[:s]):sum(need[:s + 1])]
+    slots = np.concatenate([table[s][np.arange(n) // page] * page + np.arange(n) % page for s, n in enumerate(lens)])
+    i32 = lambda x: torch.as_tensor(np.asarray(x, dtype=np.int32)).cuda()  # noqa: E731
+    cache = torch.zeros((sum(need), hkv, cb.cb_kv4_page_bytes(plan, page)), dtype=torch.uint8, device="cuda")
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), i32(slots), cache, page)
+    plan.check()
+    ks, vs = (serving.dequantise(*serving.quantise(bf16_bits_to_f64(x))) for x in (k, v))
+    cut = np.cumsum([0] + lens)
+    ref = np.zeros((len(lens), hq, d))
+    for s, (a, b) in enumerate(zip(cut, cut[1:])):
+        if b > a:
+            ref[s] = decode_attention(bf16_bits_to_f64(q)[s], ks[a:b], vs[a:b])
+    dq, dt, dl = bf16_tensor(q), i32(table), i32(lens)
+    out = torch.zeros((len(lens), hq, d), dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):  # the failure and the recovery, twice in a row
+        t0 = time.perf_counter()
+        cb.cb_test_kv4_decode_wait_timeout(plan, dq, cache, page, dt, dl, out)
+        with pytest.raises(cb.CacheBlendError) as e:
+            plan.check()
+        assert e.value.status == 4 and "flags 0x8 " in str(e.value)
+        assert time.perf_counter() - t0 < 30.0
+        plan.check()
+        out.zero_()
+        cb.cb_kv4_decode_attention(plan, dq, cache, page, dt, dl, out)
+        plan.check()
+        assert_close_bf16(bf16_bits_to_f64(bf16_bits(out)), ref, what="batch decode after a timed-out launch")
+    plan.close()

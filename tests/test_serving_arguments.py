@@ -207,3 +207,20 @@ def test_rows_and_attention_outputs_lie_apart(lib, plan, where):
     for other in ("q", "k", "v", "cu_seqlens"):
         a = place(sizes, "out", other)
         overlaps(lib.cb_prompt_attention(plan, a["q"], a["k"], a["v"], a["cu_seqlens"], 2, 9, 0.0, a["out"], None), "out", other)
+
+
+def test_decode_wait_timeout_probe_refusals(lib, plan):
+    from rag_kv_cache_gb300 import _lib
+
+    def call(plan_=plan, q=P, cache=P + (1 << 16), table=P + (1 << 17), width=4, lens=P + (1 << 18), n=3, out=P + (1 << 19)):
+        return lib.cb_test_kv4_decode_wait_timeout(plan_, q, cache, 2, 16, table, width, lens, n, out, None)
+
+    _refused(lib, call(plan_=None), "plan")
+    for name, said in (("q", "q"), ("cache", "cache"), ("table", "table"), ("lens", "kv_lens"), ("out", "out")):
+        _refused(lib, call(**{name: None}), said)
+    _refused(lib, call(out=P + 16), "overlaps")
+    for heads, dim in ((16, 128), (8, 64)):  # 16 query heads per kv head, 64 dims
+        cfg = _lib.CbConfig(1, 1, 0, heads, 1, dim, 1e4, 0, 15, 15)
+        raw = ctypes.create_string_buffer(4096)
+        ctypes.memmove(raw, ctypes.byref(cfg), ctypes.sizeof(cfg))
+        _refused(lib, call(plan_=raw), "head_dim 128", 2)
