@@ -57,6 +57,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "attn_common.cuh"
 #include "attn_tile.cuh"
@@ -820,12 +821,14 @@ cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const i
   // The register split: the block is launched with numRegs per thread and setmaxnreg moves them
   // between the warpgroups; a build with fewer than the split needs would wait forever in
   // setmaxnreg.inc, so it is never launched.
-  static int regs = -1;
+  static std::atomic<int> known{-1};  // (threads may make their first calls at once)
+  int regs = known.load(std::memory_order_relaxed);
   if (regs < 0) {
     cudaFuncAttributes a;
     const cudaError_t e = cudaFuncGetAttributes(&a, prompt_attention_kernel<D>);
     if (e != cudaSuccess) return e;
     regs = a.numRegs;
+    known.store(regs, std::memory_order_relaxed);
   }
   if (regs * kThreads < kTiles * kSoftmaxThreads * kSoftmaxRegs + kSoftmaxThreads * kOtherRegs)
     return cudaErrorNotSupported;

@@ -1036,3 +1036,53 @@ def test_prompt_over_neighbouring_buffers(cb):
     with pytest.raises(cb.CacheBlendError, match="out overlaps q"):
         cb.cb_prompt_attention(plan, dq, dk, dv, _i32([0, 40, 70]), half)
     plan.close()
+
+
+def test_calls_from_many_threads(cb):
+    # each thread makes every serving call on a plan and stream of its own, all at the same time
+    import threading
+
+    jobs, errors = [], []
+    for i in range(6):
+        rng = np.random.default_rng(60 + i)
+        d, page, lens = (64, 128)[i % 2], 16, [33 + 7 * i, 0, 150]
+        n, rows = len(lens), sum(lens) + 2
+        plan, free = _plan(cb, 8, 2, d), rng.permutation(40)
+        q, k, v = _bits(rng, rows, 8, d), _bits(rng, rows, 2, d), _bits(rng, rows, 2, d)
+        q1 = _bits(rng, n, 8, d)
+        t = dict(ctx=_i32([0] * n), new=_i32(lens), free=_i32(free), table=_i32(np.full((n, 12), -1)), cu=_i32([0] * (n + 1)),
+                 kv=_i32([0] * n), pos=_i32([0] * rows), slots=_i32([0] * rows), to=_i32([0]),
+                 cache=torch.zeros(40, 2, cb.cb_kv4_page_bytes(plan, page), dtype=torch.uint8, device="cuda"),
+                 out=torch.full((rows, 8, d), 9.0, dtype=torch.bfloat16, device="cuda"),
+                 out1=torch.zeros(n, 8, d, dtype=torch.bfloat16, device="cuda"), s=torch.cuda.Stream())
+        jobs.append((plan, lens, page, (q, k, v, q1), [bf16_tensor(x) for x in (q, k, v, q1)], t))
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(jobs))
+
+    def work(plan, lens, page, _, dev, t):
+        try:
+            q, k, v, q1 = dev
+            start.wait()
+            for _ in range(10):
+                cb.cb_page_tables(plan, t["ctx"], t["new"], page, t["free"], t["table"], t["cu"], t["kv"], t["pos"], t["slots"],
+                                  t["to"], stream=t["s"])
+                cb.cb_kv4_store(plan, k, v, t["slots"], t["cache"], page, stream=t["s"])
+                cb.cb_prompt_attention(plan, q, k, v, t["cu"], t["out"], stream=t["s"])
+                cb.cb_kv4_decode_attention(plan, q1, t["cache"], page, t["table"], t["kv"], t["out1"], stream=t["s"])
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for plan, lens, page, (q, k, v, q1), _, t in jobs:
+        plan.check()
+        cu = np.cumsum([0] + lens)
+        _check_prompt(q, k, v, cu, t["out"], "threads")
+        ks, vs = ([serving.dequantise(*serving.quantise(bf16_bits_to_f64(x[a:b]))) for a, b in zip(cu, cu[1:])] for x in (k, v))
+        _check_decode(plan, q1, t["out1"], ks, vs, "threads")
+        plan.close()
