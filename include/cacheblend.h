@@ -500,6 +500,21 @@ cb_status cb_test_kv4_decode_wait_timeout(cb_plan* plan, const void* q, const vo
                                           int32_t page_size, const int32_t* table, int32_t table_width,
                                           const int32_t* kv_lens, int32_t n_seqs, void* out, void* stream);
 
+/* Test support for the failure path, not part of the blend (the pages have no
+ * counterpart). Runs cb_prompt_attention's kernel (head_dim 128 only) in a form
+ * whose K producer never copies the second key tile that its CTA takes, and whose
+ * bounded waits give up after 100 us instead of 2 s (an item of work is waited for
+ * for 50 ms instead of 10 s): each CTA that takes two key tiles or more (a query
+ * row past its sequence's first 128, or a second item of work) records
+ * CB_ERR_TIMEOUT in the plan's error word, ends its list of items, walks through
+ * the rounds of those it has without work, waits (again bounded) for its own copies
+ * and tensor-core work, frees its tensor memory and returns; rows of `out` are
+ * written or left as they were. The next cb_check reports CB_ERR_TIMEOUT and clears
+ * the word, and the device and the plan stay usable. Arguments as
+ * cb_prompt_attention (scale 1/sqrt(D)). */
+cb_status cb_test_prompt_wait_timeout(cb_plan* plan, const void* q, const void* k, const void* v,
+                                      const int32_t* cu_seqlens, int32_t n_seqs, int32_t n_rows, void* out, void* stream);
+
 /* Synchronise the plan's device, read and clear its error word. Returns
  * CB_OK, CB_ERR_TIMEOUT or CB_ERR_DEVICE_CHECK (detail in
  * cb_last_error_string). Off the hot path. */

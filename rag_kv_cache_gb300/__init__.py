@@ -21,7 +21,7 @@ __all__ = ["Plan", "CacheBlendError", "cb_rope_rerotate", "cb_kv_deviation", "cb
            "cb_blend_request", "cb_hkvd_select_noalloc", "cb_kv4_page_bytes", "cb_page_tables", "cb_kv4_store",
            "cb_kv4_load", "cb_kv4_decode_attention", "cb_prompt_attention", "cb_attention_uses_paired_tiles",
            "cb_test_attention_wait_timeout", "cb_test_decode_wait_timeout", "cb_test_projection_wait_timeout",
-           "cb_test_kv4_decode_wait_timeout", "cb_check", "cb_version",
+           "cb_test_kv4_decode_wait_timeout", "cb_test_prompt_wait_timeout", "cb_check", "cb_version",
            "LayerBuffers"]
 
 
@@ -313,17 +313,22 @@ def cb_kv4_decode_attention(plan, q, cache, page_size, table, kv_lens, out, scal
                                               _plan_stream(plan, stream)))
 
 
-def cb_prompt_attention(plan, q, k, v, cu_seqlens, out, scale=0.0, stream=None):
-    """Causal attention of packed prompts: q, out [n_rows, Hq, D], k, v [n_rows, Hkv, D], sequence s in
-    rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 on the device); rows in none keep their out."""
+def _prompt_args(plan, q, k, v, cu_seqlens):
+    """The packed prompts' arguments from q to n_rows, and the shape of q and out."""
     rows, n = _size(q, "q", 0, 3), _size(cu_seqlens, "cu_seqlens")
     if n == 0:
         raise ValueError("cu_seqlens must hold at least the first offset")
     bf, q_shape, kv_shape = torch.bfloat16, (rows, plan.hq, plan.head_dim), (rows, plan.hkv, plan.head_dim)
-    check(_lib.load().cb_prompt_attention(
-        plan.handle, _arg(plan, q, bf, q_shape, "q"), _arg(plan, k, bf, kv_shape, "k"), _arg(plan, v, bf, kv_shape, "v"),
-        _arg(plan, cu_seqlens, torch.int32, (n,), "cu_seqlens"), n - 1, rows, float(scale),
-        _arg(plan, out, bf, q_shape, "out"), _plan_stream(plan, stream)))
+    return q_shape, (_arg(plan, q, bf, q_shape, "q"), _arg(plan, k, bf, kv_shape, "k"), _arg(plan, v, bf, kv_shape, "v"),
+                     _arg(plan, cu_seqlens, torch.int32, (n,), "cu_seqlens"), n - 1, rows)
+
+
+def cb_prompt_attention(plan, q, k, v, cu_seqlens, out, scale=0.0, stream=None):
+    """Causal attention of packed prompts: q, out [n_rows, Hq, D], k, v [n_rows, Hkv, D], sequence s in
+    rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 on the device); rows in none keep their out."""
+    shape, args = _prompt_args(plan, q, k, v, cu_seqlens)
+    check(_lib.load().cb_prompt_attention(plan.handle, *args, float(scale), _arg(plan, out, torch.bfloat16, shape, "out"),
+                                          _plan_stream(plan, stream)))
 
 
 def cb_attention_uses_paired_tiles(plan, mq) -> bool:
@@ -343,6 +348,13 @@ def cb_test_kv4_decode_wait_timeout(plan, q, cache, page_size, table, kv_lens, o
     shape, args = _kv4_decode_args(plan, q, cache, page_size, table, kv_lens)
     check(_lib.load().cb_test_kv4_decode_wait_timeout(plan.handle, *args, _arg(plan, out, torch.bfloat16, shape, "out"),
                                                       _plan_stream(plan, stream)))
+
+
+def cb_test_prompt_wait_timeout(plan, q, k, v, cu_seqlens, out, stream=None):
+    """Packed prompt attention in a form whose bounded waits run out (see cacheblend.h; test support)."""
+    shape, args = _prompt_args(plan, q, k, v, cu_seqlens)
+    check(_lib.load().cb_test_prompt_wait_timeout(plan.handle, *args, _arg(plan, out, torch.bfloat16, shape, "out"),
+                                                  _plan_stream(plan, stream)))
 
 
 def cb_test_projection_wait_timeout(plan, x, m, w_qkv, q, k, v, stream=None):

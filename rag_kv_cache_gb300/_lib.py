@@ -30,7 +30,8 @@ EXPORTS = ("cb_plan_create", "cb_plan_destroy", "cb_layer_sizes", "cb_rope_rerot
            "cb_kv4_page_bytes", "cb_page_tables", "cb_kv4_store", "cb_kv4_load", "cb_kv4_decode_attention",
            "cb_prompt_attention",
            "cb_attention_uses_paired_tiles", "cb_test_attention_wait_timeout", "cb_test_decode_wait_timeout",
-           "cb_test_projection_wait_timeout", "cb_test_kv4_decode_wait_timeout", "cb_check",
+           "cb_test_projection_wait_timeout", "cb_test_kv4_decode_wait_timeout",
+           "cb_test_prompt_wait_timeout", "cb_check",
            "cb_last_error_string", "cb_version")
 
 
@@ -95,6 +96,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "cb_attention_uses_paired_tiles": (i32, [vp, i32]),
         "cb_test_attention_wait_timeout": (i32, [vp, vp, vp, i32, vp, vp, i32, vp, vp]),
         "cb_test_kv4_decode_wait_timeout": (i32, [vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp]),
+        "cb_test_prompt_wait_timeout": (i32, [vp, vp, vp, vp, vp, i32, i32, vp, vp]),
         "cb_test_decode_wait_timeout": (i32, [vp, vp, vp, vp, i32, vp, vp]),
         "cb_test_projection_wait_timeout": (i32, [vp, vp, i32, i32, vp, vp, vp, vp, vp]),
         "cb_check": (i32, [vp]),

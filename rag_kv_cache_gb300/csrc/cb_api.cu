@@ -698,9 +698,9 @@ cb_status cb_test_kv4_decode_wait_timeout(cb_plan* plan, const void* q, const vo
                     kv_lens, n_seqs, 0.0f, out, stream);
 }
 
-cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
-                              int32_t n_seqs, int32_t n_rows, float scale, void* out, void* stream) {
-  CB_NVTX_RANGE();
+static cb_status prompt_attention(const char* fn, bool probe, cb_plan* plan, const void* q, const void* k, const void* v,
+                                  const int32_t* cu_seqlens, int32_t n_seqs, int32_t n_rows, float scale, void* out,
+                                  void* stream) {
   CB_TRY(check_plan(plan));
   const auto& c = plan->cfg;
   if (n_seqs < 0 || n_rows < 0) return fail(CB_ERR_INVALID_ARG, "negative size");
@@ -721,9 +721,26 @@ cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const
                                                       {cu_seqlens, 4 * ((int64_t)n_seqs + 1), "cu_seqlens"}}));
   CB_TRY(check_device(plan));
   if (!(scale > 0.0f)) scale = 1.0f / std::sqrt((float)c.head_dim);
-  return cuda_status(cb::launch_prompt_attention(q, k, v, cu_seqlens, n_seqs, n_rows, c.hq, c.hkv, c.head_dim, scale,
-                                                 out, plan->err, static_cast<cudaStream_t>(stream)),
-                     "cb_prompt_attention");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(probe ? cb::launch_prompt_timeout_probe(q, k, v, cu_seqlens, n_seqs, n_rows, c.hq, c.hkv, scale, out,
+                                                             plan->err, s)
+                           : cb::launch_prompt_attention(q, k, v, cu_seqlens, n_seqs, n_rows, c.hq, c.hkv, c.head_dim,
+                                                         scale, out, plan->err, s),
+                     fn);
+}
+
+cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                              int32_t n_seqs, int32_t n_rows, float scale, void* out, void* stream) {
+  CB_NVTX_RANGE();
+  return prompt_attention("cb_prompt_attention", false, plan, q, k, v, cu_seqlens, n_seqs, n_rows, scale, out, stream);
+}
+
+cb_status cb_test_prompt_wait_timeout(cb_plan* plan, const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
+                                      int32_t n_seqs, int32_t n_rows, void* out, void* stream) {
+  CB_NVTX_RANGE();
+  CB_TRY(check_plan(plan));
+  if (plan->cfg.head_dim != 128) return fail(CB_ERR_UNSUPPORTED, "the wait-timeout probe needs head_dim 128");
+  return prompt_attention("cb_test_prompt_wait_timeout", true, plan, q, k, v, cu_seqlens, n_seqs, n_rows, 0.0f, out, stream);
 }
 
 struct LayerShape {

@@ -189,6 +189,11 @@ int64_t prompt_items(int32_t n_seqs, int32_t n_rows, int32_t hq, int32_t hkv);
 cudaError_t launch_prompt_attention(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,
                                     int32_t n_rows, int32_t hq, int32_t hkv, int32_t head_dim, float scale, void* out,
                                     int32_t* err, cudaStream_t s);
+// Test support: the same kernel (head_dim 128) in a form where the second key tile of every CTA never arrives and
+// whose waits give up after kProbeTimeoutNs.
+cudaError_t launch_prompt_timeout_probe(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,
+                                        int32_t n_rows, int32_t hq, int32_t hkv, float scale, void* out, int32_t* err,
+                                        cudaStream_t s);
 
 // QKV projection of listed rows: q / k / v rows of token t_i = tokens[i] (null: i) from
 // x[x_index[i]] W^T (x_index null: x[i], read in place; else the rows are first copied to

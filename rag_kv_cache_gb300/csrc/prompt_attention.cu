@@ -90,7 +90,10 @@ constexpr int kOtherRegs = 72;     // per thread of WG2 after setmaxnreg.dec
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only when the max grows by > 2^8
 constexpr float kTileSumLimit = 65536.0f;  // a later tile whose P sum exceeds 2^16 moves the reference
 constexpr int64_t kGroupBytes = 48 << 20;  // K and V of the sequences that are taken side by side
-constexpr unsigned long long kItemLimitNs = 5 * kTimeoutNs;  // the producer's own waits end well before
+// Limit of the wait for an item, of a kernel whose other waits give up after limit_ns. It must not run out while the
+// producer lives, since roles that see different lists would miss one another at the named barriers: the producer
+// makes two waits at most before it ends the list, each over at the first look at the clock past its limit (every 1.6 ms).
+__host__ __device__ constexpr uint64_t item_limit(uint64_t limit_ns) { return 5 * limit_ns + 50000000ull; }
 
 __host__ __device__ constexpr uint32_t col_s(int i) { return (uint32_t)(i * kBN); }
 __host__ __device__ constexpr uint32_t col_o(int i, int d) { return 256u + (uint32_t)(i * d); }
@@ -274,11 +277,15 @@ __device__ __forceinline__ bool zero_not_finite(uint32_t tile, int from, int lan
   return found;
 }
 
-template <int D>
+// PROBE: the wait-timeout probe (test support only): the K producer of every CTA arms the barrier of its second key
+// tile but never copies the tile, and the waits give up after kProbeTimeoutNs, so each CTA with two key tiles or more
+// takes its failure path. The kernel itself has no part of it.
+template <int D, bool PROBE = false>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                             const PromptParams p) {
+  constexpr uint64_t kLimit = PROBE ? kProbeTimeoutNs : kTimeoutNs;
   constexpr int kBoxes = D / 64;
   constexpr uint32_t kQBytes = kBM * D * 2;  // one query tile
   constexpr uint32_t kKVBytes = kBN * D * 2;
@@ -342,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!there) {
       const uint64_t t0 = global_timer();
       for (uint32_t n = 1; !(there = mbar_try_wait_sleep(bar, (it / kItems) & 1)); ++n)
-        if ((n & 7u) == 0 && global_timer() - t0 > kItemLimitNs) break;
+        if ((n & 7u) == 0 && global_timer() - t0 > item_limit(kLimit)) break;
     }
     there = __all_sync(0xffffffffu, there);
     if (there) return items[it % kItems].n_kv;
@@ -388,11 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = rounds + j, st = r % kStages;
             // K of round r - 2 held this stage: free once S_1 of that round (issued after S_0) is complete
             if (r >= kStages &&
-                !mbar_wait_inl(smem_u32(&bars.s_full[1][st]), ((r / kStages) - 1) & 1, abort_flag, p.err, 41))
+                !mbar_wait_inl(smem_u32(&bars.s_full[1][st]), ((r / kStages) - 1) & 1, abort_flag, p.err, 41, true,
+                               kLimit))
               return false;
             const uint32_t kb = smem_u32(&bars.k_full[st]);
             mbar_expect_tx(kb, kKVBytes);
-            tma_load_4d(sK0 + st * kKVBytes, &tm_k, kb, 0, x.row0 + j * kBN, 0, x.g);
+            if (!(PROBE && r == 1)) tma_load_4d(sK0 + st * kKVBytes, &tm_k, kb, 0, x.row0 + j * kBN, 0, x.g);
             nk = r + 1;
             return true;
           };
@@ -411,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         // not honouring the abort flag: the answer must have landed before the CTA exits
         const bool there =
-            __all_sync(0xffffffffu, mbar_wait_inl(cb, claims & 1, abort_flag, p.err, 44, false));
+            __all_sync(0xffffffffu, mbar_wait_inl(cb, claims & 1, abort_flag, p.err, 44, false, kLimit));
         ++claims;
         idx = there ? claimed_block(smem_u32(&s_claim)) : -1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before the next answer is written
@@ -420,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Before the CTA can exit, every copy issued must have landed (also after an abort).
       if (lane == 0) {
         for (int r = nk < kStages ? 0 : nk - kStages; r < nk; ++r)
-          mbar_wait_inl(smem_u32(&bars.k_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 57, false);
+          mbar_wait_inl(smem_u32(&bars.k_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 57, false, kLimit);
       }
     } else if (warp == kWarpProducerV) {
       int rounds = 0, nv = 0, nq = 0;  // V tiles, query tiles requested
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = rounds + j, st = r % kStages;
             // V of round r - 2 held this stage: free once P_1 V of that round (after P_0 V) is complete
             ok = r < kStages ||
-                 mbar_wait_inl(smem_u32(&bars.o_done[1][st]), ((r / kStages) - 1) & 1, abort_flag, p.err, 43);
+                 mbar_wait_inl(smem_u32(&bars.o_done[1][st]), ((r / kStages) - 1) & 1, abort_flag, p.err, 43, true, kLimit);
             if (!ok) return;
             const uint32_t vb = smem_u32(&bars.v_full[st]);
             mbar_expect_tx(vb, kKVBytes);
@@ -445,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // is complete. Rows past the sequence's end are other sequences' (or the fill value).
           auto load_q = [&](int i) {
             const int r = rounds - 1;
-            ok = ok && (r < 0 || mbar_wait_inl(smem_u32(&bars.s_full[i][r % kStages]), (r / kStages) & 1, abort_flag, p.err, 42));
+            ok = ok && (r < 0 || mbar_wait_inl(smem_u32(&bars.s_full[i][r % kStages]), (r / kStages) & 1, abort_flag,
+                                               p.err, 42, true, kLimit));
             if (!ok) return;
             const uint32_t qb = smem_u32(&bars.q_full[i]);
             mbar_expect_tx(qb, kQBytes);
@@ -465,17 +474,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0)
         for (int i = 0; i < kTiles; ++i) {
           const int n = (nq + 1 - i) / kTiles;  // tiles i requested
-          if (n > 0) mbar_wait_inl(smem_u32(&bars.q_full[i]), (n - 1) & 1, abort_flag, p.err, 56, false);
+          if (n > 0) mbar_wait_inl(smem_u32(&bars.q_full[i]), (n - 1) & 1, abort_flag, p.err, 56, false, kLimit);
         }
       if (lane == 0)
         for (int r = nv < kStages ? 0 : nv - kStages; r < nv; ++r)
-          mbar_wait_inl(smem_u32(&bars.v_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 58, false);
+          mbar_wait_inl(smem_u32(&bars.v_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 58, false, kLimit);
     } else if (warp == kWarpWaiter) {
       // Per round, its V tile and the item's next K tile, published to the issuer through shared memory
       // before the waiter meets the issuer (and WG0) on a named barrier. Every round is joined, also
       // after a failure.
       auto spin_all = [&](uint32_t bar, uint32_t parity, int site) -> bool {
-        return __all_sync(0xffffffffu, mbar_spin_inl(bar, parity, abort_flag, p.err, site));
+        return __all_sync(0xffffffffu, mbar_spin_inl(bar, parity, abort_flag, p.err, site, kLimit));
       };
       int rounds = 0;
       bool ok = true;
@@ -528,8 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // This warp's own wait for query tile i and the first K tile of item it (round r).
       auto inputs = [&](int i, int it, int r) -> bool {
-        const bool there = mbar_spin_inl(smem_u32(&bars.q_full[i]), it & 1, abort_flag, p.err, 45 + i) &&
-                           mbar_spin_inl(smem_u32(&bars.k_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 47);
+        const bool there = mbar_spin_inl(smem_u32(&bars.q_full[i]), it & 1, abort_flag, p.err, 45 + i, kLimit) &&
+                           mbar_spin_inl(smem_u32(&bars.k_full[r % kStages]), (r / kStages) & 1, abort_flag, p.err, 47,
+                                         kLimit);
         return __all_sync(0xffffffffu, there);
       };
       // An item's first S_i, once per item: as a loop, which leaves the registers to the rounds' products.
@@ -587,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // All tensor-core work issued by this CTA completes before TMEM is freed.
       if (elect_one()) tc_commit(smem_u32(&bars.drain));
       __syncwarp();
-      mbar_wait_inl(smem_u32(&bars.drain), 0, abort_flag, p.err, 49, false);
+      mbar_wait_inl(smem_u32(&bars.drain), 0, abort_flag, p.err, 49, false, kLimit);
     }
     // The two register regions end separately (no common tail after the branch): every warp
     // meets on named barrier 1 before warp 0 frees the tensor memory.
@@ -611,14 +621,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = -INFINITY, l = 0.0f;  // reference max (log2 units) that O_ti and l are scaled to
       auto wait_o = [&](int r, int site) -> bool {
         const bool w =
-            mbar_spin_inl(smem_u32(&bars.o_done[ti][r % kStages]), (r / kStages) & 1, abort_flag, p.err, site);
+            mbar_spin_inl(smem_u32(&bars.o_done[ti][r % kStages]), (r / kStages) & 1, abort_flag, p.err, site, kLimit);
         return __all_sync(0xffffffffu, w);
       };
       // One key tile; false if a wait gave up (the abort flag is raised then).
       auto tile = [&](int j) -> bool {
         const int r = rounds + j;
         if (!__all_sync(0xffffffffu, mbar_spin_inl(smem_u32(&bars.s_full[ti][r % kStages]), (r / kStages) & 1,
-                                                   abort_flag, p.err, 50 + ti)))
+                                                   abort_flag, p.err, 50 + ti, kLimit)))
           return false;
         tc_fence_after();
         uint32_t sv[kBN];  // this row's 128 scores
@@ -812,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool PROBE = false>
 cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,
                             int32_t n_rows, int32_t hq, int32_t hkv, float scale, void* out, int32_t* err,
                             cudaStream_t s) {
@@ -825,7 +835,7 @@ cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const i
   int regs = known.load(std::memory_order_relaxed);
   if (regs < 0) {
     cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, prompt_attention_kernel<D>);
+    const cudaError_t e = cudaFuncGetAttributes(&a, prompt_attention_kernel<D, PROBE>);
     if (e != cudaSuccess) return e;
     regs = a.numRegs;
     known.store(regs, std::memory_order_relaxed);
@@ -862,10 +872,10 @@ cudaError_t launch_prompt_t(const void* q, const void* k, const void* v, const i
   p.err = err;
   const size_t smem = 1024 + (size_t)(kTiles * kBM + 2 * kStages * kBN) * D * 2 + 2 * kSoftmaxThreads / 32 * kOutWarp;
   static std::atomic<uint64_t> configured{0};
-  const cudaError_t e = set_smem_limit_once(prompt_attention_kernel<D>, (int)smem, configured);
+  const cudaError_t e = set_smem_limit_once(prompt_attention_kernel<D, PROBE>, (int)smem, configured);
   if (e != cudaSuccess) return e;
   const int64_t most = prompt_items(n_seqs, n_rows, hq, hkv);
-  return launch_pdl(prompt_attention_kernel<D>, dim3((unsigned)most), dim3(kThreads), smem, s,
+  return launch_pdl(prompt_attention_kernel<D, PROBE>, dim3((unsigned)most), dim3(kThreads), smem, s,
                     tq_map, tk_map, tv_map, to_map, p);
 }
 
@@ -884,6 +894,13 @@ cudaError_t launch_prompt_attention(const void* q, const void* k, const void* v,
     return launch_prompt_t<128>(q, k, v, cu, n_seqs, n_rows, hq, hkv, scale, out, err, s);
   if (head_dim == 64) return launch_prompt_t<64>(q, k, v, cu, n_seqs, n_rows, hq, hkv, scale, out, err, s);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prompt_timeout_probe(const void* q, const void* k, const void* v, const int32_t* cu, int32_t n_seqs,
+                                        int32_t n_rows, int32_t hq, int32_t hkv, float scale, void* out, int32_t* err,
+                                        cudaStream_t s) {
+  if (n_seqs <= 0 || n_rows <= 0) return cudaSuccess;
+  return launch_prompt_t<128, true>(q, k, v, cu, n_seqs, n_rows, hq, hkv, scale, out, err, s);
 }
 
 }  // namespace cb

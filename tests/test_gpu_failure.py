@@ -177,3 +177,33 @@ def test_kv4_decode_wait_timeout_is_reported_and_the_plan_stays_usable(cb, lens)
         plan.check()
         assert_close_bf16(bf16_bits_to_f64(bf16_bits(out)), ref, what="batch decode after a timed-out launch")
     plan.close()
+
+
+@pytest.mark.parametrize("lens", [[300, 5, 700], [64] * 200, [2000, 1, 0, 130, 2000, 900, 64, 2000]])
+def test_prompt_wait_timeout_is_reported_and_the_plan_stays_usable(cb, lens):
+    # cb_test_prompt_wait_timeout: the second key tile of every CTA never arrives (within its first item; as the first tile
+    # of its second item, which it claimed; both) and waits give up after 100 us. Every role of the CTA has to walk to the
+    # end of a list that the producer ends early; a normal call on the same plan right after must match the oracle.
+    from oracle import serving
+
+    hq, hkv, d = 8, 2, 128
+    plan = cb.Plan(1, 1, 0, hq, hkv, d, 1e4)
+    rng = np.random.default_rng(407 + sum(lens))
+    cu, rows = np.cumsum([0] + lens), sum(lens)
+    q, k, v = (f32_to_bf16_bits(rng.standard_normal((rows, h, d)).astype(np.float32)) for h in (hq, hkv, hkv))
+    ref, _ = serving.packed_attention(*(bf16_bits_to_f64(x) for x in (q, k, v)), cu)
+    dq, dk, dv, dc = bf16_tensor(q), bf16_tensor(k), bf16_tensor(v), torch.as_tensor(cu.astype(np.int32)).cuda()
+    out = torch.zeros((rows, hq, d), dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):  # the failure and the recovery, twice in a row
+        t0 = time.perf_counter()
+        cb.cb_test_prompt_wait_timeout(plan, dq, dk, dv, dc, out)
+        with pytest.raises(cb.CacheBlendError) as e:
+            plan.check()
+        assert e.value.status == 4 and "flags 0x8 " in str(e.value)
+        assert time.perf_counter() - t0 < 30.0
+        plan.check()
+        out.zero_()
+        cb.cb_prompt_attention(plan, dq, dk, dv, dc, out)
+        plan.check()
+        assert_close_bf16(bf16_bits_to_f64(bf16_bits(out)), ref, what="prompts after a timed-out launch")
+    plan.close()

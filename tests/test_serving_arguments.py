@@ -224,3 +224,19 @@ def test_decode_wait_timeout_probe_refusals(lib, plan):
         raw = ctypes.create_string_buffer(4096)
         ctypes.memmove(raw, ctypes.byref(cfg), ctypes.sizeof(cfg))
         _refused(lib, call(plan_=raw), "head_dim 128", 2)
+
+
+def test_prompt_wait_timeout_probe_refusals(lib, plan):
+    from rag_kv_cache_gb300 import _lib
+
+    def call(plan_=plan, q=P, k=P + (1 << 16), v=P + (1 << 17), cu=P + (1 << 18), n=2, rows=8, out=P + (1 << 19)):
+        return lib.cb_test_prompt_wait_timeout(plan_, q, k, v, cu, n, rows, out, None)
+
+    _refused(lib, call(plan_=None), "plan")
+    for name, said in (("q", "q"), ("k", "k"), ("v", "v"), ("cu", "cu_seqlens"), ("out", "out")):
+        _refused(lib, call(**{name: None}), said)
+    _refused(lib, call(out=P + 16), "overlaps")
+    cfg = _lib.CbConfig(1, 1, 0, 8, 2, 64, 1e4, 0, 15, 15)
+    raw = ctypes.create_string_buffer(4096)
+    ctypes.memmove(raw, ctypes.byref(cfg), ctypes.sizeof(cfg))
+    _refused(lib, call(plan_=raw), "head_dim 128", 2)
