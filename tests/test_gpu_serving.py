@@ -1086,3 +1086,41 @@ def test_calls_from_many_threads(cb):
         ks, vs = ([serving.dequantise(*serving.quantise(bf16_bits_to_f64(x[a:b]))) for a, b in zip(cu, cu[1:])] for x in (k, v))
         _check_decode(plan, q1, t["out1"], ks, vs, "threads")
         plan.close()
+
+
+@pytest.mark.parametrize("hkv,d", [(2, 64), (8, 128), (1, 64), (3, 128)])
+@pytest.mark.parametrize("n,page", [(10, 16), (130, 64), (333, 48)])
+def test_store_leaves_every_other_byte(cb, hkv, d, n, page):
+    # every byte of the cache after a store row by row, with groups of zeros, tiny, huge and not finite among the rows: the
+    # bytes of other tokens, of padding and of unused slots stay, and a NaN scale is the same bits in each form
+    rng = np.random.default_rng(70 + hkv * n + d)
+    plan = _plan(cb, hkv, hkv, d)
+    n_pages = -(-2 * n // page) + 2
+    slots = rng.permutation(n_pages * page)[:n]
+    slots[2], slots[n - 1] = -1, -5
+    k, v = _bits(rng, n, hkv, d), _bits(rng, n, hkv, d, scale=20.0)
+    for x in (k, v):
+        x[0], x[1, :, 5] = 0, 0xC040
+        x[3] = f32_to_bf16_bits((rng.standard_normal((hkv, d)) * 1e-39).astype(np.float32))
+        x[4] = f32_to_bf16_bits((rng.standard_normal((hkv, d)) * 5e37).astype(np.float32))
+        x[5, 0, 33], x[6, 0, 1], x[7] = 0x7F80, 0x7FC1, 0xFF80
+    before = rng.integers(0, 256, (n_pages, hkv, serving.page_bytes(page, d)), dtype=np.uint8)
+    cache = torch.as_tensor(before).cuda()
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(slots), cache, page)
+    plan.check()
+    want = before.copy()
+    serving.store(want, page, slots, bf16_bits_to_f64(k), bf16_bits_to_f64(v))
+    assert np.array_equal(cache.cpu().numpy(), want)
+    plan.close()
+
+
+def test_page_tables_with_too_few_rows_still_give_out_all_pages(cb):
+    plan = _plan(cb, 4, 2, 64)
+    ctx, new, free, table = [20, 3, 0], [20, 30, 40], [3, 4, 5, 6, 1, 2, 0, 9], [[8, 10, -1], [7, -1, -1], [-1, -1, -1]]
+    t, cu, kv, pos, slots, to = _tables(cb, plan, ctx, new, 16, free, table, 25)
+    with pytest.raises(cb.CacheBlendError):
+        plan.check()
+    want = serving.page_tables(ctx, new, 16, free, table, 25)
+    for got, w in zip((t, cu, kv, pos, slots, to), want):
+        assert np.array_equal(got.reshape(-1), np.asarray(w).reshape(-1))
+    plan.close()
