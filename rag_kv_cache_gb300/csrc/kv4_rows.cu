@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRunThreads = 64, kRunBlocks = 10;  // whole records: threads per block, blocks per SM at least
-constexpr int32_t kRunRows = 4096;
+constexpr int64_t kRunUnits = 32768;  // (row, kv head) pairs of a call that is taken by runs, at least
 
 struct Kv4RowParams {
   const int32_t* slots;
@@ -462,11 +462,15 @@ __global__ void __launch_bounds__(kRunThreads, kRunBlocks)
 
 template <int D, bool STORE>
 cudaError_t launch_rows(void* k, void* v, void* cache, const Kv4RowParams& p, cudaStream_t s) {
-  // By runs from kRunRows rows on, where there are warps enough to take 16 rows each; row by row below. Whole
-  // pages of 8 heads of 128 dims, by runs against row by row, store and load: 2,048 rows 6.2 and 5.1 against
-  // 5.2 and 4.6 us, 4,096 rows 6.6 and 4.6 against 9.2 and 7.8. Scattered slots cost the other way: 4,096
-  // rows 13.8 and 13.4 against 9.2 and 7.9, 32,768 rows 72 and 66 against 71 and 65.
-  const bool runs = p.n >= kRunRows;
+  // By runs from kRunUnits (row, kv head) pairs on, where there are warps enough that take 16 rows each; row by row
+  // below. Whole pages, by runs against row by row, store / load in us: 8 heads of 128 dims 2,048 rows 6.1 / 4.7 against
+  // 5.2 / 4.6, 4,096 rows 6.6 / 4.5 against 9.1 / 7.8; 2 heads of 128, 8,192 rows 6.0 / 4.7 against 5.2 / 4.6, 16,384 rows
+  // 6.5 / 4.5 against 9.1 / 7.8; one head of 64, 16,384 rows 4.0 / 2.9 against 3.4 / 3.0, 32,768 rows 4.4 / 3.8 against
+  // 5.2 / 4.5; 16 heads of 128, 1,024 rows 6.1 / 4.6 against 5.3 / 4.6, 2,048 rows 6.7 / 4.5 against 9.4 / 7.8. (Loads
+  // of whole pages are up to 1.1 faster by runs from 2,048 pairs on.) Scattered slots cost the other way: 32,768 pairs
+  // 13.7 / 11.8 against 9.1 / 7.8 with 128 dims, 17.2 / 16.4 against 5.3 / 4.6 with 64, 8,192 pairs 9.8 / 8.8 against
+  // 3.4 / 3.0; 262,144 pairs 72 / 66 against 71 / 65.
+  const bool runs = (int64_t)p.n * p.hkv >= kRunUnits;
   const int64_t lanes = runs ? ((int64_t)p.n + kKv4Block - 1) / kKv4Block * p.hkv * 32 : (int64_t)p.n * p.hkv * 2 * (D / 8);
   const int threads = runs ? kRunThreads : kThreads;
   const int64_t blocks = (lanes + threads - 1) / threads;

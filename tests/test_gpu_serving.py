@@ -1124,3 +1124,41 @@ def test_page_tables_with_too_few_rows_still_give_out_all_pages(cb):
     for got, w in zip((t, cu, kv, pos, slots, to), want):
         assert np.array_equal(got.reshape(-1), np.asarray(w).reshape(-1))
     plan.close()
+
+
+@pytest.mark.parametrize("hkv,d,page", [(1, 64, 16), (2, 64, 16), (3, 128, 48), (16, 128, 64)])
+@pytest.mark.parametrize("below", [0, 1])
+def test_store_and_load_on_both_sides_of_the_choice(cb, hkv, d, page, below):
+    # the first call that is taken by whole records (32,768 rows times kv heads), and the last that is taken row by row
+    rng = np.random.default_rng(71 + hkv + d)
+    plan = _plan(cb, hkv, hkv, d)
+    n = -(-32768 // hkv) - below
+    n_pages = -(-600 // page) + 2
+    slots = np.full(n, -1)
+    at = 3 if hkv > 2 else 13  # records that begin off the warps' windows, a run that ends inside a record, single rows
+    for start, size in ((0, 48), (64, 37), (112, 16), (131, 5), (160, 240)):
+        slots[at:at + size] = np.arange(start, start + size)
+        at += size + 3
+    rest = np.arange(400, n_pages * page - 16)
+    slots[at:at + 60] = rng.permutation(rest)[:60]
+    slots[n - 16:] = np.arange(n_pages * page - 16, n_pages * page)  # the cache's last record in the call's last rows
+    k, v = (np.zeros((n, hkv, d), np.uint16) for _ in range(2))
+    used = slots >= 0
+    k[used], v[used] = _bits(rng, used.sum(), hkv, d), _bits(rng, used.sum(), hkv, d, scale=9.0)
+    k[20], v[21] = 0, f32_to_bf16_bits((rng.standard_normal((hkv, d)) * 1e-39).astype(np.float32))
+    v[60, 0, 33], k[70, hkv - 1, 1] = 0xFF80, 0x7FC1
+    before = rng.integers(0, 256, (n_pages, hkv, serving.page_bytes(page, d)), dtype=np.uint8)
+    cache = torch.as_tensor(before).cuda()
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(slots), cache, page)
+    want = before.copy()
+    serving.store(want, page, slots[used], bf16_bits_to_f64(k[used]), bf16_bits_to_f64(v[used]))
+    assert np.array_equal(cache.cpu().numpy(), want)
+    ok, ov = (torch.full((n, hkv, d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cb.cb_kv4_load(plan, cache, page, _i32(slots), ok, ov)
+    plan.check()
+    wk, wv = serving.load(want, page, slots[used], d)
+    for g, w in ((ok, wk), (ov, wv)):
+        g, w = _f64(g), serving._to_bf16(w)
+        assert (g[~used] == 7.0).all()
+        assert np.array_equal(np.isnan(g[used]), np.isnan(w)) and np.array_equal(g[used][~np.isnan(w)], w[~np.isnan(w)])
+    plan.close()
