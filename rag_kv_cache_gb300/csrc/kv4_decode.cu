@@ -61,7 +61,6 @@ namespace {
 
 constexpr float kHigh = 256.0f;           // a weight above it moves the reference
 constexpr float kLow = -3e38f;            // reference of a head that has seen nothing
-constexpr int kAlone = 6;                 // records per warp up to which a CTA takes a (request, kv head) alone
 constexpr int kMaxCtas = 160;             // of a launch (one wave: one per SM)
 constexpr float kKOffset = 8.0f / 16777216.0f;  // value of a nibble of K for code 0
 constexpr uint32_t kNibbles = 0x000f000fu;
@@ -425,6 +424,18 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
 template <int NT>
 constexpr int kWarpsOf = NT == 1 ? 12 : 8;
 
+// Records per warp up to which a CTA takes a (request, kv head) alone, where the batch has no more of them than the launch
+// has CTAs. Alone against split, us, 1 to 16 requests of one length:
+//   64 dims, 12 warps (2 kv heads): 960 keys (5 records per warp) 7.5 - 7.8 against 8.3 - 9.0, 1,152 (6) 8.1 - 8.4 against
+//     8.3 - 9.0, 1,280 (7) 8.8 - 8.9 against 8.4 - 9.3;
+//   128 dims, 12 warps (2 and 8 kv heads): 768 (4) 8.5 - 9.0 against 8.9 - 9.2, 960 (5) 9.5 - 10.0 against 9.0 - 10.5, 1,152 (6)
+//     10.4 - 10.8 against 9.0 - 11.0;
+//   16 query heads per kv head, 8 warps (1 and 2 kv heads): 880 keys (7) 9.7 - 13.4 against 9.7 - 17.2, 1,024 (8) 10.4 - 14.5
+//     against 9.8 - 13.0.
+// (A batch of 128 pairs is faster alone at all these lengths, by 3 - 4 us at some.)
+template <int D, int NT>
+constexpr int kAlone = NT == 2 ? 7 : D == 128 ? 5 : 6;
+
 // A partial result's O [heads][D] in shared memory (its references and sums lie in s_ml).
 template <int D, int NT>
 constexpr int kSlotFloats = 8 * NT * D;
@@ -503,7 +514,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   const int warps = gridDim.x * kWarps;
   int quota, cta_records, cta0, cta1;  // records per warp, per CTA, this CTA's first and last
   int run_seq = 0, run_start = 0;      // the request that this warp's run begins in, that request's first record
-  auto alone = [&](int longest) -> bool { return p.n_seqs * p.hkv <= (int)gridDim.x && longest <= kAlone * kWarps; };
+  auto alone = [&](int longest) -> bool { return p.n_seqs * p.hkv <= (int)gridDim.x && longest <= kAlone<D, NT> * kWarps; };
   // A small batch of short requests: a CTA for each (request, kv head), so that none is merged over CTAs.
   auto split_alone = [&]() {
     const int s = blockIdx.x / p.hkv, h = blockIdx.x - s * p.hkv;

@@ -1162,3 +1162,18 @@ def test_store_and_load_on_both_sides_of_the_choice(cb, hkv, d, page, below):
         assert (g[~used] == 7.0).all()
         assert np.array_equal(np.isnan(g[used]), np.isnan(w)) and np.array_equal(g[used][~np.isnan(w)], w[~np.isnan(w)])
     plan.close()
+
+
+@pytest.mark.parametrize("hq,hkv,d,most", [(4, 2, 64, 1152), (8, 2, 128, 960), (16, 1, 64, 896), (32, 2, 128, 896)])
+def test_decode_on_both_sides_of_the_split(cb, hq, hkv, d, most):
+    # the longest request that a CTA takes alone, one key more, and batches beside them
+    rng = np.random.default_rng(72 + hq + d)
+    plan, page = _plan(cb, hq, hkv, d), 32
+    for lens in ([most], [most + 1], [most - 15, 0, 17, most], [1, most + 1, 400]):
+        cache, table, ks, vs = _cache(cb, plan, rng, lens, page)
+        q = _bits(rng, len(lens), hq, d)
+        out = torch.full((len(lens), hq, d), 9.0, dtype=torch.bfloat16, device="cuda")
+        cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32(lens), out)
+        plan.check()
+        _check_decode(plan, q, out, ks, vs, f"lengths {lens}")
+    plan.close()
