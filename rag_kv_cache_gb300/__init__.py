@@ -295,40 +295,29 @@ def cb_kv4_load(plan, cache, page_size, slots, k, v, stream=None):
     check(_lib.load().cb_kv4_load(plan.handle, pc, n_pages, page_size, ps, n, pk, pv, _plan_stream(plan, stream)))
 
 
-def _kv4_decode_args(plan, q, cache, page_size, table, kv_lens):
-    """The batch's arguments from q to n_seqs, and the shape of q and out."""
-    n, width = _size(kv_lens, "kv_lens"), _size(table, "table", 1, 2)
-    shape = (n, plan.hq, plan.head_dim)
-    pc, n_pages = _kv4_cache(plan, cache, page_size)
-    return shape, (_arg(plan, q, torch.bfloat16, shape, "q"), pc, n_pages, page_size,
-                   _arg(plan, table, torch.int32, (n, width), "table"), width,
-                   _arg(plan, kv_lens, torch.int32, (n,), "kv_lens"), n)
-
-
 def cb_kv4_decode_attention(plan, q, cache, page_size, table, kv_lens, out, scale=0.0, stream=None):
     """One decode step of a batch: q, out [n, Hq, D] over the pages table [n, width] of the 4-bit cache,
     kv_lens [n] keys each (0: zeros)."""
-    shape, args = _kv4_decode_args(plan, q, cache, page_size, table, kv_lens)
-    check(_lib.load().cb_kv4_decode_attention(plan.handle, *args, float(scale), _arg(plan, out, torch.bfloat16, shape, "out"),
-                                              _plan_stream(plan, stream)))
-
-
-def _prompt_args(plan, q, k, v, cu_seqlens):
-    """The packed prompts' arguments from q to n_rows, and the shape of q and out."""
-    rows, n = _size(q, "q", 0, 3), _size(cu_seqlens, "cu_seqlens")
-    if n == 0:
-        raise ValueError("cu_seqlens must hold at least the first offset")
-    bf, q_shape, kv_shape = torch.bfloat16, (rows, plan.hq, plan.head_dim), (rows, plan.hkv, plan.head_dim)
-    return q_shape, (_arg(plan, q, bf, q_shape, "q"), _arg(plan, k, bf, kv_shape, "k"), _arg(plan, v, bf, kv_shape, "v"),
-                     _arg(plan, cu_seqlens, torch.int32, (n,), "cu_seqlens"), n - 1, rows)
+    n, width = _size(kv_lens, "kv_lens"), _size(table, "table", 1, 2)
+    shape = (n, plan.hq, plan.head_dim)
+    pc, n_pages = _kv4_cache(plan, cache, page_size)
+    check(_lib.load().cb_kv4_decode_attention(
+        plan.handle, _arg(plan, q, torch.bfloat16, shape, "q"), pc, n_pages, page_size,
+        _arg(plan, table, torch.int32, (n, width), "table"), width, _arg(plan, kv_lens, torch.int32, (n,), "kv_lens"), n,
+        float(scale), _arg(plan, out, torch.bfloat16, shape, "out"), _plan_stream(plan, stream)))
 
 
 def cb_prompt_attention(plan, q, k, v, cu_seqlens, out, scale=0.0, stream=None):
     """Causal attention of packed prompts: q, out [n_rows, Hq, D], k, v [n_rows, Hkv, D], sequence s in
     rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (int32 on the device); rows in none keep their out."""
-    shape, args = _prompt_args(plan, q, k, v, cu_seqlens)
-    check(_lib.load().cb_prompt_attention(plan.handle, *args, float(scale), _arg(plan, out, torch.bfloat16, shape, "out"),
-                                          _plan_stream(plan, stream)))
+    rows, n = _size(q, "q", 0, 3), _size(cu_seqlens, "cu_seqlens")
+    if n == 0:
+        raise ValueError("cu_seqlens must hold at least the first offset")
+    bf, q_shape, kv_shape = torch.bfloat16, (rows, plan.hq, plan.head_dim), (rows, plan.hkv, plan.head_dim)
+    check(_lib.load().cb_prompt_attention(
+        plan.handle, _arg(plan, q, bf, q_shape, "q"), _arg(plan, k, bf, kv_shape, "k"), _arg(plan, v, bf, kv_shape, "v"),
+        _arg(plan, cu_seqlens, torch.int32, (n,), "cu_seqlens"), n - 1, rows, float(scale),
+        _arg(plan, out, bf, q_shape, "out"), _plan_stream(plan, stream)))
 
 
 def cb_attention_uses_paired_tiles(plan, mq) -> bool:
@@ -345,16 +334,23 @@ def cb_test_decode_wait_timeout(plan, q, k, v, n_keys, out, stream=None):
 
 def cb_test_kv4_decode_wait_timeout(plan, q, cache, page_size, table, kv_lens, out, stream=None):
     """The batch decode over 4-bit pages in a form whose bounded waits run out (see cacheblend.h; test support)."""
-    shape, args = _kv4_decode_args(plan, q, cache, page_size, table, kv_lens)
-    check(_lib.load().cb_test_kv4_decode_wait_timeout(plan.handle, *args, _arg(plan, out, torch.bfloat16, shape, "out"),
-                                                      _plan_stream(plan, stream)))
+    n, width = _size(kv_lens, "kv_lens"), _size(table, "table", 1, 2)
+    shape = (n, plan.hq, plan.head_dim)
+    pc, n_pages = _kv4_cache(plan, cache, page_size)
+    check(_lib.load().cb_test_kv4_decode_wait_timeout(
+        plan.handle, _arg(plan, q, torch.bfloat16, shape, "q"), pc, n_pages, page_size,
+        _arg(plan, table, torch.int32, (n, width), "table"), width, _arg(plan, kv_lens, torch.int32, (n,), "kv_lens"), n,
+        _arg(plan, out, torch.bfloat16, shape, "out"), _plan_stream(plan, stream)))
 
 
 def cb_test_prompt_wait_timeout(plan, q, k, v, cu_seqlens, out, stream=None):
     """Packed prompt attention in a form whose bounded waits run out (see cacheblend.h; test support)."""
-    shape, args = _prompt_args(plan, q, k, v, cu_seqlens)
-    check(_lib.load().cb_test_prompt_wait_timeout(plan.handle, *args, _arg(plan, out, torch.bfloat16, shape, "out"),
-                                                  _plan_stream(plan, stream)))
+    bf, rows, n = torch.bfloat16, _size(q, "q", 0, 3), _size(cu_seqlens, "cu_seqlens")
+    q_shape, kv_shape = (rows, plan.hq, plan.head_dim), (rows, plan.hkv, plan.head_dim)
+    check(_lib.load().cb_test_prompt_wait_timeout(
+        plan.handle, _arg(plan, q, bf, q_shape, "q"), _arg(plan, k, bf, kv_shape, "k"), _arg(plan, v, bf, kv_shape, "v"),
+        _arg(plan, cu_seqlens, torch.int32, (n,), "cu_seqlens"), n - 1, rows, _arg(plan, out, bf, q_shape, "out"),
+        _plan_stream(plan, stream)))
 
 
 def cb_test_projection_wait_timeout(plan, x, m, w_qkv, q, k, v, stream=None):
