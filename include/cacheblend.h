@@ -414,7 +414,10 @@ cb_status cb_kv4_load(cb_plan* plan, const void* cache, int32_t n_pages, int32_t
  * k_j, v_j the rows at slot table[s][j / P] * P + j % P. q, out: [n_seqs, hq, D]; scale <= 0 selects
  * 1/sqrt(D). A request with kv_lens 0 (a padded batch) gets zeros and its table row is not read; slots
  * behind a request's length may hold any bytes. Requests may share pages. fp32 scores, softmax and
- * accumulation; the softmax weights times V's scales are rounded to bf16 before the product.
+ * accumulation; the softmax weights times V's scales are rounded to bf16 before the product, and q is held in fp16,
+ * scaled by head: each value to within 2^-35 of its head's largest magnitude. Sums are formed before the division by
+ * the weights' sum, over codes with an offset: values of magnitude up to 2^84 cannot overflow them, larger ones may
+ * (infinity or NaN).
  * Recorded as CB_ERR_DEVICE_CHECK: a negative length (as 0), one past table_width * P (cut there), a
  * table entry outside [0, n_pages) (its keys are left out). n_seqs * hkv * table_width * P must stay below
  * 2^34 (CB_ERR_UNSUPPORTED). out must overlap no input. A bounded wait that gives up records CB_ERR_TIMEOUT.
@@ -432,9 +435,11 @@ cb_status cb_kv4_decode_attention(cb_plan* plan, const void* q, const void* cach
  * within [0, n_rows], n_seqs at most CB_PROMPT_MAX_SEQS; empty sequences are allowed, and rows in no
  * sequence keep their out. Values of keys that a row does not see (later ones, other sequences') do
  * not reach it, whatever they are. scale <= 0 selects 1/sqrt(D). fp32 accumulation and softmax, bf16 P,
- * bf16 output; tcgen05 (TMEM accumulators) fed by TMA. out must overlap no input. Offsets that fall or leave [0, n_rows] are
- * recorded as CB_ERR_DEVICE_CHECK (clipped, a falling pair read as empty). No scratch: calls on one
- * plan may overlap. A bounded wait that gives up records CB_ERR_TIMEOUT. */
+ * bf16 output; tcgen05 (TMEM accumulators) fed by TMA. Sums are formed before the division by the weights' sum:
+ * values of magnitude up to 2^84 cannot overflow them, larger ones may (infinity or NaN).
+ * out must overlap no input. Offsets that fall or leave [0, n_rows] are recorded as CB_ERR_DEVICE_CHECK
+ * (clipped, a falling pair read as empty). No scratch: calls on one plan may overlap. A bounded wait that
+ * gives up records CB_ERR_TIMEOUT. */
 #define CB_PROMPT_MAX_SEQS 16384
 cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const void* v, const int32_t* cu_seqlens,
                               int32_t n_seqs, int32_t n_rows, float scale, void* out, void* stream);

@@ -1177,3 +1177,32 @@ def test_decode_on_both_sides_of_the_split(cb, hq, hkv, d, most):
         plan.check()
         _check_decode(plan, q, out, ks, vs, f"lengths {lens}")
     plan.close()
+
+
+@pytest.mark.parametrize("power", [84, -100])
+def test_values_of_any_magnitude_that_the_header_allows(cb, power):
+    # A weight is at most 2^8 (decode) of its reference, a prompt's tile of weights at most 2^16 in sum: over 2^31 keys,
+    # times 143 / 7 for decode's codes, 2^43.4 times the largest value, below 2^128 up to 2^84. Scores jump at 40 and 600.
+    rng = np.random.default_rng(80 + abs(power))
+    hq, hkv, d, page, n = 8, 2, 128, 32, 700
+    plan = _plan(cb, hq, hkv, d)
+    q, k = _bits(rng, n, hq, d), _bits(rng, n, hkv, d, scale=0.3)
+    base = bf16_bits_to_f64(q).reshape(n, hkv, hq // hkv, d).mean((0, 2))
+    q = f32_to_bf16_bits((bf16_bits_to_f64(q) + np.repeat(np.sign(base), hq // hkv, 0)).astype(np.float32))
+    for at, size in ((40, 0.4), (600, 1.2)):
+        k[at] = f32_to_bf16_bits((size * np.sign(base)).astype(np.float32))
+    v = rng.standard_normal((n, hkv, d))
+    v = f32_to_bf16_bits((np.clip(v / 4, -1, 1) * 2.0**power).astype(np.float32))
+    out = _prompt(cb, plan, q, k, v, [0, n])
+    plan.check()
+    _check_prompt(q, k, v, [0, n], out, f"prompt, values up to 2^{power}")
+    table = rng.permutation(-(-n // page))[None]
+    cache = torch.zeros((table.size, hkv, serving.page_bytes(page, d)), dtype=torch.uint8, device="cuda")
+    pos = np.arange(n)
+    cb.cb_kv4_store(plan, bf16_tensor(k), bf16_tensor(v), _i32(table[0][pos // page] * page + pos % page), cache, page)
+    ks, vs = (serving.dequantise(*serving.quantise(bf16_bits_to_f64(x))) for x in (k, v))
+    out = torch.empty((1, hq, d), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q[-1:].copy()), cache, page, _i32(table), _i32([n]), out)
+    plan.check()
+    _check_decode(plan, q[-1:], out, [ks], [vs], f"decode, values up to 2^{power}")
+    plan.close()
