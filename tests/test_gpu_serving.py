@@ -1206,3 +1206,76 @@ def test_values_of_any_magnitude_that_the_header_allows(cb, power):
     plan.check()
     _check_decode(plan, q[-1:], out, [ks], [vs], f"decode, values up to 2^{power}")
     plan.close()
+
+
+@pytest.mark.parametrize("hq,hkv,d,page", [(4, 2, 64, 16), (16, 2, 128, 64)])
+def test_chunks_cached_loaded_blended_cached_and_decoded(cb, hq, hkv, d, page):
+    """What ties these calls to the blend: chunks are encoded on their own and cached in 4 bits, read back as the blend's
+    k_old / v_old, blended, the fused cache stored as a request's pages, and its first token decoded over them."""
+    import dataclasses
+
+    from conftest import assert_close_attention, assert_close_bf16
+    from oracle.blend import blend_layer
+    from workloads import get_config
+    from workloads.generator import generate_layer, hkvd_noise_sets
+    from workloads.torch_io import layer_tensors
+
+    cfg = dataclasses.replace(get_config("tiny"), n_chunks=3, chunk_len=84, n_suffix=21, hq=hq, hkv=hkv, head_dim=d)
+    rng = np.random.default_rng(90 + d)
+    inp = generate_layer(cfg, 1, hkvd_noise_sets(cfg))
+    plan, serve = cb.Plan.from_config(cfg), cb.Plan(1, 512, 0, hq, hkv, d, cfg.rope_theta)
+    n_ctx, n = cfg.n_ctx, cfg.n_tokens
+    pool, lens = 64, [cfg.chunk_len] * 3
+    free, cache = _i32(rng.permutation(pool)), torch.zeros((pool, hkv, serving.page_bytes(page, d)), dtype=torch.uint8, device="cuda")
+    i0 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    # the chunks: laid out, attended on their own, cached
+    cu, kv, pos, slots, to = i0(4), i0(3), i0(n_ctx), i0(n_ctx), i0(1)
+    cb.cb_page_tables(serve, i0(3), _i32(lens), page, free, i0(3, 8) - 1, cu, kv, pos, slots, to)
+    t = layer_tensors(inp)
+    qc = _bits(rng, n_ctx, hq, d)
+    out = torch.empty((n_ctx, hq, d), dtype=torch.bfloat16, device="cuda")
+    cb.cb_prompt_attention(serve, bf16_tensor(qc), t["k_old"], t["v_old"], cu, out)
+    cb.cb_kv4_store(serve, t["k_old"], t["v_old"], slots, cache, page)
+    serve.check()
+    _check_prompt(qc, inp.k_old, inp.v_old, np.cumsum([0] + lens), out, "chunks")
+    # read back, blended
+    t["k_old"], t["v_old"] = torch.empty_like(t["k_old"]), torch.empty_like(t["v_old"])
+    cb.cb_kv4_load(serve, cache, page, slots, t["k_old"], t["v_old"])
+    for got, x in ((t["k_old"], inp.k_old), (t["v_old"], inp.v_old)):
+        assert np.array_equal(_f64(got), serving._to_bf16(serving.dequantise(*serving.quantise(bf16_bits_to_f64(x)))))
+    bufs = cb.LayerBuffers(plan)
+    cb.cb_blend_layer(plan, 1, cand=None, bufs=bufs, **t)
+    plan.check()
+    _, k, mq, selects = plan.layer_sizes(1)
+    want = blend_layer(cfg, dataclasses.replace(inp, k_old=bf16_bits(t["k_old"]), v_old=bf16_bits(t["v_old"])), 1,
+                       np.arange(n_ctx), k, bool(selects))
+    assert np.array_equal(bufs.sel_tok[:k].cpu().numpy(), want.sel_tok)
+    assert np.array_equal(_f64(bufs.v_fused), want.v_fused)
+    assert_close_bf16(_f64(bufs.k_fused), want.k_fused, what="fused K")
+    assert_close_attention(_f64(bufs.out[:mq]), want.out, want.out_vscale)
+    # the fused cache as a request's pages, behind those of the chunks, which stay
+    table, cu, kv, pos, slots2, end = i0(1, 36 if page == 16 else 8) - 1, i0(2), i0(1), i0(n), i0(n), i0(1)
+    cb.cb_page_tables(serve, i0(1), _i32([n]), page, free, table, cu, kv, pos, slots2, end, free_from=to)
+    cb.cb_kv4_store(serve, bufs.k_fused, bufs.v_fused, slots2, cache, page)
+    # its first token
+    q1, k1, v1 = _bits(rng, 1, hq, d), _bits(rng, 1, hkv, d), _bits(rng, 1, hkv, d)
+    dq, dk = bf16_tensor(q1), bf16_tensor(k1)
+    qe, ke, kv1 = torch.empty_like(dq), torch.empty_like(dk), i0(1)
+    cu, pos, slot, last = i0(2), i0(1), i0(1), i0(1)
+    cb.cb_page_tables(serve, kv, _i32([1]), page, free, table, cu, kv1, pos, slot, last, free_from=end)
+    cb.cb_rope_rerotate(serve, qe, dq, pos)
+    cb.cb_rope_rerotate(serve, ke, dk, pos)
+    cb.cb_kv4_store(serve, ke, bf16_tensor(v1), slot, cache, page)
+    out = torch.empty((1, hq, d), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(serve, qe, cache, page, table, kv1, out)
+    serve.check()
+    assert pos.tolist() == [n] and kv1.tolist() == [n + 1]
+    ks, vs = (serving.dequantise(*serving.quantise(bf16_bits_to_f64(np.concatenate((bf16_bits(a), b)))))
+              for a, b in ((bufs.k_fused, bf16_bits(ke)), (bufs.v_fused, v1)))
+    _check_decode(serve, bf16_bits(qe), out, [ks], [vs], "first token")
+    again = [torch.empty_like(x) for x in (t["k_old"], t["v_old"])]
+    cb.cb_kv4_load(serve, cache, page, slots, *again)
+    for a, b in zip(again, (t["k_old"], t["v_old"])):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    plan.close()
+    serve.close()
