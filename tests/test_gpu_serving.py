@@ -1279,3 +1279,161 @@ def test_chunks_cached_loaded_blended_cached_and_decoded(cb, hq, hkv, d, page):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
     plan.close()
     serve.close()
+
+
+# ---- calls at the ends of what is allowed ---------------------------------------------------------
+
+
+@pytest.mark.parametrize("page", [1024, 1008])
+def test_largest_pages(cb, page):
+    rng = np.random.default_rng(100 + page)
+    plan, lens = _plan(cb, 8, 2, 64), [page, 3 * page - 5, 0, 17, page + 1]
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, page)
+    q = _bits(rng, len(lens), 8, 64)
+    out = torch.full((len(lens), 8, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32(lens), out)
+    slots = _i32(table[1][np.arange(lens[1]) // page] * page + np.arange(lens[1]) % page)
+    k, v = (torch.empty((lens[1], 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cb.cb_kv4_load(plan, cache, page, slots, k, v)
+    plan.check()
+    _check_decode(plan, q, out, ks, vs, f"pages of {page}")
+    assert np.array_equal(_f64(k), serving._to_bf16(ks[1])) and np.array_equal(_f64(v), serving._to_bf16(vs[1]))
+    plan.close()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(1, 1, 64), (1, 1, 128), (256, 16, 128), (512, 32, 64), (32, 32, 64)])
+def test_smallest_and_largest_head_layouts(cb, hq, hkv, d):
+    rng = np.random.default_rng(101 + hq)
+    plan, lens, page = _plan(cb, hq, hkv, d), [40, 0, 141, 3], 48
+    cu, n = np.cumsum([0] + lens), sum(lens) + 2
+    q, k, v = _bits(rng, n, hq, d), _bits(rng, n, hkv, d), _bits(rng, n, hkv, d)
+    out = _prompt(cb, plan, q, k, v, cu)
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, page)
+    q1 = _bits(rng, len(lens), hq, d)
+    out1 = torch.full((len(lens), hq, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q1), cache, page, _i32(table), _i32(lens), out1)
+    plan.check()
+    _check_prompt(q, k, v, cu, out, "prompt")
+    _check_decode(plan, q1, out1, ks, vs, "decode")
+    plan.close()
+
+
+def test_decode_of_thousands_of_requests(cb):
+    rng = np.random.default_rng(102)
+    plan, page = _plan(cb, 4, 2, 64), 16
+    lens = [int(x) for x in rng.integers(0, 36, 3001)]
+    cache, table, ks, vs = _cache(cb, plan, rng, lens, page)
+    q = _bits(rng, len(lens), 4, 64)
+    out = torch.full((len(lens), 4, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q), cache, page, _i32(table), _i32(lens), out)
+    plan.check()
+    _check_decode(plan, q, out, ks, vs, "many requests")
+    plan.close()
+
+
+def test_prompt_of_the_most_sequences(cb):
+    rng = np.random.default_rng(103)
+    plan = _plan(cb, 4, 2, 64)
+    lens = rng.integers(0, 3, 16384)
+    lens[[0, 5000, 16383]] = 0, 150, 70
+    cu, n = np.cumsum(np.r_[0, lens]), int(lens.sum()) + 1
+    q, k, v = _bits(rng, n, 4, 64), _bits(rng, n, 2, 64), _bits(rng, n, 2, 64)
+    out = _prompt(cb, plan, q, k, v, cu)
+    plan.check()
+    _check_prompt(q, k, v, cu, out, "most sequences")
+    plan.close()
+
+
+def test_no_pages_no_width_no_requests(cb):
+    plan, page = _plan(cb, 8, 2, 64), 16
+    bf = lambda *s: torch.full(s, 9.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    none = torch.zeros((0, 2, serving.page_bytes(page, 64)), dtype=torch.uint8, device="cuda")
+    some = torch.zeros((3, 2, serving.page_bytes(page, 64)), dtype=torch.uint8, device="cuda")
+    # nothing to do
+    cb.cb_kv4_store(plan, bf(0, 2, 64), bf(0, 2, 64), _i32([]), some, page)
+    cb.cb_kv4_load(plan, none, page, _i32([]), bf(0, 2, 64), bf(0, 2, 64))
+    cb.cb_kv4_decode_attention(plan, bf(0, 8, 64), none, page, _i32(np.zeros((0, 4))), _i32([]), bf(0, 8, 64))
+    cb.cb_prompt_attention(plan, bf(0, 8, 64), bf(0, 2, 64), bf(0, 2, 64), _i32([0, 0]), bf(0, 8, 64))
+    out = bf(5, 8, 64)
+    cb.cb_prompt_attention(plan, bf(5, 8, 64), bf(5, 2, 64), bf(5, 2, 64), _i32([3]), out)  # no sequence
+    plan.check()
+    assert (out == 9.0).all()
+    # requests without keys over a table without columns and a cache without pages
+    out = bf(3, 8, 64)
+    cb.cb_kv4_decode_attention(plan, bf(3, 8, 64), none, page, _i32(np.zeros((3, 0))), _i32([0, 0, 0]), out)
+    plan.check()
+    assert not out.any()
+    # keys that the table has no room for, pages that the cache does not have: left out, and recorded
+    for cache, table in ((some, np.zeros((3, 0))), (none, np.zeros((3, 2)))):
+        out = bf(3, 8, 64)
+        cb.cb_kv4_decode_attention(plan, bf(3, 8, 64), cache, page, _i32(table), _i32([0, 20, 9]), out)
+        with pytest.raises(cb.CacheBlendError) as e:
+            plan.check()
+        assert e.value.status == 5 and not out.any()
+    for n in (3, 17000):  # row by row, and by runs
+        k, v = bf(n, 2, 64), bf(n, 2, 64)
+        cb.cb_kv4_load(plan, none, page, _i32(np.arange(n)), k, v)
+        with pytest.raises(cb.CacheBlendError):
+            plan.check()
+        assert (k == 9.0).all() and (v == 9.0).all()
+        cb.cb_kv4_store(plan, k, v, _i32(np.arange(n)), none, page)
+        with pytest.raises(cb.CacheBlendError):
+            plan.check()
+    plan.close()
+
+
+def test_page_tables_at_the_ends_of_32_bits(cb):
+    plan, top = _plan(cb, 4, 2, 64), (1 << 31) - 1
+    ctx, new, free = [top, 5, top - 3, 0], [3, 20, 2, 0], [4, 8, 9]
+    table = [[1, -1, -1], [2, -1, -1], [3, 6, 7], [-1, -1, -1]]
+    t, cu, kv, pos, slots, to = _tables(cb, plan, ctx, new, 16, free, table, 27, free_from=1)
+    with pytest.raises(cb.CacheBlendError) as e:
+        plan.check()
+    assert e.value.status == 5
+    want = serving.page_tables(ctx, new, 16, free, table, 27, 1)
+    for got, w in zip((t, cu, kv, pos, slots, to), (*want[:3], np.minimum(want[3], top), *want[4:])):
+        assert np.array_equal(got.reshape(-1), np.asarray(w).reshape(-1))
+    # a free list whose start lies behind its end, or is the last of 32 bits
+    for frm in (7, top):
+        t, cu, kv, pos, slots, to = _tables(cb, plan, [0], [20], 16, free, [[-1, -1]], 20, free_from=frm)
+        with pytest.raises(cb.CacheBlendError):
+            plan.check()
+        assert to.tolist() == [frm] and t.tolist() == [[-1, -1]] and (slots == -1).all() and kv.tolist() == [20]
+    # rows for none of the new tokens
+    t, cu, kv, pos, slots, to = _tables(cb, plan, [0, 16], [20, 1], 16, free, [[-1, -1], [5, -1]], 0)
+    with pytest.raises(cb.CacheBlendError):
+        plan.check()
+    assert t.tolist() == [[4, 8], [5, 9]] and cu.tolist() == [0, 0, 0] and kv.tolist() == [20, 17] and to.tolist() == [3]
+    plan.close()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (16, 1, 128), (4, 4, 128)])
+def test_queries_that_are_not_finite_stay_with_their_row_and_head(cb, hq, hkv, d):
+    rng = np.random.default_rng(104 + hq)
+    plan, page = _plan(cb, hq, hkv, d), 16
+    cu, n = [0, 150, 200], 200
+    q, k, v = _bits(rng, n, hq, d), _bits(rng, n, hkv, d), _bits(rng, n, hkv, d)
+    clean = q.copy()
+    bad = np.zeros((n, hq), bool)
+    for row, head, bits in ((0, 0, 0x7FC0), (77, 1, 0x7F80), (140, hq - 1, 0xFF80), (160, 2, 0x7FC1)):
+        q[row, head, 5], bad[row, head] = bits, True
+    got = _f64(_prompt(cb, plan, q, k, v, cu))
+    plan.check()
+    assert np.isnan(got[bad & (np.arange(n) % 10 == 0)[:, None]]).all()  # NaNs, and an infinity over many keys
+    ref, vs = serving.packed_attention(*(bf16_bits_to_f64(x) for x in (clean, k, v)), cu)
+    _close(got[~bad], ref[~bad], vs[~bad], 40 * 2.0**-23 * d**0.5 * np.abs(bf16_bits_to_f64(clean)).max() * np.abs(bf16_bits_to_f64(k)).max(), "prompt")
+    lens = [50, 700, 3]
+    cache, table, ks, vs4 = _cache(cb, plan, rng, lens, page)
+    q1 = _bits(rng, 3, hq, d)
+    clean = q1.copy()
+    for s, head, bits in ((0, 0, 0x7FC0), (1, hq - 1, 0x7F80)):
+        q1[s, head, 9] = bits
+    out = torch.empty((3, hq, d), dtype=torch.bfloat16, device="cuda")
+    cb.cb_kv4_decode_attention(plan, bf16_tensor(q1), cache, page, _i32(table), _i32(lens), out)
+    plan.check()
+    got = _f64(out)
+    assert np.isnan(got[0, 0]).all() and np.isnan(got[1, hq - 1]).all()
+    for s, head in ((0, 0), (1, hq - 1)):  # the rest is as it would be
+        got[s, head] = decode_attention(bf16_bits_to_f64(clean)[s], ks[s], vs4[s])[head]
+    _check_decode(plan, clean, bf16_tensor(f32_to_bf16_bits(got.astype(np.float32))), ks, vs4, "decode")
+    plan.close()
