@@ -5,9 +5,10 @@
 // with k and v = code * (scale of the row's group of 32 dims).
 //
 // Floor: a (key, kv head) is 18/16 D bytes. At 6.7 TB/s an SM receives 23 bytes per cycle, so it has
-// about 6 cycles per (key, kv head) at D = 128. Widening the codes in shared memory for tcgen05 would write
-// and read 512 bytes per key there, 8 cycles at 128 bytes per cycle, more than the floor; so the codes
-// are widened in registers, straight into the operand layout of mma.sync:
+// about 6 cycles per (key, kv head) at D = 128. The codes are widened in registers, straight into the
+// operand layout of mma.sync, which leaves shared memory out of it; the batch below takes 12 cycles. (tcgen05 reads
+// at least one operand from shared memory: widened codes there are 512 bytes per key to write and read, 8 cycles at 128
+// bytes per cycle. Above the floor, below what this kernel takes; such a form has not been built.)
 //   K   word & 0x000f000f and word & 0x00f000f0 are pairs of fp16 of value nibble * 2^-24 and * 2^-20
 //       (subnormals, exact): 5 instructions per 8 codes;
 //   V   (word >> 4 i & 0x000f000f) | 0x43004300 is a pair of bf16 of value 128 + nibble = 136 + code
@@ -42,10 +43,16 @@
 // Measured (8 kv heads of 128 dims): 64 requests of up to 8,449 keys, 64 query heads (308 MB, 46 us at
 // the copy rate) 89 us, 0.52 of that rate; one request of 32,897 keys, 32 query heads (38 MB, 5.7 us) 22 us:
 // the first records arrive after 3.3 us, a warp's ten take 9, the merges 5 (a CTA's own, the ticket, the parts).
+// With 16 query heads per kv head (8 warps) and other sizes: 64 requests of 4,225 keys, 8 kv heads of 128 dims, 124 us
+// against 82 with 8 query heads (0.37 and 0.56 of the copy rate), of 64 dims 90 against 59 (0.26 and 0.39);
+// one request of 32,897 keys, 16 query heads on one kv head of 128 dims, 49 us, of 64 dims 30; one of 4,096,
+// 8,192, 16,384 keys, 8 kv heads of 128 dims, 10, 14 and 17 us.
 // Runs of equal length by CTA instead of by warp are slower, 92 us for the batch. What bounds the batch
-// is the instructions: about 360 per record and warp, 175 of them on the integer pipe, which takes one every
-// other cycle, so 350 cycles per record for a scheduler, 0.9 of the bytes' time; three warps per scheduler
-// overlap them with the products and the exponentials to 1.6 times that. With 14 and 16 warps, of fewer
+// is latency: a record costs a warp about 360 instructions, 175 of them on the integer pipe, which takes one every
+// other cycle, and three warps per scheduler are too few to fill any pipe (issue slots 50% in use while active, integer
+// 49%, tensor 27%). Of the 6.0 cycles per instruction of a warp 1.0 is its issue, 1.7 are fixed latencies, 0.9 a
+// busy pipe, 0.8 another warp's turn, 0.4 branches, 0.3 each barriers and memory, 0.6 shared memory, dispatch and
+// instruction fetch. With 14 and 16 warps, of fewer
 // registers, the batch takes 96 and 94 us. Records two to a copy (92 us then) or two at a time through the
 // registers (88 against 89), Q in shared memory to make room for 16 warps (105), shifts as multiplications (96),
 // and K in e4m3 with Q in two terms (102; 3 instructions per 8 codes, but such a product costs more than

@@ -11,9 +11,10 @@
 // requests in its shared memory (12 bytes per request) and then takes its own share of the pages and
 // of the rows, finding each one's request by a binary search. A page that a row falls in is looked
 // up where its owner finds it (the old table or the free list), never in an entry that another block
-// writes in the same launch. 64 requests that decode take 3.9 us on the device, 512
-// prompts of 2,048 tokens at most (about 524,000 rows, 4.2 MB out: 0.7 us at the copy rate) 8.0, the chain
-// lengths -> sums -> search -> page -> row; the Python call takes 8.9.
+// writes in the same launch. 64 requests that decode take 3.5 us on the device, 512 prompts of 2,048 tokens at most
+// (540,000 rows, 4.3 MB out: 0.7 us at the copy rate) 8.0: 2.5 for a launch that does nothing but the sums (of 64
+// requests or 512), 2.5 more where 264 blocks also write padding for every row, 2.6 more for the rows' searches and the pages
+// that they look up, 0.4 for 34,000 table entries. The Python call takes 8.9.
 #include "common.cuh"
 #include "kernels.h"
 

@@ -10,7 +10,7 @@
 // softmax and tensor-core work alternate, so that each softmax hides behind the other tile's MMAs.
 //
 // What differs, and why:
-//   Persistent CTAs. A chunk of 2,048 tokens has items of 1 to 16 key tiles, about 9 rounds of 1.4 us
+//   Persistent CTAs. A chunk of 2,048 tokens has items of 1 to 16 key tiles, 8.5 rounds of 1.4 us
 //   on average, and starting a CTA (TMEM, barriers, first loads) costs about 3 us, a quarter of that.
 //   One CTA per SM takes items in turn; the rings of K and V run on across items, and the next
 //   item's first tiles load while the last softmax of the current one runs.
@@ -47,9 +47,12 @@
 // item i + 3. After a wait that gave up (abort flag) every warp still walks through the rounds of the
 // current item, without work, and the producer ends the list, so no named barrier is left short.
 //
-// Measured (8 kv heads of 128 dims): 16 chunks of 2,048 tokens, 32 query heads, 425 us with new inputs in each
+// Measured (8 kv heads of 128 dims): 16 chunks of 2,048 tokens, 32 query heads, 427 us with new inputs in each
 // call, 394 with the same (284 us at the tensor cores' rate, 100 of HBM); 40 prompts of 1 to 1,087 tokens,
-// 64 query heads, 282 us (135 and 117); one prompt of 16,384 tokens 1.29 ms, 0.88 of that rate.
+// 64 query heads, 283 us (135 and 117); one prompt of 16,384 tokens 1.32 ms, 0.86 of that rate. Other head layouts, 16
+// chunks of 2,048 tokens: 16 query heads on 16 kv heads of 128 dims 227 us (142; tile 0 runs an item's last round masked
+// whole), on one 197; of 64 dims 16 on one 169 (71), 32 on 16 329 (142): there a score costs the softmax as much for
+// half the products. 64 prompts of 64 tokens, 32 query heads, 23 us.
 // A round (a key tile against both query tiles) takes 2,750 - 2,850 cycles, of which the tensor cores need 2,504;
 // an item adds about 6,000: on its softmax warps' path the masks of the diagonal tile (600), the last product
 // (1,000), the output (2,000), the next item and the first maximum (600).
