@@ -94,8 +94,8 @@ __device__ __noinline__ bool wait_record(uint32_t bar, uint32_t parity, volatile
 // After it: the lane that asks for the records waits once more for those in flight, from stage `stage` of the ring on,
 // for as long as the limit again for all of them together, and asks for no more (returns false): a barrier whose phase
 // has not completed must not be armed again. So no copy is under way when the ring is used for something else or
-// the CTA ends, unless it takes longer than both limits. (A flag that the lane tests before each request and the wait's
-// result cost 1 us of 88; asking on after the second limit, as it was without them, armed such a barrier.)
+// the CTA ends, unless it takes longer than both limits. (The flag that the lane tests before each request and the
+// wait's result cost 1 us of 88.)
 __device__ __noinline__ bool stop_requests(uint32_t bar0, int stage, uint32_t parity, int stages, int in_flight,
                                            uint64_t limit_ns) {
   const uint64_t t0 = global_timer();
@@ -476,7 +476,7 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.
 
 // PROBE: the wait-timeout probe (test support only): every warp arms the barrier of its second record but never
 // copies it, and the waits give up after kProbeTimeoutNs, so each warp with two records or more takes its failure
-// path. The kernel itself has no part of it.
+// path. Compiled out of the kernel itself.
 template <int D, int NT, bool PROBE = false>
 __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const Kv4DecodeParams p) {
   constexpr uint64_t kLimit = PROBE ? kProbeTimeoutNs : kTimeoutNs;

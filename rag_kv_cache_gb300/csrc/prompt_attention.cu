@@ -282,7 +282,7 @@ __device__ __forceinline__ bool zero_not_finite(uint32_t tile, int from, int lan
 
 // PROBE: the wait-timeout probe (test support only): the K producer of every CTA arms the barrier of its second key
 // tile but never copies the tile, and the waits give up after kProbeTimeoutNs, so each CTA with two key tiles or more
-// takes its failure path. The kernel itself has no part of it.
+// takes its failure path. Compiled out of the kernel itself.
 template <int D, bool PROBE = false>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
