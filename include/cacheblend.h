@@ -459,7 +459,7 @@ cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const
  * empty), a negative kv_lens (as 0), one past table_width * P (cut there, its last row at the last place), a table
  * entry outside [0, n_pages) (its keys are left out). out and lse must overlap no input nor one another.
  * fp32 scores, softmax and accumulation; tcgen05 (TMEM accumulators). The cache's scale * code is held in fp16 after a
- * power of two for every 128 keys: exact, but for scales below 2^-8 of the largest among them (within 2^-19 of that one's
+ * power of two for every 128 keys: exact, but for scales below 2^-29 of the largest among them (within 2^-39 of that one's
  * reach); softmax weights are rounded to fp16, q to within 2^-35 of its head's largest magnitude. In a batch of many
  * requests those of up to 8 rows per kv head (16 where 16 heads share one) run on mma.sync: codes and K's scales are
  * exact there, a weight times V's scale is rounded to fp16 (to 2^-31 where it is small against the largest scale that

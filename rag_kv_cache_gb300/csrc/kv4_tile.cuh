@@ -3,11 +3,14 @@
 //
 // fp16 holds a product scale * code exactly (8 significant bits times 3) as long as its exponent fits, which bf16,
 // with 8 bits, does not. So a tile is scaled by a power of two: 2^-e_k for its keys, 2^-e_v for its values, from
-// the largest scale of each, which puts that scale into [2^-9, 2^-8); products of scales down to 2^-8 of the largest
-// are exact, those of smaller ones within 2^-25 (after scaling, where the largest product is 7 2^-8 at most). The powers
-// leave through the softmax's factor and the output's.
-//   A nibble n = code + 8 at the low bits of a half is the fp16 subnormal n 2^-24, at bits 4 .. 7 n 2^-20; one fused
-//   multiply-add with 2^24 scale (2^20 scale) and -8 scale gives (n - 8) scale without a rounding.
+// the largest scale of each, which puts that scale into [2^12, 2^13), and eight times it below fp16's largest value. Products
+// of scales down to 2^-29 of the largest are exact, those of smaller ones within 2^-25 (after scaling): a group of dims
+// whose values lie far below the others' keeps its own precision. The powers leave through the softmax's factor and the
+// output's.
+//   A nibble n = code + 8 under the bits of 1024 is the half 1024 + n, at bits 4 .. 7 1024 + 16 n: a sum with -1032, or a
+//   multiply-add with 1/16 and -72, gives the code, a product the value. (From subnormals n 2^-24 one multiply-add with
+//   2^24 scale and -8 scale gives it, nine instructions for eight values in place of thirteen, but 2^24 scale must stay below
+//   2^16, which leaves 2^-8 between the largest scale and the first that loses bits.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -25,7 +28,7 @@ constexpr int kUnitKeys = kUnitRecords * kKv4Block;
 constexpr int kTileUnits = 2;
 constexpr int kTileTokens = kUnitKeys * kTileUnits;
 constexpr uint32_t kNoRecord = 0xffffffffu;
-constexpr int kLeastExponent = -100;  // of a tile's power of two (its factors stay inside fp32)
+constexpr int kLeastExponent = -120;  // of a tile's power of two (its factors stay inside fp32)
 
 // Records in shared memory. They come by TMA, one copy for the records of a unit that lie in one page, as lines of 128 bytes
 // whose 16-byte chunks are swizzled by the line (18 D / 128 lines a record, an even number at D = 128, so that eight lanes
@@ -59,28 +62,25 @@ __device__ __forceinline__ void sts1(uint32_t at, uint32_t a) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(a) : "memory");
 }
 
-// The factors of a scale for both nibbles of a byte: S = 2^24 scale for the low one (n 2^-24 as an fp16 subnormal), 2^20 scale for
-// the high one (n 2^-20), and -8 scale.
-struct Factors {
-  __half2 lo, hi, off;
-  __device__ __forceinline__ explicit Factors(__half2 S)
-      : lo(S), hi(__hmul2(S, __float2half2_rn(0.0625f))), off(__hmul2(S, __float2half2_rn(-1.0f / 2097152.0f))) {}
-};
-// The four pairs of a word's nibbles (bits 4 i of its halves), times the scale: 9 instructions for 8 values.
-__device__ __forceinline__ void widen_word(uint32_t w, const Factors& f, uint32_t (&x)[4]) {
+// The four pairs of a word's nibbles (bits 4 i of its halves), times the scale: 13 instructions for 8 values.
+__device__ __forceinline__ void widen_word(uint32_t w, __half2 scale, uint32_t (&x)[4]) {
+  const __half2 low = __float2half2_rn(-1032.0f), by = __float2half2_rn(0.0625f), high = __float2half2_rn(-72.0f);
   const uint32_t v = w >> 8;
-  x[0] = h2_bits(__hfma2(h2_of(w & 0x000f000fu), f.lo, f.off));
-  x[1] = h2_bits(__hfma2(h2_of(w & 0x00f000f0u), f.hi, f.off));
-  x[2] = h2_bits(__hfma2(h2_of(v & 0x000f000fu), f.lo, f.off));
-  x[3] = h2_bits(__hfma2(h2_of(v & 0x00f000f0u), f.hi, f.off));
+  x[0] = h2_bits(__hmul2(__hadd2(h2_of((w & 0x000f000fu) | 0x64006400u), low), scale));
+  x[1] = h2_bits(__hmul2(__hfma2(h2_of((w & 0x00f000f0u) | 0x64006400u), by, high), scale));
+  x[2] = h2_bits(__hmul2(__hadd2(h2_of((v & 0x000f000fu) | 0x64006400u), low), scale));
+  x[3] = h2_bits(__hmul2(__hfma2(h2_of((v & 0x00f000f0u) | 0x64006400u), by, high), scale));
 }
 
-// The scales of a tile, in place, by one converged warp: bf16 [128 tokens][K NG, V NG] become, for every 8 tokens, fp16 S
+// The scales of a tile, in place, by one converged warp: bf16 [128 tokens][K NG, V NG] become, for every 8 tokens, fp16 scales
 // of K [8 tokens][NG], then of V [NG][8 tokens]. Tokens from `valid` on, and those of records in `bad`, get 0. e_k and
 // e_v: the tile's exponents; e_v is kNoExponent where all values are 0. A V scale that is not finite gets 0, and
 // nan_from[its group] the least of what it was and first + its token. Two passes of four turns, 32 tokens each, in few
 // instructions: the roles of a kernel share its instruction cache.
 constexpr int kNoExponent = -1000;
+// The exponent of a tile whose largest scale has the bits `top`: one in [2^x, 2^(x+1)) times 2^-e, e >= x - 12, lies below
+// 2^13, eight times it (a bf16's 8 bits) below fp16's largest value.
+__device__ __forceinline__ int exponent_of(uint32_t top) { return max((int)(top >> 7) - 127 - 12, kLeastExponent); }
 template <int D>
 __device__ __forceinline__ void prepare_scales(uint32_t at, int valid, uint32_t bad, int lane, int first, int* nan_from,
                                                int& e_k, int& e_v) {
@@ -126,10 +126,9 @@ __device__ __forceinline__ void prepare_scales(uint32_t at, int valid, uint32_t 
     top_k = __reduce_max_sync(0xffffffffu, top_k);
     top_v = __reduce_max_sync(0xffffffffu, top_v);
   }
-  // a scale in [2^x, 2^(x+1)) times 2^(24 - e), e >= x + 9, lies below 2^16 (and a bf16's 8 bits end below fp16's largest)
-  e_k = max((int)(top_k >> 7) - 127 + 9, kLeastExponent);
-  e_v = max((int)(top_v >> 7) - 127 + 9, kLeastExponent);
-  const float fk = power_of_2(24 - e_k), fv = power_of_2(24 - e_v);  // e_k, e_v: -100 .. 136
+  e_k = exponent_of(top_k);
+  e_v = exponent_of(top_v);
+  const float fk = power_of_2(-e_k), fv = power_of_2(-e_v);  // e_k, e_v: -120 .. 115
   if (top_v == 0) e_v = kNoExponent;
 #pragma unroll 1
   for (int k = 0; k < kTileTokens / 32; ++k) {
@@ -175,9 +174,9 @@ __device__ __forceinline__ void widen_keys(uint32_t tile, uint32_t raw, uint32_t
 #pragma unroll 1
     for (int box = 0; box < NG / 2; ++box) {  // (in a loop, the words moving up: few instructions)
       uint32_t x[4];
-      widen_word(w[0], Factors(__low2half2(h2_of(s[0]))), x);
+      widen_word(w[0], __low2half2(h2_of(s[0])), x);
       sts4(to, x[0], x[1], x[2], x[3]);
-      widen_word(w[1], Factors(__high2half2(h2_of(s[0]))), x);
+      widen_word(w[1], __high2half2(h2_of(s[0])), x);
       sts4(to ^ 64, x[0], x[1], x[2], x[3]);
       if constexpr (NG == 4) w[0] = w[2], w[1] = w[3], s[0] = s[1];
       to += kTileTokens * 128;
@@ -205,7 +204,7 @@ __device__ __forceinline__ void widen_values(uint32_t tile, uint32_t raw, uint32
     uint32_t x[4][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      widen_word(w[c][0], Factors(h2_of(s[c])), x[c]);
+      widen_word(w[c][0], h2_of(s[c]), x[c]);
       w[c][0] = w[c][1];
     }
 #pragma unroll

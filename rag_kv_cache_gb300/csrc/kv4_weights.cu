@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int stage = it & 3, valid = it >> 2 & 31;
       ok = wait(bars.raw[mine_rec][slot], phase, 139) && (!(used >> stage & 1) || wait(bars.k_free[stage], (uses >> stage & 1) ^ 1, 132));
       if (!ok) return;
-      // the record's exponent: its largest scale into [2^-9, 2^-8)
+      // the record's exponent
       const uint32_t raw = ring + slot * kRaw;
       uint32_t top = 0, sc[NG / 2];
       lds<NG / 2>(sc, raw + 8 * D + lane % kKv4Block * (4 * NG));
@@ -472,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         top = max(top, max(lo >= 0x7f80u ? 0u : lo, hi >= 0x7f80u ? 0u : hi));
       }
       top = __reduce_max_sync(0xffffffffu, top);
-      const int e_k = max((int)(top >> 7) - 127 + 9, kLeastExponent);
-      const float fk = power_of_2(24 - e_k);
+      const int e_k = exponent_of(top);
+      const float fk = power_of_2(-e_k);
 #pragma unroll
       for (int i = 0; i < NG / 2; ++i)
         sc[i] = h2_bits(__floats2half2_rn(__uint_as_float(sc[i] << 16) * fk, __uint_as_float(sc[i] & 0xffff0000u) * fk));
@@ -487,9 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < NG / 2; ++i) s[i] = __shfl_sync(0xffffffffu, sc[i], 8 * half + t0);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const Factors f(g % 2 ? __high2half2(h2_of(s[g / 2])) : __low2half2(h2_of(s[g / 2])));
           uint32_t y[4];
-          widen_word(w[g], f, y);
+          widen_word(w[g], g % 2 ? __high2half2(h2_of(s[g / 2])) : __low2half2(h2_of(s[g / 2])), y);
           sts4(sK + stage * kKBytes + (g / 2) * kBox + key * 128 + (uint32_t)(((4 * (g % 2) + c) ^ (key & 7)) * 16), y[0], y[1], y[2],
                y[3]);
         }

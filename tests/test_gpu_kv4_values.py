@@ -1,0 +1,89 @@
+"""Chunk attention and attention weights over 4-bit pages on contents whose parts differ by orders of magnitude,
+against the oracle in 64 bits.
+
+Tolerances. With s = sum_j p_j |v_j| of the output's own dim, an output is within (2^-11 + 2 e + 2^-20 + t) s of the exact
+value, and 2^-8 of itself by its rounding to bf16: a softmax weight is rounded to fp16 once (2^-11), scores are off by at most
+e = (D + 16) 2^-23 scale max_j sum_d |q_d| max|k_d| (fp32 sums of D products, each of D + 8 roundings of 2^-23 since the
+matrix unit truncates) and 2^-35 scale max|q| sum_d max|k_d| (q is held to within 2^-35 of its head's largest, which moves a score
+by no more than that times the sum of the key's magnitudes: small beside the first term where q's dims are of one size, not
+where some are 2^24 of the others), 2^x and its sum by 2^-20, and the sum over n keys by
+t = (n / 16 + 16) 2^-22: one truncation of 2^-23 for every 16 keys, and as much for the joins. Where a weight is below 2^-14 in
+the units in which the row's largest is at least 2^4, its rounding is 2^-25 of those units instead: n 2^-29 p_max of the
+group's largest value. Requests of few rows round the weights times V's scales instead, in units of the largest scale of all
+groups, which the row's largest weight brings to 2^6 at least: n 2^-31 p_max of the largest value of all groups. lse is within
+e + 2^-20 + 2^-22 |lse| + n 2^-24.
+"""
+
+import numpy as np
+import pytest
+from test_gpu_kv4_batch import Batch, _f64
+
+from oracle import serving
+
+pytestmark = pytest.mark.gpu
+
+
+class Values(Batch):
+    def error(self, q, k, c):
+        top = np.abs(k).max(0, initial=0.0)
+        return super().error(q, k, c) + float(c * 2.0**-35 * np.abs(q).max(initial=0.0) * top.sum(-1).max(initial=0.0))
+
+
+def check(b, out, lse, rows_of=None, few=False):
+    """Every request's out and lse (of its rows rows_of only, where there are many) within the limits above."""
+    got, glse, q = _f64(out), lse.cpu().numpy().astype(np.float64), _f64(b.q)
+    c = b.d**-0.5
+    for s in range(len(b.lens)):
+        a, m = int(b.cu[s]), b.new[s]
+        if m == 0:
+            continue
+        k, v = b.cached(s)
+        for i in range(m) if rows_of is None else rows_of:
+            n = len(k) - m + i + 1
+            kk, vv, qq = k[:n], v[:n], q[a + i:a + i + 1]
+            ref, rlse, vs = serving.chunk_attention(qq, kk, vv)
+            e = b.error(qq, kk, c)
+            g = np.arange(b.hq) * b.hkv // b.hq
+            peak = np.exp(c * np.einsum("nhd,hd->hn", kk[:, g], qq[0]).max(-1) - rlse[0])  # [hq]
+            top = np.abs(vv).reshape(n, b.hkv, -1, 32).max((0, 3))[g]  # [hq, groups]
+            top = np.repeat(top, 32, 1) * 2.0**-29 if not few else top.max(1, keepdims=True) * 2.0**-31
+            lim = (2.0**-11 + 2 * e + 2.0**-20 + (n / 16 + 16) * 2.0**-22) * vs[0] + 2.0**-8 * np.abs(ref[0])
+            lim += n * peak[:, None] * top + 1e-37
+            err = np.abs(got[a + i] - ref[0])
+            assert (err <= lim).all(), f"request {s}, row {i}: err/limit {np.nanmax(err / lim):.3f}"
+            err, lim = np.abs(glse[a + i] - rlse[0]), e + 2.0**-20 + 2.0**-22 * np.abs(rlse[0]) + n * 2.0**-24
+            assert (err <= lim).all(), f"lse of request {s}, row {i}: err/limit {np.nanmax(err / lim):.3f}"
+
+
+@pytest.mark.parametrize("down", [4, 12, 16, 24])
+@pytest.mark.parametrize("heads,few", [((8, 2, 128), False), ((8, 4, 64), False), ((16, 16, 128), False), ((32, 8, 128), True)])
+def test_a_group_of_values_far_below_the_others(cb, heads, few, down):
+    # dims 32 .. 63 are 2^-down of the others: their outputs are as close to their own magnitude
+    def edit(k, v):
+        v[:, :, 32:64] *= 2.0**-down
+
+    lens, new = ([300] * 33, [1] * 33) if few else ([300, 129], [140, 1])
+    b = Values(cb, heads, lens, new, 32, edit=edit)
+    out, lse = b.chunk()
+    b.plan.check()
+    check(b, out, lse, few=few)
+    b.plan.close()
+
+
+@pytest.mark.parametrize("down", [4, 12, 16, 24])
+@pytest.mark.parametrize("heads,few", [((8, 2, 128), False), ((8, 4, 64), False), ((32, 8, 128), True)])
+def test_a_group_of_keys_far_below_the_others_with_queries_above(cb, heads, few, down):
+    # dims 32 .. 63 of k are 2^-down of the others, of q 2^down: they count as much in the scores
+    def edit(k, v):
+        k[:, :, 32:64] *= 2.0**-down
+
+    lens, new = ([300] * 33, [1] * 33) if few else ([300, 129], [140, 1])
+    b = Values(cb, heads, lens, new, 32, edit=edit)
+    b.q[:, :, 32:64] *= 2.0**down
+    out, lse = b.chunk()
+    b.plan.check()
+    check(b, out, lse, few=few)
+    w = b.weights(lse)
+    b.plan.check()
+    b.check_weights(w, lse)
+    b.plan.close()
