@@ -456,7 +456,8 @@ cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const
  * not see (later ones, slots behind the request's length) do not reach it, whatever they are. n_seqs is at most
  * CB_PROMPT_MAX_SEQS.
  * Recorded as CB_ERR_DEVICE_CHECK: offsets that fall or leave [0, n_rows] (clipped, a falling pair read as
- * empty), a negative kv_lens (as 0), one past table_width * P (cut there, its last row at the last place), a table
+ * empty; rows that several requests then have hold a mix of their results, and where such requests together go past the
+ * limit on sizes below, those of many rows are not computed), a negative kv_lens (as 0), one past table_width * P (cut there, its last row at the last place), a table
  * entry outside [0, n_pages) (its keys are left out). out and lse must overlap no input nor one another.
  * fp32 scores, softmax and accumulation; tcgen05 (TMEM accumulators). The cache's scale * code is held in fp16 after a
  * power of two for every 128 keys: exact, but for scales below 2^-29 of the largest among them (within 2^-39 of that one's

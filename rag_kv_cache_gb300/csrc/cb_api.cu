@@ -783,7 +783,7 @@ static cb_status kv4_batch(cb_plan* plan, const void* q, const void* cache, int3
     return fail(CB_ERR_INVALID_ARG, "page table too large: n_seqs * table_width above 2^30");
   // row tiles times key tiles of all kv heads, 128 rows or keys each
   const int64_t tiles = ((int64_t)n_rows / (128 / (c.hq / c.hkv)) + n_seqs) * c.hkv;
-  if (tiles * (std::max<int64_t>((int64_t)table_width * page_size, n_rows) / 128 + 1) > (1ll << 30))
+  if (tiles * (std::max<int64_t>((int64_t)table_width * page_size, n_rows) / 128 + 1) > cb::kKv4MostTiles)
     return fail(CB_ERR_UNSUPPORTED, "n_rows, n_seqs and table_width * page_size make more than 2^30 tiles");
   if (n_seqs == 0 || n_rows == 0) return CB_OK;
   CB_TRY(need_tensor(q, "q"));

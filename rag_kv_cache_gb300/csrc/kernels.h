@@ -213,6 +213,8 @@ struct Kv4Batch {
   float scale;
   int32_t* err;
 };
+// Row tiles times key tiles of all kv heads, 128 rows or keys each, that a call may have (counted by the host from n_rows).
+constexpr int64_t kKv4MostTiles = 1ll << 30;
 // Scratch of the chunk attention (owned by the plan): two partial results of 256 rows per CTA of one wave, and what
 // the join needs to know of them.
 struct Kv4ChunkScratch {

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int2 scale_info[kScaleStages];  // (valid tokens, bad records)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_seq, s_before;
-  __shared__ int w_sum[kThreads / 32];
+  __shared__ int64_t w_sum[kThreads / 32];
 
   pdl_launch_dependents();
   const Kv4Batch& b = p.b;
@@ -276,32 +276,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  // The batch's rounds, and where this CTA's run of them begins (31 bits hold them: the host checks).
+  // The batch's rounds, and where this CTA's run of them begins. 31 bits hold them (the host checks), unless offsets that
+  // rise again behind a fall give the same rows to several requests: then nothing is computed past that limit.
   const int run_s = (b.n_seqs + kThreads - 1) / kThreads;
   const int q0 = min(tid * run_s, b.n_seqs), q1 = min(q0 + run_s, b.n_seqs);
-  int mine = 0;
+  int64_t mine = 0;
   for (int s = q0; s < q1; ++s) mine += shape_of<ONE>(kv4_request(b, s), p.lg, p.few).all() * b.hkv;
-  int up = mine;
+  int64_t up = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, up, d);
+    const int64_t y = __shfl_up_sync(0xffffffffu, up, d);
     if (lane >= d) up += y;
   }
   if (lane == 31) w_sum[warp] = up;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int total = 0, before = up - mine;
-#pragma unroll
+  int64_t all_rounds = 0, before = up - mine;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += w_sum[w];
-    total += w_sum[w];
+    all_rounds += w_sum[w];
   }
+  const int total = all_rounds <= kKv4MostTiles ? (int)all_rounds : 0;
   const int quota = (total + gridDim.x - 1) / gridDim.x;
   const int run0 = (int)min((int64_t)blockIdx.x * quota, (int64_t)total);
   const int run1 = (int)min((int64_t)run0 + quota, (int64_t)total);
-  if (mine > 0 && before <= run0 && run0 < before + mine) {
-    int at = before, s = q0;
+  if (before <= run0 && run0 < before + mine && total > 0) {
+    int at = (int)before, s = q0;
     for (int n; run0 >= at + (n = shape_of<ONE>(kv4_request(b, s), p.lg, p.few).all() * b.hkv); ++s) at += n;
     s_seq = s;
     s_before = at;

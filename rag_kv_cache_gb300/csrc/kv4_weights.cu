@@ -231,6 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += w_cost[i];
     all_tiles += w_tiles[i];
   }
+  // A tile costs one and one for each product, of which the host bounds the number: no more than twice its limit, unless offsets
+  // that rise again behind a fall give the same rows to several requests. Nothing is computed then.
+  if (total > 2 * kKv4MostTiles) total = 0;
   const int64_t quota = (total + gridDim.x - 1) / gridDim.x;
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
