@@ -455,19 +455,20 @@ cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const
  * out and lse; a row that sees no key (kv_lens below m) gets zeros and an lse of -infinity. Keys that a row does
  * not see (later ones, slots behind the request's length) do not reach it, whatever they are. n_seqs is at most
  * CB_PROMPT_MAX_SEQS.
- * Recorded as CB_ERR_DEVICE_CHECK: offsets that fall or leave [0, n_rows] (clipped, a falling pair read as
- * empty; rows that several requests then have hold a mix of their results, and where such requests together go past the
- * limit on sizes below, those of many rows are not computed), a negative kv_lens (as 0), one past table_width * P (cut there, its last row at the last place), a table
- * entry outside [0, n_pages) (its keys are left out). out and lse must overlap no input nor one another.
- * fp32 scores, softmax and accumulation; tcgen05 (TMEM accumulators). The cache's scale * code is held in fp16 after a
- * power of two for every 128 keys: exact, but for scales below 2^-29 of the largest among them (within 2^-39 of that one's
- * reach); softmax weights are rounded to fp16, q to within 2^-35 of its head's largest magnitude. In a batch of many
- * requests those of up to 8 rows per kv head (16 where 16 heads share one) run on mma.sync: codes and K's scales are
- * exact there, a weight times V's scale is rounded to fp16 (to 2^-31 where it is small against the largest scale that
- * the request's rows have met). So a request's results depend on the batch that it comes in, within these roundings; a
- * call's repetition gives the same bits. n_rows (in tiles of
- * 128 / (hq/hkv), each request one more) * hkv times the larger of table_width * P and n_rows over 128 must stay below
- * 2^30, table_width * P may not pass it (CB_ERR_UNSUPPORTED). A bounded wait that gives up records CB_ERR_TIMEOUT.
+ * Recorded as CB_ERR_DEVICE_CHECK: offsets that fall or leave [0, n_rows] (clipped, a falling pair read as empty; rows
+ * that several requests then have hold a mix of their results, and where such requests together go past the limit on
+ * sizes below, those of many rows are not computed), a negative kv_lens (as 0), one past table_width * P (cut there,
+ * its last row at the last place), a table entry outside [0, n_pages) (its keys are left out). out and lse must
+ * overlap no input nor one another. fp32 scores, softmax and accumulation; tcgen05 (TMEM accumulators). The cache's
+ * scale * code is held in fp16 after a power of two for every 128 keys: exact, but for scales below 2^-29 of the
+ * largest among them (within 2^-39 of that one's reach), and for values below 2^-60 of the largest of earlier ones
+ * (within 2^-85 of it); softmax weights are rounded to fp16, q to within 2^-35 of its head's largest magnitude. In a
+ * batch of many requests those of up to 8 rows per kv head (16 where 16 heads share one) run on mma.sync: codes and
+ * K's scales are exact there, a weight times V's scale is rounded to fp16 (to 2^-31 where it is small against the
+ * largest scale that the request's rows have met). So a request's results depend on the batch that it comes in, within
+ * these roundings; a call's repetition gives the same bits. n_rows (in tiles of 128 / (hq/hkv), each request one more)
+ * times hkv times the larger of table_width * P and n_rows over 128 must stay below 2^30, table_width * P may not pass
+ * it (CB_ERR_UNSUPPORTED). A bounded wait that gives up records CB_ERR_TIMEOUT.
  * Partial results meet in the plan's scratch: calls of this function on one plan must not overlap on the GPU; order them
  * on one stream, or give each stream its own plan (graphs that may run at once too). */
 cb_status cb_kv4_chunk_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,

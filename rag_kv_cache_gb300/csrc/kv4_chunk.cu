@@ -42,6 +42,9 @@
 // 2^(score a + e_v - ref), in fp16 with at most 2^15, so P V = 2^(score a - ref) v; the sum of the weights takes
 // 2^(e_b - e_v) per round, with e_b of the run's first round, and out = O 2^e_b / l. So each weight is rounded once to
 // 11 bits, relative to what it contributes: to 2^-25 where the largest weight times its values' power is 2^6 or more.
+// The sum itself must not depend on the values: an e_v lies 60 below the largest one of the run so far at most (a weight 2^-60
+// of the largest is still summed; values below 2^-85 of the largest become 0), and where a reference has to move up because
+// the values do, e_b moves with it.
 #include <math.h>
 
 #include <algorithm>
@@ -78,6 +81,7 @@ constexpr int kSoftmaxRegs = 152, kWidenRegs = 56, kOtherRegs = 64;
 constexpr float kHeadroom = 6.0f;         // log2 of P at the reference: what lies 2^-31 below it still counts
 constexpr float kRescaleThreshold = 6.0f; // log2 units
 constexpr float kHalfSumLimit = 32768.0f; // half a round whose P sums to more moves the reference (P fits fp16)
+constexpr int kValueRange = 60;           // powers of two that a round's e_v may lie below one before it
 
 __host__ __device__ constexpr uint32_t col_s(int i) { return (uint32_t)(i * kBN); }
 __host__ __device__ constexpr uint32_t col_o(int i, int d) { return 256u + (uint32_t)(i * d); }
@@ -450,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int it = 0, n; ok && (n = item_at(it)) > 0; ++it) {
         const int j0 = items[it % kItems].j0;
+        int most_v = kNoExponent;  // of the run so far
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++r) {
           const int st = r % kScaleStages;
@@ -458,7 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int2 info = scale_info[st];
           int e_k, e_v;
           prepare_scales<D>(sScale + st * Raw::kScaleBytes, info.x, (uint32_t)info.y, lane, (j0 + j) * kBN, nan_from[it % kItems],
-                            e_k, e_v);
+                            most_v - kValueRange, e_k, e_v);
+          most_v = max(most_v, e_v);
           if (lane == 0) rounds_info[r % kItems] = Round{(float)e_k, (float)e_v, info.y};
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars.sc_ready[st]));
@@ -653,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             has_b = true;
           }
         }
-        const float to_l = ex2(fminf(fmaxf(e_b - e_v, -126.0f), 126.0f));
+        float to_l = ex2(fminf(fmaxf(e_b - e_v, -126.0f), 126.0f));
         const int lim = my_place - (x.j0 + j) * kBN;  // columns c <= lim are visible to this row
         const bool hidden = info.bad != 0 || __any_sync(0xffffffffu, lim < kBN - 1);
 #pragma unroll 1
@@ -693,7 +699,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float alpha = raise ? ex2(m_ref - mt) : 1.0f;  // 0 for a row that had nothing visible
               const bool scale_o = raise && m_ref != -INFINITY;
               if (raise) {
-                l *= alpha;
+                // what of it the values ask for, and not the scores, leaves the sum as it is
+                const float up = floorf(fminf(fmaxf(e_v - e_b, 0.0f), mt - m_ref));
+                l *= ex2(m_ref - mt + up);
+                e_b += up;
+                to_l = ex2(fminf(fmaxf(e_b - e_v, -126.0f), 126.0f));
                 m_ref = mt;
               }
               const float f = scale_o ? alpha : 1.0f;
@@ -785,7 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (odd_too && top != -INFINITY) {
           w0 = ex2(m_ref - top);
           w1 = ex2(m1 - top);
-          l = l * w0 + l1 * ex2(m1 - top + fminf(fmaxf(e_b - e1, -126.0f), 126.0f));
+          // the sum relative to the larger of both sums' references m - e (within 1)
+          const float e = m1 - e1 > m_ref - e_b ? e1 + floorf(top - m1) : e_b + floorf(top - m_ref);
+          l = l * ex2(m_ref - top + (e - e_b)) + l1 * ex2(m1 - top + (e - e1));
+          e_b = e;
           m_ref = top;
         }
       }

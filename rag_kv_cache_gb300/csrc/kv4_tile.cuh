@@ -74,7 +74,7 @@ __device__ __forceinline__ void widen_word(uint32_t w, __half2 scale, uint32_t (
 
 // The scales of a tile, in place, by one converged warp: bf16 [128 tokens][K NG, V NG] become, for every 8 tokens, fp16 scales
 // of K [8 tokens][NG], then of V [NG][8 tokens]. Tokens from `valid` on, and those of records in `bad`, get 0. e_k and
-// e_v: the tile's exponents; e_v is kNoExponent where all values are 0. A V scale that is not finite gets 0, and
+// e_v: the tile's exponents; e_v is least_v at least, and kNoExponent where all values are 0. A V scale that is not finite gets 0, and
 // nan_from[its group] the least of what it was and first + its token. Two passes of four turns, 32 tokens each, in few
 // instructions: the roles of a kernel share its instruction cache.
 constexpr int kNoExponent = -1000;
@@ -83,7 +83,7 @@ constexpr int kNoExponent = -1000;
 __device__ __forceinline__ int exponent_of(uint32_t top) { return max((int)(top >> 7) - 127 - 12, kLeastExponent); }
 template <int D>
 __device__ __forceinline__ void prepare_scales(uint32_t at, int valid, uint32_t bad, int lane, int first, int* nan_from,
-                                               int& e_k, int& e_v) {
+                                               int least_v, int& e_k, int& e_v) {
   constexpr int NG = Kv4<D>::kGroups;
   auto there = [&](int tok) -> bool { return tok < valid && !(bad >> (tok / kKv4Block) & 1); };
   uint32_t top_k = 0, top_v = 0;  // of both halves of the words
@@ -127,7 +127,7 @@ __device__ __forceinline__ void prepare_scales(uint32_t at, int valid, uint32_t 
     top_v = __reduce_max_sync(0xffffffffu, top_v);
   }
   e_k = exponent_of(top_k);
-  e_v = exponent_of(top_v);
+  e_v = max(exponent_of(top_v), least_v);
   const float fk = power_of_2(-e_k), fv = power_of_2(-e_v);  // e_k, e_v: -120 .. 115
   if (top_v == 0) e_v = kNoExponent;
 #pragma unroll 1

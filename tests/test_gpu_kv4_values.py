@@ -87,3 +87,22 @@ def test_a_group_of_keys_far_below_the_others_with_queries_above(cb, heads, few,
     b.plan.check()
     b.check_weights(w, lse)
     b.plan.close()
+
+
+@pytest.mark.parametrize("how", ["up", "down", "waves", "once", "none"])
+@pytest.mark.parametrize("m", [3, 140])
+def test_values_hundreds_of_powers_apart_leave_the_weights_as_they_are(cb, how, m):
+    # (enough requests for several rounds of 128 keys of one request to meet in a CTA)
+    def edit(k, v):
+        x = np.arange(len(v)) % 3000
+        e = {"up": np.where(x < 1500, -100, 60), "down": np.where(x < 1500, 60, -100), "waves": np.where(x // 128 % 2, 60, -100),
+             "once": np.where(x == 900, 60, -100), "none": np.where(x < 1500, -100, -30)}[how]
+        v *= np.exp2(e)[:, None, None].astype(np.float32)
+        if how == "none":
+            v[x < 700] = 0
+
+    b = Values(cb, (8, 2, 128), [3000] * 20, [m] + [3] * 19, 16, edit=edit)
+    out, lse = b.chunk()
+    b.plan.check()
+    b.check_chunk(out, lse, skip=range(3 if m == 3 else 1, 20))
+    b.plan.close()
