@@ -62,6 +62,8 @@
 // whose weights have to keep 11 bits: V is widened as K is, into fp16, and P_g is held as fp16(p * scale 2^-e) with e from the
 // largest of V's scales that the warp has met, which moves O's units as the references do. 64 requests of 8,192 keys of one
 // token and 4 query heads on each of 8 kv heads: 172 us with a launch of the other kernel for no request, 373 on that one.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "attn_common.cuh"
@@ -136,12 +138,18 @@ struct Kv4DecodeParams {
   float2* part_ml;   // [CTA][2][16 heads]
   int32_t* tickets;  // [CTA]
   int32_t* err;
-  // CHUNK: request s has rows cu[s] .. cu[s + 1] - 1 of q, out [n_rows, heads, D], which G counts as if they were heads
+};
+// CHUNK: request s has rows cu[s] .. cu[s + 1] - 1 of q, out [n_rows, heads, D], which G counts as if they were heads. (A struct
+// of its own, and branches that the decode does not compile at all: four more members cost it 7 registers, tests of constants
+// another order of its instructions; 64 requests 90.1 us in place of 89.6, with 16 query heads per kv head 127.5 for 124.8.)
+struct Kv4FewParams : Kv4DecodeParams {
   const int32_t* cu;
   float* lse;
   int32_t n_rows;
   int32_t lg;  // log2 of the query heads per kv head
 };
+template <bool CHUNK>
+using ParamsOf = std::conditional_t<CHUNK, Kv4FewParams, Kv4DecodeParams>;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -382,7 +390,7 @@ __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.
 // CHUNK: requests of a few rows each (chunk attention): up to 8 NT of tokens times heads take the places of the heads, and
 // requests that have more are left to kv4_chunk.cu. Keys are hidden by row, out and lse go to the rows' places.
 template <int D, int NT, bool PROBE = false, bool CHUNK = false>
-__global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const Kv4DecodeParams p) {
+__global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const ParamsOf<CHUNK> p) {
   constexpr uint64_t kLimit = PROBE ? kProbeTimeoutNs : kTimeoutNs;
   constexpr int NG = Kv4<D>::kGroups;
   constexpr int kWarps = kWarpsOf<NT>, kThreads = kWarps * 32;
@@ -418,24 +426,34 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   };
   const int r = lane / 4, c = lane % 4;
   const int32_t room = p.width * p.page_size;  // fits: the host checks
-  auto row0_of = [&](int s) -> int { return min(max(__ldg(p.cu + s), 0), p.n_rows); };
+  auto row0_of = [&](int s) -> int {
+    if constexpr (CHUNK) return min(max(__ldg(p.cu + s), 0), p.n_rows);
+    return 0;
+  };
   // CHUNK: the rows (tokens) of a request, 0 where this kernel does not take it
   auto tokens_of = [&](int s) -> int {
-    const int m = max(row0_of(s + 1) - row0_of(s), 0);
-    return m <= 8 * NT >> p.lg ? m : 0;
+    if constexpr (CHUNK) {
+      const int m = max(row0_of(s + 1) - row0_of(s), 0);
+      return m <= 8 * NT >> p.lg ? m : 0;
+    }
+    return 1;
   };
   auto len_of = [&](int s) -> int32_t {
-    if (CHUNK && tokens_of(s) == 0) return 0;
+    if constexpr (CHUNK)
+      if (tokens_of(s) == 0) return 0;
     return min(max(__ldg(p.lens + s), 0), room);
   };
   // Row n (of its group of heads) of request s and kv head h in out and lse, -1: there is none.
   auto out_row = [&](int s, int h, int n) -> int64_t {
-    if constexpr (!CHUNK) return ((int64_t)s * p.hkv + h) * p.G + n;
-    if (n >= tokens_of(s) << p.lg) return -1;
-    return (((int64_t)row0_of(s) + (n >> p.lg)) * p.hkv + h << p.lg) + (n & ((1 << p.lg) - 1));
+    if constexpr (CHUNK) {
+      if (n >= tokens_of(s) << p.lg) return -1;
+      return (((int64_t)row0_of(s) + (n >> p.lg)) * p.hkv + h << p.lg) + (n & ((1 << p.lg) - 1));
+    }
+    return ((int64_t)s * p.hkv + h) * p.G + n;
   };
   auto write_lse = [&](int64_t row, float m, float l) {
-    if (CHUNK && p.lse != nullptr) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    if constexpr (CHUNK)
+      if (p.lse != nullptr) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   };
   auto records_of = [&](int s) -> int { return (int)(((int64_t)len_of(s) + kKv4Block - 1) / kKv4Block); };
 
@@ -674,7 +692,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
           const int head = 8 * t + 2 * c + e;
           if (head >= p.G) continue;
           const float inv = inverse(st.l[t][e]);
-          const int64_t to = whole ? out_row(s, h, head) : 0;
+          const int64_t to = CHUNK && !whole ? 0 : out_row(s, h, head);
           if (CHUNK && whole && to >= 0 && r == 0) write_lse(to, st.m[t][e], st.l[t][e]);
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
@@ -784,9 +802,13 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
     const SlotInfo& x = info[g0];
     const float2 ml = s_group[g0][head];
     if (x.p0 >= cta0 && x.p1 <= cta1) {
-      const int64_t to = CHUNK ? out_row(x.pair / p.hkv, x.pair % p.hkv, head) : (int64_t)x.pair * p.G + head;
-      if (to >= 0) write_out4(p.out, to, D, at % (D / 4), acc, inverse(ml.y));
-      if (CHUNK && to >= 0 && at % (D / 4) == 0) write_lse(to, ml.x, ml.y);
+      if constexpr (CHUNK) {
+        const int64_t to = out_row(x.pair / p.hkv, x.pair % p.hkv, head);
+        if (to >= 0) write_out4(p.out, to, D, at % (D / 4), acc, inverse(ml.y));
+        if (to >= 0 && at % (D / 4) == 0) write_lse(to, ml.x, ml.y);
+      } else {
+        write_out4(p.out, (int64_t)x.pair * p.G + head, D, at % (D / 4), acc, inverse(ml.y));
+      }
     } else {
       const int part = blockIdx.x * 2 + (x.p0 < cta0 ? 0 : 1);
       *reinterpret_cast<float4*>(p.part_o + part * kKv4MaxGroup * D + at * 4) = acc;
@@ -858,14 +880,17 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
       }
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-      if (lane == 0) weights[kSums + head] = l, weights[kTops + head] = m;
+      if (lane == 0) {
+        weights[kSums + head] = l;
+        if (CHUNK) weights[kTops + head] = m;
+      }
     }
   }
   __syncthreads();
   auto write_joined = [&](int e, int pr, int head, int i, const float4 a) {
     const float l = scratch[e * kWeights + kSums + head];
     const int64_t to = CHUNK ? out_row(pr / p.hkv, pr % p.hkv, head) : (int64_t)pr * p.G + head;
-    if (to >= 0) write_out4(p.out, to, D, i % (D / 4), a, inverse(l));
+    if (!CHUNK || to >= 0) write_out4(p.out, to, D, i % (D / 4), a, inverse(l));
     if (CHUNK && to >= 0 && i % (D / 4) == 0) write_lse(to, scratch[e * kWeights + kTops + head], l);
   };
   // the threads in teams of n4 (a power of two), each taking every (kThreads / n4)-th part
@@ -918,7 +943,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
 }
 
 template <int D, int NT, bool PROBE = false, bool CHUNK = false>
-cudaError_t launch_t(const Kv4DecodeParams& p, int32_t sms, cudaStream_t s) {
+cudaError_t launch_t(const ParamsOf<CHUNK>& p, int32_t sms, cudaStream_t s) {
   constexpr int kWarps = kWarpsOf<NT>;
   const int64_t most = (int64_t)p.n_seqs * p.hkv * p.width * (p.page_size / kKv4Block);  // records at most
   const int64_t pairs = (int64_t)p.n_seqs * p.hkv;
@@ -955,9 +980,6 @@ Kv4DecodeParams params_of(const void* q, const void* cache, int32_t n_pages, int
   p.part_ml = ws.part_ml;
   p.tickets = ws.tickets;
   p.err = err;
-  p.cu = nullptr;
-  p.lse = nullptr;
-  p.n_rows = p.lg = 0;
   return p;
 }
 
@@ -986,8 +1008,9 @@ cudaError_t launch_kv4_decode_timeout_probe(const void* q, const void* cache, in
 
 cudaError_t launch_kv4_chunk_few(const Kv4Batch& b, int32_t head_dim, void* out, float* lse, const Kv4Scratch& ws,
                                  cudaStream_t s) {
-  Kv4DecodeParams p = params_of(b.q, b.cache, b.n_pages, b.page_size, b.table, b.width, b.kv_lens, b.n_seqs, b.hq, b.hkv,
-                                b.scale, out, ws, b.err);
+  Kv4FewParams p;
+  static_cast<Kv4DecodeParams&>(p) = params_of(b.q, b.cache, b.n_pages, b.page_size, b.table, b.width, b.kv_lens, b.n_seqs,
+                                               b.hq, b.hkv, b.scale, out, ws, b.err);
   p.cu = b.cu;
   p.lse = lse;
   p.n_rows = b.n_rows;
