@@ -1,5 +1,5 @@
-"""Chunk attention and attention weights over 4-bit pages on contents whose parts differ by orders of magnitude,
-against the oracle in 64 bits.
+"""Chunk attention and attention weights over 4-bit pages on contents whose parts differ by orders of magnitude, and on a
+long context whose parts can be told apart, against the oracle in 64 bits.
 
 Tolerances. With s = sum_j p_j |v_j| of the output's own dim, an output is within (2^-11 + 2 e + 2^-20 + t) s of the exact
 value, and 2^-8 of itself by its rounding to bf16: a softmax weight is rounded to fp16 once (2^-11), scores are off by at most
@@ -16,6 +16,7 @@ e + 2^-20 + 2^-22 |lse| + n 2^-24.
 
 import numpy as np
 import pytest
+import torch
 from test_gpu_kv4_batch import Batch, _f64
 
 from oracle import serving
@@ -53,6 +54,36 @@ def check(b, out, lse, rows_of=None, few=False):
             assert (err <= lim).all(), f"request {s}, row {i}: err/limit {np.nanmax(err / lim):.3f}"
             err, lim = np.abs(glse[a + i] - rlse[0]), e + 2.0**-20 + 2.0**-22 * np.abs(rlse[0]) + n * 2.0**-24
             assert (err <= lim).all(), f"lse of request {s}, row {i}: err/limit {np.nanmax(err / lim):.3f}"
+
+
+def _segments(k, v):
+    """Values that are 1 in one dim and 0 in the others, by the part of the context: an output is the weight of a part."""
+    n, _, d = v.shape
+    v[:] = 0
+    v[np.arange(n), :, np.arange(n) * d // n] = 1
+
+
+@pytest.mark.parametrize("m", [1, 3, 40, 150])
+@pytest.mark.parametrize("heads", [(32, 8, 128), (16, 1, 64), (8, 4, 128), (16, 16, 128)])
+def test_each_part_of_a_long_context_has_its_weight(cb, heads, m):
+    # one request over all SMs, joined: a part that is lost or weighed wrongly shows in the dim that stands for it
+    b = Values(cb, heads, [20011], [m], 64, qs=0.5, edit=_segments)
+    out, lse = b.chunk()
+    b.plan.check()
+    check(b, out, lse, rows_of=range(m) if m < 4 else (0, m // 2, m - 1))
+    b.plan.close()
+
+
+@pytest.mark.parametrize("heads,n", [((32, 8, 128), 33), ((16, 1, 64), 70), ((32, 16, 64), 20)])
+def test_each_part_of_a_long_context_has_its_weight_with_few_rows(cb, heads, n):
+    # a long request among short ones, on the kernel for few rows: its parts are merged within CTAs and over them
+    lens, new = [50] * n, [1] * n
+    lens[n // 2] = 20011
+    b = Values(cb, heads, lens, new, 32, qs=0.5, edit=lambda k, v: _segments(k[50 * (n // 2):][:20011], v[50 * (n // 2):][:20011]))
+    out, lse = b.chunk()
+    b.plan.check()
+    check(b, out, lse, few=True)
+    b.plan.close()
 
 
 @pytest.mark.parametrize("down", [4, 12, 16, 24])
@@ -105,4 +136,33 @@ def test_values_hundreds_of_powers_apart_leave_the_weights_as_they_are(cb, how, 
     out, lse = b.chunk()
     b.plan.check()
     b.check_chunk(out, lse, skip=range(3 if m == 3 else 1, 20))
+    b.plan.close()
+
+
+@pytest.mark.parametrize("how", ["up", "down", "waves", "once"])
+def test_values_hundreds_of_powers_apart_with_few_rows(cb, how):
+    def edit(k, v):
+        x = np.arange(len(v))
+        e = {"up": np.where(x < 1500, -100, 60), "down": np.where(x < 1500, 60, -100), "waves": np.where(x // 16 % 2, 60, -100),
+             "once": np.where(x == 900, 60, -100)}[how]
+        v *= np.exp2(np.where(x < 3000, e, 0))[:, None, None].astype(np.float32)
+
+    b = Values(cb, (32, 8, 128), [3000] + [90] * 32, [2] + [1] * 32, 16, edit=edit)
+    out, lse = b.chunk()
+    b.plan.check()
+    b.check_chunk(out, lse)
+    b.plan.close()
+
+
+def test_rows_of_different_magnitudes(cb):
+    # rows that share a tile, 2^-20 and 2^-30 of one another: the softmax of each is its own
+    b = Values(cb, (8, 2, 128), [300, 90], [140, 9], 16)
+    scale = torch.tensor([1.0, 2.0**-20, 2.0**-30], device="cuda")[torch.arange(b.rows, device="cuda") % 3]
+    b.q.mul_(scale[:, None, None].bfloat16())
+    out, lse = b.chunk()
+    b.plan.check()
+    b.check_chunk(out, lse)
+    w = b.weights(lse)
+    b.plan.check()
+    b.check_weights(w, lse)
     b.plan.close()
