@@ -225,6 +225,7 @@ cb_status cb_plan_create(const cb_config* cfg, cb_plan** out) {
   if (e == cudaSuccess) e = cudaMalloc(&p->chunk.part_o, sizeof(float) * chunk_rows * c.head_dim);
   if (e == cudaSuccess) e = cudaMalloc(&p->chunk.part_ml, sizeof(float2) * chunk_rows);
   if (e == cudaSuccess) e = cudaMalloc(&p->chunk.parts, cb::kv4_chunk_parts_bytes(p->chunk.sms));
+  if (e == cudaSuccess) e = cudaMalloc(&p->chunk.own, sizeof(float2) * cb::kv4_chunk_own_keys(p->chunk.sms));
   p->chunk.few.sms = p->chunk.sms;
   if (e == cudaSuccess) e = cudaMalloc(&p->chunk.few.part_o, sizeof(float) * kv4_units * c.head_dim);
   if (e == cudaSuccess) e = cudaMalloc(&p->chunk.few.part_ml, sizeof(float2) * kv4_units);
@@ -273,6 +274,7 @@ cb_status cb_plan_destroy(cb_plan* plan) {
   cudaFree(plan->chunk.part_o);
   cudaFree(plan->chunk.part_ml);
   cudaFree(plan->chunk.parts);
+  cudaFree(plan->chunk.own);
   cudaFree(plan->chunk.few.part_o);
   cudaFree(plan->chunk.few.part_ml);
   cudaFree(plan->chunk.few.tickets);

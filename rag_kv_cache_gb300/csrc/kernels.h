@@ -221,11 +221,13 @@ struct Kv4ChunkScratch {
   float* part_o;    // [kv4_chunk_part_rows][D]
   float2* part_ml;  // [kv4_chunk_part_rows]
   void* parts;      // kv4_chunk_parts_bytes
+  float2* own;      // [kv4_chunk_own_keys]: exponents of keys and values of their own, by CTA and round
   Kv4Scratch few;   // of launch_kv4_chunk_few
   int32_t sms;
 };
 size_t kv4_chunk_part_rows(int32_t sms);
 size_t kv4_chunk_parts_bytes(int32_t sms);
+size_t kv4_chunk_own_keys(int32_t sms);
 cudaError_t launch_kv4_chunk(const Kv4Batch& b, int32_t head_dim, void* out, float* lse, const Kv4ChunkScratch& ws,
                              cudaStream_t s);
 // The requests of few rows of a chunk attention call, by the decode kernel (kv4_decode.cu) with rows for heads: those of at most

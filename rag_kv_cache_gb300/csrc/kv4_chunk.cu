@@ -45,6 +45,10 @@
 // The sum itself must not depend on the values: an e_v lies 60 below the largest one of the run so far at most (a weight 2^-60
 // of the largest is still summed; values below 2^-85 of the largest become 0), and where a reference has to move up because
 // the values do, e_b moves with it.
+//
+// Nor may a row depend on keys that it does not see, which may be of any size. Those behind an item's last row count as zeros.
+// Where the keys of a round that some of its rows do not see lie more than 2^20 apart, each has a power of its own for its key
+// and its value, and the round's softmax goes by columns, twice over the scores (`wide`, rare: not made fast).
 #include <math.h>
 
 #include <algorithm>
@@ -101,6 +105,7 @@ struct Round {
   float e_k;  // exponents of the round's keys and values (kNoExponent: all values are 0)
   float e_v;
   int bad;    // its records whose page is none
+  int wide;   // its keys have exponents of their own
 };
 // What the join needs of an item that begins in a CTA and goes on in the next.
 struct Part {
@@ -128,6 +133,7 @@ struct ChunkParams {
   float* part_o;    // [CTA][2][256 rows][D]
   float2* part_ml;  // [CTA][2][256 rows]
   Part* parts;      // [CTA]
+  float2* own;      // [CTA][kItems][128 keys]: exponents of a wide round's keys and values
   int lg;           // log2 of the query heads per kv head
   int few;          // requests of so many rows or fewer are another kernel's
   int run;          // records per copy: the four of a unit or two, where a page holds so many or a multiple, else 1
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scales were rewritten in place
           if (lane == 0) {
-            scale_info[st] = make_int2(max(rq.len - (j0 + j) * kBN, 0), (int)bad);
+            scale_info[st] = make_int2(max(min(rq.len, x.place0 + x.tokens) - (j0 + j) * kBN, 0), (int)bad);
             if (held != 0)
               mbar_expect_tx(smem_u32(&bars.sc_full[st]), __popc(held) * p.run * Raw::kScaleRecord);
             else
@@ -453,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int r = 0;
       bool ok = true;
       for (int it = 0, n; ok && (n = item_at(it)) > 0; ++it) {
-        const int j0 = items[it % kItems].j0;
+        const int j0 = items[it % kItems].j0, place0 = items[it % kItems].place0;
         int most_v = kNoExponent;  // of the run so far
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++r) {
@@ -462,10 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           const int2 info = scale_info[st];
           int e_k, e_v;
-          prepare_scales<D>(sScale + st * Raw::kScaleBytes, info.x, (uint32_t)info.y, lane, (j0 + j) * kBN, nan_from[it % kItems],
-                            most_v - kValueRange, e_k, e_v);
+          const bool wide = prepare_scales<D>(sScale + st * Raw::kScaleBytes, info.x, (uint32_t)info.y, lane, (j0 + j) * kBN,
+                                              nan_from[it % kItems], most_v - kValueRange,
+                                              (j0 + j) * kBN + min(info.x, kBN) - 1 > place0,
+                                              p.own + ((int)blockIdx.x * kItems + r % kItems) * kBN, e_k, e_v);
           most_v = max(most_v, e_v);
-          if (lane == 0) rounds_info[r % kItems] = Round{(float)e_k, (float)e_v, info.y};
+          if (lane == 0) rounds_info[r % kItems] = Round{(float)e_k, (float)e_v, info.y, wide};
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars.sc_ready[st]));
         }
@@ -647,9 +655,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s0[kQuarter], s1[kQuarter];
         tmem_ld_x32_async(taddr, s0);
         const Round info = rounds_info[rr % kItems];
-        // the row's factor in this round (not 0, which times -infinity, a hidden key's score, is NaN)
-        const float e = info.e_k + e_row, eh = floorf(0.5f * e);
-        const float a = fmaxf(a_row * ex2(eh) * ex2(e - eh), 1.2e-38f) + (a_row - a_row);
+        // the row's factor for keys of exponent e_k (not 0, which times -infinity, a hidden key's score, is NaN)
+        auto factor = [&](float e_k) -> float {
+          const float e = e_k + e_row, eh = floorf(0.5f * e);
+          return fmaxf(a_row * ex2(eh) * ex2(e - eh), 1.2e-38f) + (a_row - a_row);
+        };
+        const int lim = my_place - (x.j0 + j) * kBN;  // columns c <= lim are visible to this row
+        if (__builtin_expect(info.wide != 0, 0)) {
+          tmem_wait_ld(s0);
+          const float2* own = p.own + ((int)blockIdx.x * kItems + rr % kItems) * kBN;
+          // Columns 16 u .. + 15: their scores (log2 units) and values' exponents.
+          auto columns = [&](int u, float (&y)[16], float (&ev)[16]) {
+            uint32_t z[16];
+            tmem_ld_x16(taddr + 16 * u, z);
+            const bool gone = info.bad >> u & 1;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = __ldcg(own + 16 * u + i);
+              y[i] = gone || 16 * u + i > lim ? -INFINITY : __uint_as_float(z[i]) * factor(e.x);
+              ev[i] = e.y;
+            }
+          };
+          float y[16], ev[16];
+          float most = -INFINITY, top = -INFINITY;  // score; score and value
+#pragma unroll 1
+          for (int u = 0; u < kBN / 16; ++u) {
+            columns(u, y, ev);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              most = fmaxf(most, y[i]);
+              top = fmaxf(top, y[i] + ev[i]);
+            }
+          }
+          float f = 1.0f;
+          const float mt = top - kHeadroom;
+          if (mt > m_ref + kRescaleThreshold) {  // by whole powers of two, and e_b with it: the sum stays as it is
+            const float by = m_ref == -INFINITY ? 0.0f : ceilf(mt - m_ref);
+            f = ex2(-by);
+            e_b = m_ref == -INFINITY ? floorf(top - most) : e_b + by;
+            m_ref = m_ref == -INFINITY ? mt : m_ref + by;
+          }
+          const float over = floorf(most - kHeadroom - (m_ref - e_b));
+          if (over > 30.0f && m_ref != -INFINITY) {  // scores far above those before, of small values
+            l *= ex2(-over);
+            e_b -= over;
+          }
+          has_b = has_b || m_ref != -INFINITY;
+          if (j > first && __any_sync(0xffffffffu, f != 1.0f)) {
+            if (!wait(bars.o_done[ti], (done - 1) & 1, 116 + ti)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int i0 = 0; i0 < D; i0 += 16) {
+              uint32_t o[16];
+              tmem_ld_x16(lane_base + col_o(ti, D) + i0, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_x16(lane_base + col_o(ti, D) + i0, o);
+            }
+          }
+          const float off = m_ref == -INFINITY ? 0.0f : m_ref, off_l = m_ref == -INFINITY ? 0.0f : m_ref - e_b;
+#pragma unroll 1
+          for (int u = 0; u < kBN / 16; ++u) {  // (a column of P lies over scores that have been read)
+            columns(u, y, ev);
+            uint32_t pk[8];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              l += ex2(y[i] - off_l) + ex2(y[i + 1] - off_l);
+              pk[i / 2] = h2_bits(__floats2half2_rn(ex2(y[i] + (ev[i] - off)), ex2(y[i + 1] + (ev[i + 1] - off))));
+            }
+            tmem_st_x8(taddr + 8 * u, pk);
+          }
+          tmem_st_wait();
+          return true;
+        }
+        const float a = factor(info.e_k);
         float e_v = e_b;
         if (info.e_v != (float)kNoExponent) {
           e_v = info.e_v;
@@ -660,7 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         float to_l = ex2(fminf(fmaxf(e_b - e_v, -126.0f), 126.0f));
-        const int lim = my_place - (x.j0 + j) * kBN;  // columns c <= lim are visible to this row
         const bool hidden = info.bad != 0 || __any_sync(0xffffffffu, lim < kBN - 1);
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
@@ -932,6 +1010,7 @@ cudaError_t launch_t(const Kv4Batch& b, void* out, float* lse, const Kv4ChunkScr
   p.part_o = ws.part_o;
   p.part_ml = ws.part_ml;
   p.parts = static_cast<Part*>(ws.parts);
+  p.own = ws.own;
   p.lg = 31 - __builtin_clz(b.hq / b.hkv);
   p.few = PROBE ? 0 : kv4_chunk_few_rows(b) >> p.lg;
   // (1.15 ms for 2,048 tokens over 30,720 where each record has a copy of its own, 1.13 with four to a copy)
@@ -959,6 +1038,7 @@ cudaError_t launch_t(const Kv4Batch& b, void* out, float* lse, const Kv4ChunkScr
 
 size_t kv4_chunk_part_rows(int32_t sms) { return (size_t)sms * 2 * kTiles * kBM; }
 size_t kv4_chunk_parts_bytes(int32_t sms) { return (size_t)sms * sizeof(Part); }
+size_t kv4_chunk_own_keys(int32_t sms) { return (size_t)sms * kItems * kBN; }
 
 // (Request, kv head) pairs of a batch from which on its requests of few rows are worth a launch of their own, whether it has
 // any or not; where the mean request has so few rows, fewer are enough. With and without the launch, us, 32 query on 8 kv

@@ -77,13 +77,16 @@ __device__ __forceinline__ void widen_word(uint32_t w, __half2 scale, uint32_t (
 // e_v: the tile's exponents; e_v is least_v at least, and kNoExponent where all values are 0. A V scale that is not finite gets 0, and
 // nan_from[its group] the least of what it was and first + its token. Two passes of four turns, 32 tokens each, in few
 // instructions: the roles of a kernel share its instruction cache.
+//   mixed: not every row sees every token. Where one's largest scale then lies more than 2^20 below the tile's, it returns
+// true, each token has exponents of its own, and `own` [128 tokens] holds them (global memory).
 constexpr int kNoExponent = -1000;
+constexpr int kCommonRange = 20;  // the other 9 of 29 powers of two are left to the groups of a token
 // The exponent of a tile whose largest scale has the bits `top`: one in [2^x, 2^(x+1)) times 2^-e, e >= x - 12, lies below
 // 2^13, eight times it (a bf16's 8 bits) below fp16's largest value.
 __device__ __forceinline__ int exponent_of(uint32_t top) { return max((int)(top >> 7) - 127 - 12, kLeastExponent); }
 template <int D>
-__device__ __forceinline__ void prepare_scales(uint32_t at, int valid, uint32_t bad, int lane, int first, int* nan_from,
-                                               int least_v, int& e_k, int& e_v) {
+__device__ __forceinline__ bool prepare_scales(uint32_t at, int valid, uint32_t bad, int lane, int first, int* nan_from,
+                                               int least_v, bool mixed, float2* own, int& e_k, int& e_v) {
   constexpr int NG = Kv4<D>::kGroups;
   auto there = [&](int tok) -> bool { return tok < valid && !(bad >> (tok / kKv4Block) & 1); };
   uint32_t top_k = 0, top_v = 0;  // of both halves of the words
@@ -129,6 +132,41 @@ __device__ __forceinline__ void prepare_scales(uint32_t at, int valid, uint32_t 
   e_k = exponent_of(top_k);
   e_v = max(exponent_of(top_v), least_v);
   const float fk = power_of_2(-e_k), fv = power_of_2(-e_v);  // e_k, e_v: -120 .. 115
+  bool wide = false;
+  if (mixed) {  // (a tile or two of an item)
+#pragma unroll 1
+    for (int i = 0; i < 2 * kTileTokens / 32; ++i) {
+      const int tok = i / 2 * 32 + lane;
+      uint32_t w[NG / 2];
+      lds<NG / 2>(w, at + tok * (4 * NG) + i % 2 * (2 * NG));
+      const uint32_t x = __vmaxu2(w[0] & 0x7fff7fffu, w[NG / 2 - 1] & 0x7fff7fffu), top = max(x & 0xffffu, x >> 16);
+      wide = wide || (there(tok) && top > 0 && top + (kCommonRange << 7) < (i % 2 == 0 ? top_k : top_v));
+    }
+    wide = __any_sync(0xffffffffu, wide);
+  }
+  if (wide) {  // rare: the tokens' scales to the size of the tile's largest
+#pragma unroll 1
+    for (int i = 0; i < 2 * kTileTokens / 32; ++i) {
+      const int tok = i / 2 * 32 + lane, v = i % 2;
+      const uint32_t scales = at + tok * (4 * NG) + v * (2 * NG);
+      uint32_t top = 0, w;
+#pragma unroll 1
+      for (int g = 0; g < NG && there(tok); ++g) {
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w) : "r"(scales + 2 * g) : "memory");
+        if ((w & 0x7fffu) < 0x7f80u) top = max(top, w & 0x7fffu);
+      }
+      const int e = exponent_of(top), by = (v == 0 ? e_k : e_v) - e;  // by: 0 .. 235
+#pragma unroll 1
+      for (int g = 0; g < NG && there(tok); ++g) {
+        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w) : "r"(scales + 2 * g) : "memory");
+        const float x = __uint_as_float(w << 16) * power_of_2(by >> 1) * power_of_2(by - (by >> 1));
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(scales + 2 * g), "h"((uint16_t)(__float_as_uint(x) >> 16)) : "memory");
+      }
+      (v == 0 ? own[tok].x : own[tok].y) = (float)e;
+    }
+    __threadfence();
+    __syncwarp();
+  }
   if (top_v == 0) e_v = kNoExponent;
 #pragma unroll 1
   for (int k = 0; k < kTileTokens / 32; ++k) {
@@ -154,6 +192,7 @@ __device__ __forceinline__ void prepare_scales(uint32_t at, int valid, uint32_t 
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 16), "h"((uint16_t)(h >> 16)) : "memory");
     }
   }
+  return wide;
 }
 
 // Keys of unit u: records first .. first + count - 1 of the unit at `raw` into the K-major tile at `tile` (rows of 64

@@ -31,7 +31,7 @@ class Values(Batch):
 
 
 def check(b, out, lse, rows_of=None, few=False):
-    """Every request's out and lse (of its rows rows_of only, where there are many) within the limits above."""
+    """Every request's out and lse (of its rows rows_of(request) only, where that is given) within the limits above."""
     got, glse, q = _f64(out), lse.cpu().numpy().astype(np.float64), _f64(b.q)
     c = b.d**-0.5
     for s in range(len(b.lens)):
@@ -39,7 +39,7 @@ def check(b, out, lse, rows_of=None, few=False):
         if m == 0:
             continue
         k, v = b.cached(s)
-        for i in range(m) if rows_of is None else rows_of:
+        for i in range(m) if rows_of is None else rows_of(s):
             n = len(k) - m + i + 1
             kk, vv, qq = k[:n], v[:n], q[a + i:a + i + 1]
             ref, rlse, vs = serving.chunk_attention(qq, kk, vv)
@@ -70,7 +70,7 @@ def test_each_part_of_a_long_context_has_its_weight(cb, heads, m):
     b = Values(cb, heads, [20011], [m], 64, qs=0.5, edit=_segments)
     out, lse = b.chunk()
     b.plan.check()
-    check(b, out, lse, rows_of=range(m) if m < 4 else (0, m // 2, m - 1))
+    check(b, out, lse, rows_of=lambda s: range(m) if m < 4 else (0, m // 2, m - 1))
     b.plan.close()
 
 
@@ -165,4 +165,46 @@ def test_rows_of_different_magnitudes(cb):
     w = b.weights(lse)
     b.plan.check()
     b.check_weights(w, lse)
+    b.plan.close()
+
+
+@pytest.mark.parametrize("up", [20, 40, 100])
+@pytest.mark.parametrize("what", ["keys", "values", "both"])
+@pytest.mark.parametrize("heads,few,m", [((8, 2, 128), False, 140), ((16, 16, 64), False, 40), ((32, 2, 128), False, 12)])
+def test_later_keys_of_any_size_do_not_reach_a_row(cb, heads, few, m, what, up):
+    # keys and values 2^up of the others from the request's last rows on: hidden from its rows before
+    n, late = 300, max(m // 3, 1)
+    at = n - late  # the first such key
+
+    def edit(k, v):
+        if what != "values":
+            k[at:n] *= 2.0**up
+        if what != "keys":
+            v[at:n] *= 2.0**up
+
+    lens, new = ([n] + [50] * 33, [m] + [1] * 33) if few else ([n, 129], [m, 5])
+    b = Values(cb, heads, lens, new, 16, edit=edit)
+    out, lse = b.chunk()
+    b.plan.check()
+    check(b, out, lse, rows_of=lambda s: range(m - late if s == 0 else b.new[s]), few=few)
+    b.plan.close()
+
+
+@pytest.mark.parametrize("down", [30, 70])
+@pytest.mark.parametrize("what", ["keys", "values", "both"])
+def test_keys_of_many_sizes_in_a_round(cb, what, down):
+    # every third key (or value) 2^-down of the others, some zero; enough requests for a CTA to take several rounds
+    def edit(k, v):
+        x = np.arange(len(v)) % 3000
+        for t, name in ((k, "keys"), (v, "values")):
+            if what in (name, "both"):
+                t[x % 3 == 1] *= 2.0**-down
+                t[x % 50 == 7] = 0
+
+    b = Values(cb, (8, 2, 128), [3000] * 20, [40] + [3] * 19, 16, qs=0.5, edit=edit)
+    out, lse = b.chunk()
+    b.plan.check()
+    b.check_chunk(out, lse, skip=range(3, 20))
+    again, l2 = b.chunk()
+    assert torch.equal(again, out) and torch.equal(l2, lse)
     b.plan.close()
