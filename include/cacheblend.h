@@ -465,7 +465,7 @@ cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const
  * (within 2^-85 of it); softmax weights are rounded to fp16, q to within 2^-35 of its head's largest magnitude. In a
  * batch of many requests those of up to 8 rows per kv head (16 where 16 heads share one) run on mma.sync: codes and
  * K's scales are exact there, a weight times V's scale is rounded to fp16 (to 2^-31 where it is small against the
- * largest scale that the request's rows have met). So a request's results depend on the batch that it comes in, within
+ * largest scale that the row has met). So a request's results depend on the batch that it comes in, within
  * these roundings; a call's repetition gives the same bits. n_rows (in tiles of 128 / (hq/hkv), each request one more)
  * times hkv times the larger of table_width * P and n_rows over 128 must stay below 2^30, table_width * P may not pass
  * it (CB_ERR_UNSUPPORTED). A bounded wait that gives up records CB_ERR_TIMEOUT.

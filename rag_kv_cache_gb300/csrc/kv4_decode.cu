@@ -60,7 +60,7 @@
 //
 // The same kernel (CHUNK) takes the requests of few rows, several tokens among them, of a chunk attention call (kv4_chunk.cu),
 // whose weights have to keep 11 bits: V is widened as K is, into fp16, and P_g is held as fp16(p * scale 2^-e) with e from the
-// largest of V's scales that the warp has met, which moves O's units as the references do. 64 requests of 8,192 keys of one
+// largest of V's scales that the row has seen, which moves O's units as the references do. 64 requests of 8,192 keys of one
 // token and 4 query heads on each of 8 kv heads: 172 us with a launch of the other kernel for no request, 373 on that one.
 #include <type_traits>
 
@@ -170,8 +170,8 @@ struct State {
   static constexpr int NG = Kv4<D>::kGroups;
   float o[NT][2 * NG][4];    // O^T, dims 32 g + 4 r + .. (r = lane / 4)
   float m[NT][2], l[NT][2];  // reference (log2 units, the same in all lanes of a head), this lane's share of the sum
-  int top;  // CHUNK: the largest exponent of V's scales so far (biased, the warp's); o is in units of 2^(top - 133 - 24) for
-            // the dims of codes in low nibbles, of 2^(top - 133 - 20) for the others
+  int top[NT][2];  // CHUNK: the largest exponent of V's scales that the row has seen so far (biased); o is in units of
+                   // 2^(top - 133 - 24) for the dims of codes in low nibbles, of 2^(top - 133 - 20) for the others
 };
 
 template <int D, int NT>
@@ -183,7 +183,7 @@ __device__ __forceinline__ void reset(State<D, NT>& st) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) st.o[t][i][e] = 0.0f;
     st.m[t][0] = st.m[t][1] = kLow;
-    st.top = 7;  // 2^(133 - top) is a float
+    st.top[t][0] = st.top[t][1] = 15;  // a weight (to 2^8) times 2^(133 - top) is a float
     st.l[t][0] = st.l[t][1] = 0.0f;
   }
 }
@@ -229,27 +229,26 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
     for (int e = 0; e < 4; ++e) pr[t][e] = ex2(fmaf(s[t][e], qf.scale[t][e % 2], -st.m[t][e % 2]));
     most = fmaxf(max3(most, pr[t][0], pr[t][1]), fmaxf(pr[t][2], pr[t][3]));
   }
-  uint32_t scale_top = 0;
+  bool larger = false;  // CHUNK: than the scales so far
   if constexpr (CHUNK) {
+    uint32_t scale_top = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int g = NG / 2; g < NG; ++g) scale_top = __vmaxu2(scale_top, sc[h][g] & 0x7fff7fffu);
     scale_top = max(scale_top >> 16, scale_top & 0xffffu) >> 7;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) larger = larger || (int)scale_top > min(st.top[t][0], st.top[t][1]);
   }
-  const bool high = most > kHigh || (CHUNK && (int)scale_top > st.top);
+  const bool high = most > kHigh || larger;
   if (__any_sync(0xffffffffu, high)) {
-    float unit = 1.0f;
+    int token_top[2] = {0, 0};  // CHUNK: of tokens r and r + 8, of the scales that are finite
     if constexpr (CHUNK) {
-      uint32_t most_scale = 0;  // of those that are finite
 #pragma unroll
       for (int i = 0; i < 2 * NG; ++i) {
-        const uint32_t e = sc[i / NG][NG / 2 + i % NG / 2] >> (i % 2 ? 23 : 7) & 0xffu;
-        if (e < 255u) most_scale = max(most_scale, e);
+        const int e = sc[i / NG][NG / 2 + i % NG / 2] >> (i % 2 ? 23 : 7) & 0xffu;
+        if (e < 255) token_top[i / NG] = max(token_top[i / NG], e);
       }
-      const int top = max((int)__reduce_max_sync(0xffffffffu, most_scale), st.top);
-      unit = power_of_2(max(st.top - top, -126));  // (what is below 2^-126 of the new ones rounds to nothing)
-      st.top = top;
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -264,11 +263,19 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
         alpha[e] = move ? ex2(st.m[t][e] - top) : 1.0f;  // 0 where the head had nothing
         if (move) st.m[t][e] = top;
         st.l[t][e] *= alpha[e];
+        if constexpr (CHUNK) {  // the units follow the scales of the tokens that the row sees
+          int seen = max(WHOLE || r < sees[t][e] ? token_top[0] : 0, WHOLE || r + 8 < sees[t][e] ? token_top[1] : 0);
+          seen = max(seen, __shfl_xor_sync(0xffffffffu, seen, 4));
+          seen = max(seen, __shfl_xor_sync(0xffffffffu, seen, 8));
+          seen = max(max(seen, __shfl_xor_sync(0xffffffffu, seen, 16)), st.top[t][e]);
+          alpha[e] *= power_of_2(max(st.top[t][e] - seen, -126));  // (what is below 2^-126 of the new ones rounds to nothing)
+          st.top[t][e] = seen;
+        }
       }
 #pragma unroll
       for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[t][i][e] *= CHUNK ? alpha[e % 2] * unit : alpha[e % 2];
+        for (int e = 0; e < 4; ++e) st.o[t][i][e] *= alpha[e % 2];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         pr[t][e] = ex2(fmaf(s[t][e], qf.scale[t][e % 2], -st.m[t][e % 2]));
@@ -283,11 +290,16 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
   // V words of both halves
 #pragma unroll
   for (int h = 0; h < 2; ++h) load_vec<NG>(w[h], rec + Kv4<D>::kV + h * Kv4<D>::kPlane + lane * (4 * NG));
-  const float unit_of_p = CHUNK ? power_of_2(133 - st.top) : 1.0f;  // weights to 2^8, scales below 2: P to 2^15
+  if constexpr (CHUNK) {  // weights to 2^8, scales below 2: P to 2^15
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pr[t][e] *= power_of_2(133 - st.top[t][e % 2]);
+  }
   uint32_t pb[NT][NG][2];  // P times the scales of group g: keys 0-7, keys 8-15
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const float s0 = CHUNK ? vs(0, g) * unit_of_p : vs(0, g), s1 = CHUNK ? vs(1, g) * unit_of_p : vs(1, g);
+    const float s0 = vs(0, g), s1 = vs(1, g);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float x[4] = {pr[t][0] * s0, pr[t][1] * s0, pr[t][2] * s1, pr[t][3] * s1};
@@ -699,7 +711,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
             float4 x = make_float4(st.o[t][2 * g][e], st.o[t][2 * g][e + 2], st.o[t][2 * g + 1][e],
                                    st.o[t][2 * g + 1][e + 2]);
             if constexpr (CHUNK) {
-              const float unit = power_of_2(st.top - 133);
+              const float unit = power_of_2(st.top[t][e] - 133);
               x = make_float4(x.x * 16777216.0f * unit, x.y * 1048576.0f * unit, x.z * 16777216.0f * unit, x.w * 1048576.0f * unit);
             }
             if (CHUNK && to < 0) continue;

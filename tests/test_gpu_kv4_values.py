@@ -170,7 +170,8 @@ def test_rows_of_different_magnitudes(cb):
 
 @pytest.mark.parametrize("up", [20, 40, 100])
 @pytest.mark.parametrize("what", ["keys", "values", "both"])
-@pytest.mark.parametrize("heads,few,m", [((8, 2, 128), False, 140), ((16, 16, 64), False, 40), ((32, 2, 128), False, 12)])
+@pytest.mark.parametrize("heads,few,m", [((8, 2, 128), False, 140), ((16, 16, 64), False, 40), ((32, 2, 128), False, 12),
+                                         ((8, 8, 128), True, 8), ((16, 8, 64), True, 4), ((32, 8, 128), True, 2)])
 def test_later_keys_of_any_size_do_not_reach_a_row(cb, heads, few, m, what, up):
     # keys and values 2^up of the others from the request's last rows on: hidden from its rows before
     n, late = 300, max(m // 3, 1)
