@@ -484,10 +484,10 @@ cb_status cb_kv4_chunk_attention(cb_plan* plan, const void* q, const void* cache
  * j. earlier is added for the tokens that were cached before these rows (j < kv_lens[s] - m); NULL: 0. weights,
  * earlier: float32 [n_seqs, hkv, table_width * P]; earlier may be weights (in place), else they must not overlap.
  * Entries from kv_lens[s] on, and those of a request without rows, are left as they are. A row whose lse is
- * -infinity adds nothing. The order of the sum is fixed, in fp32; the keys are held as in cb_kv4_chunk_attention, with a
- * power of two for every 16 (exact for requests of few rows, which run on mma.sync). Recorded, and the limits on
- * sizes, as for cb_kv4_chunk_attention (a key of a bad page gets no weight of these rows). No scratch: calls on one
- * plan may overlap. */
+ * -infinity adds nothing. The order of the sum is fixed, in fp32; the keys are held as in cb_kv4_chunk_attention, each with
+ * a power of two of its own (exact for requests of few rows, which run on mma.sync). Recorded, and the limits on sizes,
+ * as for cb_kv4_chunk_attention (a key of a bad page gets no weight of these rows). No scratch: calls on one plan may
+ * overlap. */
 cb_status cb_kv4_attention_weights(cb_plan* plan, const void* q, const float* lse, const void* cache, int32_t n_pages,
                                    int32_t page_size, const int32_t* table, int32_t table_width,
                                    const int32_t* cu_seqlens, const int32_t* kv_lens, int32_t n_seqs, int32_t n_rows,

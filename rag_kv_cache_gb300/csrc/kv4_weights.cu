@@ -29,7 +29,8 @@
 // a product takes a group 3,900 cycles with three at work (2,730 with two; 512 cycles of a scheduler's transcendental pipe).
 // Scores loaded 32 columns at a time in place of 16 ahead: 140 us.
 //
-// Powers of two: keys are held as k 2^-e_k per record of 16 tokens (a lane's factor), rows as q 2^-e_q per 128 rows.
+// Powers of two: a key is held as k 2^-e_k (its lane's factor; no key, seen or not, takes bits from another), rows as q 2^-e_q
+// per 128 rows.
 #include <math.h>
 
 #include <algorithm>
@@ -62,7 +63,10 @@ constexpr int kWarpUnits = kWarpRows + 1; // makes the list of units
 constexpr int kUnitReaders = kWarpUnits;  // all other warps
 constexpr int kThreads = 32 * (kWarpUnits + 1);
 constexpr uint32_t kTmemCols = 512;
-constexpr float kBadRecord = -4096.0f;  // in place of a record's exponent: its page is none
+constexpr int kBadRecord = -128;  // in place of a token's exponent: its page is none
+// Units whose tokens' exponents are held. A unit's keys are widened once the last product of the unit before is complete, which
+// was issued once the scores of the fourth product before it were taken; a unit has one product at least.
+constexpr int kHeldUnits = kTiles + 1;
 
 struct WeightsParams {
   Kv4Batch b;
@@ -146,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Unit units[kUnits];
   __shared__ alignas(16) float s_lse[kLseStages][kRows];  // -lse in log2 units, -inf where there is no row
   __shared__ float s_eq[kLseStages];                     // the rows' exponent
-  __shared__ float s_ek[kUnits][kTiles][kTile / kKv4Block];  // the records' exponents, by unit (the next ones' keys may
-                                                             // come while the last scores are worked on)
+  __shared__ int8_t s_ek[kHeldUnits][kTiles][kTile];  // the tokens' exponents, by unit (the next ones' keys may come while
+                                                      // the last scores are worked on)
   __shared__ float s_part[2][kGroups - 1][kTiles][kTile];    // sums for the group that writes a tile, from those after it
   __shared__ uint32_t s_top[2][kWidenWarps];
   __shared__ uint32_t s_tmem;
@@ -315,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int buf = (sn + q) % kTiles;
           ok = wait(bars.s_full[buf], (sn + q) / kTiles & 1, 131);
           tc_fence_after();
-          const float ek = s_ek[un % kUnits][q][row / kKv4Block];
+          const int ek = s_ek[un % kHeldUnits][q][row];
           // the lane's factor (not 0, which times -infinity is NaN)
-          const float e = ek + eq, eh = floorf(0.5f * e);
+          const float e = (float)ek + eq, eh = floorf(0.5f * e);
           const float a = fmaxf(scale_log2 * ex2(eh) * ex2(e - eh), 1.2e-38f);
           // columns below are rows before the token
           const int hidden = min(max((w.t + q) * kTile + row - first, 0), kRows) << p.lg;
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int stage = it & 3, valid = it >> 2 & 31;
       ok = wait(bars.raw[mine_rec][slot], phase, 139) && (!(used >> stage & 1) || wait(bars.k_free[stage], (uses >> stage & 1) ^ 1, 132));
       if (!ok) return;
-      // the record's exponent
+      // the tokens' exponents
       const uint32_t raw = ring + slot * kRaw;
       uint32_t top = 0, sc[NG / 2];
       lds<NG / 2>(sc, raw + 8 * D + lane % kKv4Block * (4 * NG));
@@ -474,13 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lo = sc[i] & 0x7fffu, hi = sc[i] >> 16 & 0x7fffu;
         top = max(top, max(lo >= 0x7f80u ? 0u : lo, hi >= 0x7f80u ? 0u : hi));
       }
-      top = __reduce_max_sync(0xffffffffu, top);
       const int e_k = exponent_of(top);
       const float fk = power_of_2(-e_k);
 #pragma unroll
       for (int i = 0; i < NG / 2; ++i)
         sc[i] = h2_bits(__floats2half2_rn(__uint_as_float(sc[i] << 16) * fk, __uint_as_float(sc[i] & 0xffff0000u) * fk));
-      if (lane == 0) s_ek[un % kUnits][stage][mine_rec] = it & 128 ? kBadRecord : (float)e_k;
+      if (lane < kKv4Block) s_ek[un % kHeldUnits][stage][mine_rec * kKv4Block + lane] = (int8_t)(it & 128 ? kBadRecord : e_k);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int key = mine_rec * kKv4Block + 8 * half + t0;

@@ -209,3 +209,28 @@ def test_keys_of_many_sizes_in_a_round(cb, what, down):
     again, l2 = b.chunk()
     assert torch.equal(again, out) and torch.equal(l2, lse)
     b.plan.close()
+
+
+@pytest.mark.parametrize("up", [20, 40, 100])
+@pytest.mark.parametrize("heads,few,m", [((8, 2, 128), False, 140), ((16, 16, 64), False, 40), ((32, 2, 128), False, 12),
+                                         ((8, 8, 128), True, 8), ((16, 8, 64), True, 4), ((32, 8, 128), True, 2)])
+def test_later_keys_of_any_size_leave_the_weights_of_others(cb, heads, few, m, up):
+    n, late = 300, max(m // 3, 1)
+    at = n - late  # the first such key
+
+    def edit(k, v):
+        k[at:n] *= 2.0**up
+
+    lens, new = ([n] + [50] * 33, [m] + [1] * 33) if few else ([n, 129], [m, 5])
+    b = Values(cb, heads, lens, new, 16, edit=edit)
+    _, lse = b.chunk()
+    b.plan.check()
+    lse[m - late:m] = -float("inf")  # (the rows that see them add nothing to the weights)
+    w = b.weights(lse).cpu().numpy().astype(np.float64)
+    b.plan.check()
+    k, q = b.cached(0)[0][:at], _f64(b.q)[:m - late]
+    ref = serving.attention_weights(q, lse.cpu().numpy().astype(np.float64)[:m - late], k)
+    rel = 2 * b.error(q, k, b.d**-0.5) + 2.0**-20 + 2.0**-22 * 20 + (m * b.hq // b.hkv) * 2.0**-23
+    assert (np.abs(w[0, :, :at] - ref) <= rel * ref + 1e-37).all()
+    assert (w[0, :, at:n] == 0).all() and (w[0, :, n:] == 7).all()
+    b.plan.close()
