@@ -530,12 +530,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(bars.q_raw[st], (qn / kQStages) & 1, 144);
           if (!ok) break;
           const uint32_t at = sQ + st * (kRows * D * 2) + (piece / 8) * kBox;
+          // rows of others, or behind the last, and rows that add nothing, whatever their q is
+          const uint32_t none = __ballot_sync(0xffffffffu, lse == -INFINITY);
           uint32_t v[kLoads][4], top = 0;
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) {
             const int r = row0 + i * kPer;
             lds<4>(v[i], at + r * 128 + (uint32_t)(((piece % 8) ^ (r & 7)) * 16));
-            if (r >= cols) v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0;  // (rows of others, or behind the last)
+            if (none >> (r % 16) & 1) v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0;
             const uint32_t x = __vmaxu2(__vmaxu2(v[i][0] & 0x7fff7fffu, v[i][1] & 0x7fff7fffu), __vmaxu2(v[i][2] & 0x7fff7fffu, v[i][3] & 0x7fff7fffu));
             const uint32_t y = max(x & 0xffffu, x >> 16);
             top = max(top, y >= 0x7f80u ? 0u : y);  // what is no number takes no part
@@ -563,7 +565,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               sts4(at + r * 128 + (uint32_t)(((piece % 8) ^ (r & 7)) * 16), h[0], h[1], h[2], h[3]);
             }
-          // (a row without keys, whose lse is -inf, adds nothing)
           const int ls = qn % kLseStages;
           ok = qn < kLseStages || wait(bars.lse_free[ls], (qn / kLseStages - 1) & 1, 146);
           if (!ok) break;

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_weights_few_kernel(c
     const int place0 = rq.len - tokens, old = rq.len - rq.m, group = 1 << p.lg;
     const int64_t base = ((int64_t)at.s * b.hkv + at.h) * b.width * b.page_size;
     auto row_of = [&](int n) -> int64_t { return q0 + (int64_t)(n >> p.lg) * b.hq + (n & (group - 1)); };
+    bool none = false;  // a row adds nothing, whatever its q is
     load_query<D, NT>(qf, [&](int n) { return b.q + row_of(n) * (D * 2); }, rows, scale_log2, lane);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -172,7 +173,9 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_weights_few_kernel(c
         const int n = 8 * t + 2 * c + e;
         const float x = n < rows ? __ldg(p.lse + row_of(n)) : -INFINITY;
         nl[t][e] = x == -INFINITY ? x : x * -1.4426950408889634f;
+        none = none || (n < rows && x == -INFINITY);
       }
+    none = __any_sync(0xffffffffu, none);
     const int count = min(at.n - at.i, rest);
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_weights_few_kernel(c
         for (int h = 0; h < 2; ++h) lds<NG / 2>(sc[h], rec + 8 * D + (r + 8 * h) * (4 * NG));
         float x[NT][4];
         record_scores<D, NT>(x, qf, rec, sc, p.nibbles, p.higher, lane);
-        const bool some = key0 + kKv4Block - 1 > place0;  // a row that does not see all keys
+        const bool some = key0 + kKv4Block - 1 > place0 || none;  // a row that does not see all keys
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -197,7 +200,8 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_weights_few_kernel(c
           if (some) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (place0 + ((8 * t + 2 * c + e % 2) >> p.lg) < key0 + r + 8 * (e / 2)) x[t][e] = -INFINITY;
+              if (place0 + ((8 * t + 2 * c + e % 2) >> p.lg) < key0 + r + 8 * (e / 2) || nl[t][e % 2] == -INFINITY)
+                x[t][e] = -INFINITY;
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) sum[e / 2] += ex2(x[t][e]);

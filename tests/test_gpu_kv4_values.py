@@ -234,3 +234,22 @@ def test_later_keys_of_any_size_leave_the_weights_of_others(cb, heads, few, m, u
     assert (np.abs(w[0, :, :at] - ref) <= rel * ref + 1e-37).all()
     assert (w[0, :, at:n] == 0).all() and (w[0, :, n:] == 7).all()
     b.plan.close()
+
+
+@pytest.mark.parametrize("what", [np.nan, np.inf, 1e30])
+@pytest.mark.parametrize("heads,few,m", [((8, 2, 128), False, 140), ((16, 16, 64), False, 40), ((8, 8, 128), True, 8),
+                                         ((32, 8, 128), True, 2)])
+def test_a_row_without_lse_adds_nothing_whatever_its_query_is(cb, heads, few, m, what):
+    lens, new = ([300] + [50] * 33, [m] + [1] * 33) if few else ([300, 129], [m, 5])
+    b = Values(cb, heads, lens, new, 16)
+    _, lse = b.chunk()
+    lse[1::2] = -float("inf")
+    want = b.weights(lse)
+    q = b.q.clone()
+    b.q[1::2] = what
+    got = b.weights(lse)
+    assert torch.equal(got, want)
+    b.q = q
+    b.check_weights(got, lse)
+    b.plan.check()
+    b.plan.close()
