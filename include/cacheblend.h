@@ -27,7 +27,9 @@
  *     the current CUDA device; every bf16 tensor pointer must be 16-byte
  *     aligned. Index arrays are int32 on the device.
  *   - The caller owns every tensor. The library owns only what a cb_plan holds
- *     (RoPE cos/sin table, device error word, per-layer scratch); no call
+ *     (RoPE cos/sin table, device error word, per-layer scratch, scratch for
+ *     partial results of the attention calls: at head_dim 128 on 152 SMs 44 MB
+ *     for cb_kv4_chunk_attention, in every plan); no call
  *     other than cb_plan_create / cb_plan_destroy allocates or frees memory.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream). Every compute
  *     call only enqueues work on it and returns without synchronising.
@@ -484,10 +486,12 @@ cb_status cb_kv4_chunk_attention(cb_plan* plan, const void* q, const void* cache
  * j. earlier is added for the tokens that were cached before these rows (j < kv_lens[s] - m); NULL: 0. weights,
  * earlier: float32 [n_seqs, hkv, table_width * P]; earlier may be weights (in place), else they must not overlap.
  * Entries from kv_lens[s] on, and those of a request without rows, are left as they are. A row whose lse is
- * -infinity adds nothing. The order of the sum is fixed, in fp32; the keys are held as in cb_kv4_chunk_attention, each with
- * a power of two of its own (exact for requests of few rows, which run on mma.sync). Recorded, and the limits on sizes,
- * as for cb_kv4_chunk_attention (a key of a bad page gets no weight of these rows). No scratch: calls on one plan may
- * overlap. */
+ * -infinity adds nothing, whatever its q is. The order of the sum is fixed, in fp32; the keys are held as in
+ * cb_kv4_chunk_attention, each with a power of two of its own (exact for requests of few rows, which run on mma.sync),
+ * q to within 2^-39 of the largest magnitude among 128 rows of a request (tokens times heads of g, in order; requests of
+ * few rows: as in cb_kv4_chunk_attention). Recorded, and the limits on sizes, as for cb_kv4_chunk_attention (a key of a bad page gets no
+ * weight of these rows; nothing is computed for requests of many rows that go past the limit together). No scratch: calls
+ * on one plan may overlap. */
 cb_status cb_kv4_attention_weights(cb_plan* plan, const void* q, const float* lse, const void* cache, int32_t n_pages,
                                    int32_t page_size, const int32_t* table, int32_t table_width,
                                    const int32_t* cu_seqlens, const int32_t* kv_lens, int32_t n_seqs, int32_t n_rows,

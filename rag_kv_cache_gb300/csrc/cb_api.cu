@@ -810,10 +810,10 @@ static cb_status kv4_batch(cb_plan* plan, const void* q, const void* cache, int3
   return CB_OK;
 }
 
-static cb_status kv4_chunk(const char* fn, bool probe, cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,
-                                 const int32_t* table, int32_t table_width, const int32_t* cu_seqlens,
-                                 const int32_t* kv_lens, int32_t n_seqs, int32_t n_rows, float scale, void* out,
-                                 float* lse, void* stream) {
+static cb_status kv4_chunk(const char* fn, bool probe, cb_plan* plan, const void* q, const void* cache, int32_t n_pages,
+                           int32_t page_size, const int32_t* table, int32_t table_width, const int32_t* cu_seqlens,
+                           const int32_t* kv_lens, int32_t n_seqs, int32_t n_rows, float scale, void* out, float* lse,
+                           void* stream) {
   CB_TRY(check_plan(plan));
   const auto& c = plan->cfg;
   cb::Kv4Batch b;
@@ -927,7 +927,8 @@ cb_status cb_kv4_keep(cb_plan* plan, const float* weights, int32_t weights_width
                       {budgets, 4 * (int64_t)n_seqs, "budgets"}}));
   CB_TRY(check_device(plan));
   return cuda_status(cb::launch_kv4_keep(weights, weights_width, kv_lens, budgets, n_seqs, plan->cfg.hkv, first, recent,
-                                         kept, kept_width, kept_lens, plan->chunk.sms, plan->err, static_cast<cudaStream_t>(stream)),
+                                         kept, kept_width, kept_lens, plan->chunk.sms, plan->err,
+                                         static_cast<cudaStream_t>(stream)),
                      "cb_kv4_keep");
 }
 

@@ -21,15 +21,15 @@
 // head 66 and 72, 70 and 76, 83 and 83, 85 and 87, 122 and 111; 8 of 8,192 87 and 100, 90 and 103, 131 and 111, 133 and 116,
 // 226 and 184; 40 of 8,192 270 and 346, 275 and 349, 501 and 377.
 //
-// Measured (8 kv heads of 128 dims): 2,048 tokens over 30,720, 32 query heads, 1.08 ms (1.06 TFLOP, 0.52 of the burst rate of a
-// library product, which also has no softmax); 128 over 32,768 113 us; 64 requests of up to 8,453 keys, up to 5
-// tokens of 64 query heads each, 326 us (378 MB, 56 us at the copy rate); 40 requests, 5 with chunks of up to 512
-// tokens, 305 us; three short ones 13 us. What bounds it: a round of 128 keys takes 4,700 cycles with 256 rows, of which the
+// Measured (8 kv heads of 128 dims): 2,048 tokens over 30,720, 32 query heads, 1.05 ms (1.06 TFLOP, 0.53 of the burst rate of a
+// library product, which also has no softmax); 128 over 32,768 111 us; 64 requests of up to 8,453 keys, up to 5
+// tokens of 64 query heads each, 341 us (378 MB, 56 us at the copy rate); 40 requests, 5 with chunks of up to 512
+// tokens, 301 us; three short ones 14 us. What bounds it: a round of 128 keys takes 4,700 cycles with 256 rows, of which the
 // tensor cores work 2,050, and 3,800 with few rows. No role is busy all the time (softmax 2,200 to 2,800 cycles of a tile's
 // round, widening 1,650 to 2,100, scales 1,600 to 1,800, issuing products 1,300 to 2,300); each waits for another one's
 // latency: two tiles of scores, K and V each is all that tensor memory and shared memory hold. Leaving out the softmax of
 // warps without rows gains nothing (24 of 128 rows). Instructions count twice: all roles together run from 32 KB of
-// instruction cache, so loops are rolled and waits are small (2.81 ms with everything unrolled, 1.08 ms now); codes
+// instruction cache, so loops are rolled and waits are small (2.81 ms with everything unrolled, 1.08 ms rolled); codes
 // through registers in place of a ring of records were slower (1.27 against 1.13 ms).
 //
 // Work split: the rounds of all items, in the order request, kv head, rows, keys, are dealt to one CTA per SM in
@@ -323,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &s_abort;
   // Rounds of the it-th item of this CTA, which lies in items[it % kItems]; 0 at the end (or after a failure).
   auto item_at = [&](int it) -> int {
-    return wait_warp(smem_u32(&bars.item[it % kItems]), (it / kItems) & 1, abort_flag, 100, kLimitUs) ? items[it % kItems].rounds : 0;
+    const bool there = wait_warp(smem_u32(&bars.item[it % kItems]), (it / kItems) & 1, abort_flag, 100, kLimitUs);
+    return there ? items[it % kItems].rounds : 0;
   };
   auto leave_item = [&](int it) {
     __syncwarp();
@@ -340,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int seq = s_seq, at = run0 - s_before;  // the request, and the round in it
       const int per_page = b.page_size / kKv4Block;
       const bool acts = lane < 8 && (lane & (p.run - 1)) == 0;
-      int it = 0, r = 0, left = run1 - run0, unit = 0, unit_phase = 0, units = 0, scales = 0;  // units, rounds of scales asked for
+      int it = 0, r = 0, left = run1 - run0, unit = 0, unit_phase = 0;
+      int units = 0, scales = 0;  // units, rounds of scales asked for
       bool ok = true;
       // lane l: record l of the next four rounds' 32
       while (left > 0 && ok) {
@@ -451,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = k - kUnits;
           if (k < kUnits ? k < unit || units >= kUnits : st < scales)
             mbar_wait_inl(k < kUnits ? smem_u32(&raw_full[k]) : smem_u32(&bars.sc_full[st]),
-                          k < kUnits ? (k < unit ? unit_phase : unit_phase ^ 1) : ((scales - 1 - st) / kScaleStages) & 1, abort_flag,
-                          b.err, 103, false, kLimit);
+                          k < kUnits ? (k < unit ? unit_phase : unit_phase ^ 1) : ((scales - 1 - st) / kScaleStages) & 1,
+                          abort_flag, b.err, 103, false, kLimit);
         }
       }
     } else if (warp == kWarpScales) {
@@ -1002,7 +1004,8 @@ cudaError_t launch_t(const Kv4Batch& b, void* out, float* lse, const Kv4ChunkScr
     regs = a.numRegs;
     known.store(regs, std::memory_order_relaxed);
   }
-  if (regs * kThreads < kSoftmaxThreads * (kTiles * kSoftmaxRegs + kWidenWarps / 4 * kWidenRegs + kOtherRegs)) return cudaErrorNotSupported;
+  if (regs * kThreads < kSoftmaxThreads * (kTiles * kSoftmaxRegs + kWidenWarps / 4 * kWidenRegs + kOtherRegs))
+    return cudaErrorNotSupported;
   ChunkParams p;
   p.b = b;
   p.out = static_cast<uint8_t*>(out);
@@ -1026,7 +1029,8 @@ cudaError_t launch_t(const Kv4Batch& b, void* out, float* lse, const Kv4ChunkScr
   cudaError_t e = set_smem_limit_once(kv4_chunk_kernel<D, ONE, PROBE>, (int)smem, configured);
   if (e != cudaSuccess) return e;
   // no more CTAs than there can be rounds
-  const int64_t most = ((int64_t)b.n_rows / ((ONE ? 1 : 2) * kBM >> p.lg) + b.n_seqs) * b.hkv * ((int64_t)b.width * b.page_size / kBN + 1);
+  const int64_t items_at_most = ((int64_t)b.n_rows / ((ONE ? 1 : 2) * kBM >> p.lg) + b.n_seqs) * b.hkv;
+  const int64_t most = items_at_most * ((int64_t)b.width * b.page_size / kBN + 1);
   const int grid = (int)std::min<int64_t>(most, ws.sms);
   e = launch_pdl(kv4_chunk_kernel<D, ONE, PROBE>, dim3((unsigned)grid), dim3(kThreads), smem, s, codes, scales, p);
   if (e != cudaSuccess) return e;

@@ -8,7 +8,8 @@
 // about 6 cycles per (key, kv head) at D = 128. The codes are widened in registers, straight into the
 // operand layout of mma.sync, which leaves shared memory out of it; the batch below takes 12 cycles. (tcgen05 reads
 // at least one operand from shared memory: widened codes there are 512 bytes per key to write and read, 8 cycles at 128
-// bytes per cycle. Above the floor, below what this kernel takes; such a form has not been built.)
+// bytes per cycle. The kernel that does so, kv4_chunk.cu, takes 373 us for requests of one token where this one's form for
+// few rows takes 172: not for that traffic, but for the 3,800 cycles of its roles' chain per 128 keys.)
 //   K   word & 0x000f000f and word & 0x00f000f0 are pairs of fp16 of value nibble * 2^-24 and * 2^-20
 //       (subnormals, exact): 5 instructions per 8 codes;
 //   V   (word >> 4 i & 0x000f000f) | 0x43004300 is a pair of bf16 of value 128 + nibble = 136 + code
@@ -41,9 +42,9 @@
 // with 8 warps), and waits for them alone; no warp waits for another one until the merge.
 //
 // Measured (8 kv heads of 128 dims): 64 requests of up to 8,449 keys, 64 query heads (308 MB, 46 us at
-// the copy rate) 89 us, 0.52 of that rate; one request of 32,897 keys, 32 query heads (38 MB, 5.7 us) 22 us:
-// the first records arrive after 3.3 us, a warp's ten take 9, the merges 5 (a CTA's own, the ticket, the parts).
-// With 16 query heads per kv head (8 warps) and other sizes: 64 requests of 4,225 keys, 8 kv heads of 128 dims, 124 us
+// the copy rate) 89.6 us, 0.51 of that rate (89.2 before the form for few rows); one request of 32,897 keys, 32 query heads
+// (38 MB, 5.7 us) 22 us: the first records arrive after 3.3 us, a warp's ten take 9, the merges 5 (a CTA's own, the ticket, the parts).
+// With 16 query heads per kv head (8 warps) and other sizes: 64 requests of 4,225 keys, 8 kv heads of 128 dims, 125 us
 // against 82 with 8 query heads (0.37 and 0.56 of the copy rate), of 64 dims 90 against 59 (0.26 and 0.39);
 // one request of 32,897 keys, 16 query heads on one kv head of 128 dims, 49 us, of 64 dims 30; one of 4,096,
 // 8,192, 16,384 keys, 8 kv heads of 128 dims, 10, 14 and 17 us.
@@ -712,7 +713,8 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
                                    st.o[t][2 * g + 1][e + 2]);
             if constexpr (CHUNK) {
               const float unit = power_of_2(st.top[t][e] - 133);
-              x = make_float4(x.x * 16777216.0f * unit, x.y * 1048576.0f * unit, x.z * 16777216.0f * unit, x.w * 1048576.0f * unit);
+              x = make_float4(x.x * 16777216.0f * unit, x.y * 1048576.0f * unit, x.z * 16777216.0f * unit,
+                              x.w * 1048576.0f * unit);
             }
             if (CHUNK && to < 0) continue;
             if (whole)
@@ -852,7 +854,8 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1) kv4_decode_kernel(const 
   if (s_last[0] + s_last[1] == 0) return;
   // Both, where this CTA is the last of both, side by side (one after the other they took 3 us longer).
   float* scratch = reinterpret_cast<float*>(smem);  // the partial results in it have been read
-  constexpr int kSums = kMaxCtas * kKv4MaxGroup, kTops = kSums + kKv4MaxGroup, kWeights = kTops + kKv4MaxGroup;  // of one of the two
+  constexpr int kSums = kMaxCtas * kKv4MaxGroup, kTops = kSums + kKv4MaxGroup;
+  constexpr int kWeights = kTops + kKv4MaxGroup;  // of one of the two
   static_assert(kWarps * kWarpBytes<D, NT> >= (2 * kWeights + 2 * 4 * kThreads) * 4, "scratch of the merge over CTAs");
   int c0[2], parts[2], pair[2];
 #pragma unroll

@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) kv4_keep_kern
   __shared__ int sums[CL > 1 ? kBins : 1];  // CL > 1: the row's bins, in the cluster's first block
   pdl_launch_dependents();
   pdl_wait();
-  const int pair = blockIdx.x / CL, rank = blockIdx.x % CL, s = pair / p.hkv, g = pair - s * p.hkv, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int pair = blockIdx.x / CL, rank = blockIdx.x % CL, s = pair / p.hkv, g = pair - s * p.hkv;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int len = __ldg(p.lens + s), given = __ldg(p.budgets + s);
   const int n = min(max(len, 0), p.width);
   const int budget = min(max(given, 0), p.kept_width);

@@ -24,9 +24,10 @@
 // Work split: the tiles of all requests and kv heads in a row, in one contiguous run per CTA, of equal cost (one for a tile,
 // one for each 128 rows that see it; 194 us before, with all of a request's tiles of equal cost, 171 with it).
 //
-// Measured (32 query on 8 kv heads of 128 dims): eight pieces of prompts of up to 1,024 tokens over up to 2,048, 137 us (27 us of
-// products at the burst rate); the last 32 rows over 32,896 tokens 31 us. The first is bound by the latency of the exponentials' loop:
-// a product takes a group 3,900 cycles with three at work (2,730 with two; 512 cycles of a scheduler's transcendental pipe).
+// Measured (32 query on 8 kv heads of 128 dims): eight pieces of prompts of up to 1,024 tokens over up to 2,048, 139 us (27 us
+// of products at the burst rate); the last 32 rows over 32,896 tokens 31 us. The first is bound by the latency of the
+// exponentials' loop: a product takes a group 3,900 cycles with three at work (2,730 with two; 512 cycles of a scheduler's
+// transcendental pipe, which is in use 25% of the time).
 // Scores loaded 32 columns at a time in place of 16 ahead: 140 us.
 //
 // Powers of two: a key is held as k 2^-e_k (its lane's factor; no key, seen or not, takes bits from another), rows as q 2^-e_q
@@ -466,7 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto widen = [&](int un) {
       const uint32_t it = meta >> (9 * slot);
       const int stage = it & 3, valid = it >> 2 & 31;
-      ok = wait(bars.raw[mine_rec][slot], phase, 139) && (!(used >> stage & 1) || wait(bars.k_free[stage], (uses >> stage & 1) ^ 1, 132));
+      ok = wait(bars.raw[mine_rec][slot], phase, 139) &&
+           (!(used >> stage & 1) || wait(bars.k_free[stage], (uses >> stage & 1) ^ 1, 132));
       if (!ok) return;
       // the tokens' exponents
       const uint32_t raw = ring + slot * kRaw;
@@ -538,7 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = row0 + i * kPer;
             lds<4>(v[i], at + r * 128 + (uint32_t)(((piece % 8) ^ (r & 7)) * 16));
             if (none >> (r % 16) & 1) v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0;
-            const uint32_t x = __vmaxu2(__vmaxu2(v[i][0] & 0x7fff7fffu, v[i][1] & 0x7fff7fffu), __vmaxu2(v[i][2] & 0x7fff7fffu, v[i][3] & 0x7fff7fffu));
+            const uint32_t x = __vmaxu2(__vmaxu2(v[i][0] & 0x7fff7fffu, v[i][1] & 0x7fff7fffu),
+                                        __vmaxu2(v[i][2] & 0x7fff7fffu, v[i][3] & 0x7fff7fffu));
             const uint32_t y = max(x & 0xffffu, x >> 16);
             top = max(top, y >= 0x7f80u ? 0u : y);  // what is no number takes no part
           }
@@ -624,7 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t dk = desc_lo(sK + q * kKBytes), dq = desc_lo(sQ + st * (kRows * D * 2)), d = tmem + (uint32_t)(buf * kRows);
+            const uint32_t dk = desc_lo(sK + q * kKBytes), dq = desc_lo(sQ + st * (kRows * D * 2));
+            const uint32_t d = tmem + (uint32_t)(buf * kRows);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
               const uint32_t at = ((ks / 4) * kBox + ks % 4 * 32) >> 4;

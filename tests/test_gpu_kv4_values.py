@@ -79,7 +79,8 @@ def test_each_part_of_a_long_context_has_its_weight_with_few_rows(cb, heads, n):
     # a long request among short ones, on the kernel for few rows: its parts are merged within CTAs and over them
     lens, new = [50] * n, [1] * n
     lens[n // 2] = 20011
-    b = Values(cb, heads, lens, new, 32, qs=0.5, edit=lambda k, v: _segments(k[50 * (n // 2):][:20011], v[50 * (n // 2):][:20011]))
+    at = 50 * (n // 2)
+    b = Values(cb, heads, lens, new, 32, qs=0.5, edit=lambda k, v: _segments(k[at:at + 20011], v[at:at + 20011]))
     out, lse = b.chunk()
     b.plan.check()
     check(b, out, lse, few=True)
