@@ -17,7 +17,7 @@ e + 2^-20 + 2^-22 |lse| + n 2^-24.
 import numpy as np
 import pytest
 import torch
-from test_gpu_kv4_batch import Batch, _f64
+from test_gpu_kv4_batch import Batch, _f64, _i32
 
 from oracle import serving
 
@@ -252,5 +252,63 @@ def test_a_row_without_lse_adds_nothing_whatever_its_query_is(cb, heads, few, m,
     assert torch.equal(got, want)
     b.q = q
     b.check_weights(got, lse)
+    b.plan.check()
+    b.plan.close()
+
+
+def test_as_many_requests_as_a_call_takes(cb):
+    rng = np.random.default_rng(4)
+    n = 16384
+    new = np.ones(n, np.int64)
+    new[rng.integers(n, size=9)] = [0, 2, 3, 5, 9, 40, 70, 130, 0]
+    lens = new + rng.integers(0, 30, n)
+    b = Values(cb, (4, 2, 64), lens, new, 16, pad=1)
+    some = set(rng.integers(n, size=60)) | set(np.flatnonzero(new != 1)) | {0, n - 1}
+    skip = set(range(n)) - some
+    out, lse = b.chunk()
+    b.plan.check()
+    b.check_chunk(out, lse, skip=skip)
+    w = b.weights(lse)
+    b.plan.check()
+    b.check_weights(w, lse, skip=skip)
+    kept = torch.full((n, 2, 20), -5, dtype=torch.int32, device="cuda")
+    kept_lens = torch.zeros(n, dtype=torch.int32, device="cuda")
+    cb.cb_kv4_keep(b.plan, w, b.t_lens, torch.full_like(kept_lens, 20), kept, kept_lens, first=1, recent=2)
+    b.plan.check()
+    assert np.array_equal(kept_lens.cpu().numpy(), np.minimum(lens, 20))
+    wh, kh = w.cpu().numpy(), kept.cpu().numpy()
+    for s in some:
+        for g in range(2):
+            want = serving.keep(wh[s, g], lens[s], 20, 1, 2)
+            assert np.array_equal(kh[s, g, :len(want)], want)
+    b.plan.close()
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_pages_behind_the_first_4_gigabytes(cb, few):
+    # the same requests in a small cache and at the end of one of 6 GB: the same bits
+    lens, new = ([700] * 33, [1] * 33) if few else ([700, 1500], [60, 3])
+    b = Values(cb, (32, 8, 128), lens, new, 256)
+    out, lse = b.chunk()
+    w = b.weights(lse)
+    small, n = b.cache, 6 * 2**30 // b.cache[0].numel()
+    b.cache = torch.zeros((n, *small.shape[1:]), dtype=torch.uint8, device="cuda")
+    b.cache[n - len(small):] = small
+    b.t_table = torch.where(b.t_table >= 0, b.t_table + (n - len(small)), b.t_table)
+    far, l2 = b.chunk()
+    w2 = b.weights(l2)
+    assert torch.equal(far, out) and torch.equal(l2, lse) and torch.equal(w2, w)
+    # the last rows of each request moved to the first pages, read back
+    kept = (b.t_lens[:, None, None] - 20 + torch.arange(20, device="cuda").int()).expand(-1, 8, -1).contiguous()
+    to = torch.arange(len(lens), dtype=torch.int32, device="cuda")[:, None].contiguous()
+    cb.cb_kv4_move(b.plan, b.cache, 256, b.t_table, kept, torch.full_like(b.t_lens, 20), to)
+    b.plan.check()
+    k, v = (torch.zeros(20, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k2, v2 = torch.zeros_like(k), torch.zeros_like(v)
+    for s in range(len(lens)):
+        at = np.arange(lens[s] - 20, lens[s])
+        cb.cb_kv4_load(b.plan, small, 256, _i32(b.table[s][at // 256] * 256 + at % 256), k, v)
+        cb.cb_kv4_load(b.plan, b.cache, 256, _i32(s * 256 + np.arange(20)), k2, v2)
+        assert torch.equal(k, k2) and torch.equal(v, v2)
     b.plan.check()
     b.plan.close()
