@@ -48,7 +48,8 @@
 //
 // Nor may a row depend on keys that it does not see, which may be of any size. Those behind an item's last row count as zeros.
 // Where the keys of a round that some of its rows do not see lie more than 2^20 apart, each has a power of its own for its key
-// and its value, and the round's softmax goes by columns, twice over the scores (`wide`, rare: not made fast).
+// and its value, and the round's softmax goes by columns, three times over the scores (`wide`, rare: not made fast). So do
+// rounds whose scores may pass 2^24.
 #include <math.h>
 
 #include <algorithm>
@@ -85,6 +86,9 @@ constexpr int kSoftmaxRegs = 152, kWidenRegs = 56, kOtherRegs = 64;
 constexpr float kHeadroom = 6.0f;         // log2 of P at the reference: what lies 2^-31 below it still counts
 constexpr float kRescaleThreshold = 6.0f; // log2 units
 constexpr float kHalfSumLimit = 32768.0f; // half a round whose P sums to more moves the reference (P fits fp16)
+// log2 of a row's factor up to which its scores (at most 2^38 times it) stay below 2^24, where a reference of 24 bits is still a number
+// that differences with it can be taken from in one multiply-add.
+constexpr int kFactorExponent = -14;
 constexpr int kValueRange = 60;           // powers of two that a round's e_v may lie below one before it
 
 __host__ __device__ constexpr uint32_t col_s(int i) { return (uint32_t)(i * kBN); }
@@ -602,6 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int r = 0;
     bool ok = true;
     float a_row = 0.0f, e_row = 0.0f;  // scale in log2 units, and the power of two of the row's q
+    float most_e_k = 0.0f;
+    const int scale_exponent = (int)(__float_as_uint(b.scale * 1.4426950408889634f) >> 23 & 255u) - 126;
     // This thread's row of the item's q into shared memory, in fp16 (rows past the item's end repeat its last token).
     auto load_q = [&](const Item& x) {
       const int token = min((ONE ? 0 : ti * tq) + (row >> p.lg), x.tokens - 1);
@@ -620,6 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f0 = power_of_2(by >> 1), f1 = power_of_2(by - (by >> 1));
       a_row = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : b.scale * 1.4426950408889634f;
       e_row = (float)-by;
+      // the keys' exponents up to which the factors of this warp's rows stay within the limit
+      most_e_k = (float)__reduce_min_sync(0xffffffffu, top >= 0x7f80u ? 1000 : kFactorExponent + by - scale_exponent);
       if (ONE && ti == 1) return;  // the first tile's warps write it for both
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
@@ -663,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return fmaxf(a_row * ex2(eh) * ex2(e - eh), 1.2e-38f) + (a_row - a_row);
         };
         const int lim = my_place - (x.j0 + j) * kBN;  // columns c <= lim are visible to this row
-        if (__builtin_expect(info.wide != 0, 0)) {
+        if (__builtin_expect(info.wide != 0 || info.e_k > most_e_k, 0)) {
           tmem_wait_ld(s0);
           const float2* own = p.own + ((int)blockIdx.x * kItems + rr % kItems) * kBN;
           // Columns 16 u .. + 15: their scores (log2 units) and values' exponents.
@@ -673,36 +681,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool gone = info.bad >> u & 1;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 e = __ldcg(own + 16 * u + i);
+              float2 e = make_float2(info.e_k, info.e_v == (float)kNoExponent ? e_b : info.e_v);
+              if (info.wide != 0) e = __ldcg(own + 16 * u + i);
               y[i] = gone || 16 * u + i > lim ? -INFINITY : __uint_as_float(z[i]) * factor(e.x);
               ev[i] = e.y;
             }
           };
           float y[16], ev[16];
-          float most = -INFINITY, top = -INFINITY;  // score; score and value
+          float most = -INFINITY, rel = -INFINITY;  // the largest score; of what a key gives, relative to it
 #pragma unroll 1
           for (int u = 0; u < kBN / 16; ++u) {
             columns(u, y, ev);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              most = fmaxf(most, y[i]);
-              top = fmaxf(top, y[i] + ev[i]);
-            }
+            for (int i = 0; i < 16; ++i) most = fmaxf(most, y[i]);
           }
-          float f = 1.0f;
-          const float mt = top - kHeadroom;
-          if (mt > m_ref + kRescaleThreshold) {  // by whole powers of two, and e_b with it: the sum stays as it is
-            const float by = m_ref == -INFINITY ? 0.0f : ceilf(mt - m_ref);
-            f = ex2(-by);
-            e_b = m_ref == -INFINITY ? floorf(top - most) : e_b + by;
-            m_ref = m_ref == -INFINITY ? mt : m_ref + by;
+#pragma unroll 1
+          for (int u = 0; u < kBN / 16; ++u) {
+            columns(u, y, ev);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) rel = fmaxf(rel, (y[i] - most) + ev[i]);
           }
-          const float over = floorf(most - kHeadroom - (m_ref - e_b));
-          if (over > 30.0f && m_ref != -INFINITY) {  // scores far above those before, of small values
-            l *= ex2(-over);
-            e_b -= over;
+          // The weights are 2^(score - ref) here, and P 2^(ev - e_b) times that: scores may be so large that a value's exponent
+          // is lost beside them, so m_ref = ref + e_b is no measure for both.
+          float ref = m_ref == -INFINITY ? 0.0f : m_ref - e_b, f = 1.0f;
+          if (most != -INFINITY) {
+            const float ref0 = m_ref - e_b;
+            ref = fmaxf(ref0, most - kHeadroom);
+            const float up = ref - ref0;
+            float e = e_b - floorf(up);  // O is not scaled up,
+            const float need = ceilf((most - ref) + rel - kHeadroom);  // and P lies about 2^6 at most
+            if (need > e + kRescaleThreshold) e = need;
+            f = ex2(e_b - e - up);
+            l *= ex2(-up);
+            e_b = e;
+            m_ref = ref + e;
+            has_b = true;
           }
-          has_b = has_b || m_ref != -INFINITY;
           if (j > first && __any_sync(0xffffffffu, f != 1.0f)) {
             if (!wait(bars.o_done[ti], (done - 1) & 1, 116 + ti)) return false;
             tc_fence_after();
@@ -715,15 +729,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_x16(lane_base + col_o(ti, D) + i0, o);
             }
           }
-          const float off = m_ref == -INFINITY ? 0.0f : m_ref, off_l = m_ref == -INFINITY ? 0.0f : m_ref - e_b;
 #pragma unroll 1
           for (int u = 0; u < kBN / 16; ++u) {  // (a column of P lies over scores that have been read)
             columns(u, y, ev);
             uint32_t pk[8];
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-              l += ex2(y[i] - off_l) + ex2(y[i + 1] - off_l);
-              pk[i / 2] = h2_bits(__floats2half2_rn(ex2(y[i] + (ev[i] - off)), ex2(y[i + 1] + (ev[i + 1] - off))));
+              const float a = y[i] - ref, b = y[i + 1] - ref;
+              l += ex2(a) + ex2(b);
+              pk[i / 2] = h2_bits(__floats2half2_rn(ex2(a + (ev[i] - e_b)), ex2(b + (ev[i + 1] - e_b))));
             }
             tmem_st_x8(taddr + 8 * u, pk);
           }
@@ -870,16 +884,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(bars.stats_full, handed++ & 1, 122);
         if (!ok) break;
         tc_fence_after();
-        const float m1 = s_ref[row], l1 = s_sum[row], e1 = s_exp[row], top = fmaxf(m_ref, m1);
+        const float m1 = s_ref[row], l1 = s_sum[row], e1 = s_exp[row];
+        const float r0 = m_ref - e_b, r1 = m1 - e1, r = fmaxf(r0, r1);  // the sums' own references
         odd_too = rounds > 1;
-        if (odd_too && top != -INFINITY) {
-          w0 = ex2(m_ref - top);
-          w1 = ex2(m1 - top);
-          // the sum relative to the larger of both sums' references m - e (within 1)
-          const float e = m1 - e1 > m_ref - e_b ? e1 + floorf(top - m1) : e_b + floorf(top - m_ref);
-          l = l * ex2(m_ref - top + (e - e_b)) + l1 * ex2(m1 - top + (e - e1));
+        if (odd_too && r != -INFINITY) {
+          const float d0 = r0 - r, d1 = r1 - r, e = ceilf(fmaxf(d0 + e_b, d1 + e1));
+          w0 = ex2(d0 + (e_b - e));
+          w1 = ex2(d1 + (e1 - e));
+          l = l * ex2(d0) + l1 * ex2(d1);
           e_b = e;
-          m_ref = top;
+          m_ref = r + e;
         }
       }
       const float e_out = e_b, m_out = m_ref, l_out = l;

@@ -279,7 +279,9 @@ __device__ __forceinline__ void step(State<D, NT>& st, const Query<D, NT>& qf, u
         for (int e = 0; e < 4; ++e) st.o[t][i][e] *= alpha[e % 2];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        pr[t][e] = ex2(fmaf(s[t][e], qf.scale[t][e % 2], -st.m[t][e % 2]));
+        // (CHUNK: scores of any size, whose references are products rounded as here)
+        pr[t][e] = CHUNK ? ex2(__fadd_rn(__fmul_rn(s[t][e], qf.scale[t][e % 2]), -st.m[t][e % 2]))
+                         : ex2(fmaf(s[t][e], qf.scale[t][e % 2], -st.m[t][e % 2]));
       }
     }
   }

@@ -189,6 +189,9 @@ def test_later_keys_of_any_size_do_not_reach_a_row(cb, heads, few, m, what, up):
     out, lse = b.chunk()
     b.plan.check()
     check(b, out, lse, rows_of=lambda s: range(m - late if s == 0 else b.new[s]), few=few)
+    # rows that see them: an average of the values
+    assert torch.isfinite(lse).all()
+    assert (_f64(out)[:m] <= 1.01 * np.repeat(np.abs(b.cached(0)[1]).max(0), b.hq // b.hkv, 0)).all()
     b.plan.close()
 
 
