@@ -467,10 +467,11 @@ cb_status cb_prompt_attention(cb_plan* plan, const void* q, const void* k, const
  * (within 2^-85 of it); softmax weights are rounded to fp16, q to within 2^-35 of its head's largest magnitude. In a
  * batch of many requests those of up to 8 rows per kv head (16 where 16 heads share one) run on mma.sync: codes and
  * K's scales are exact there, a weight times V's scale is rounded to fp16 (to 2^-31 where it is small against the
- * largest scale that the row has met). So a request's results depend on the batch that it comes in, within
- * these roundings; a call's repetition gives the same bits. n_rows (in tiles of 128 / (hq/hkv), each request one more)
- * times hkv times the larger of table_width * P and n_rows over 128 must stay below 2^30, table_width * P may not pass
- * it (CB_ERR_UNSUPPORTED). A bounded wait that gives up records CB_ERR_TIMEOUT.
+ * largest scale that the row has met), and V's codes are summed with an offset (an output is within 2^-16 of the
+ * largest value of its 32 dims). So a request's results depend on the batch that it comes in, within these roundings;
+ * a call's repetition gives the same bits. n_rows (in tiles of 128 / (hq/hkv), each request one more) times hkv times
+ * the larger of table_width * P and n_rows over 128 must stay below 2^30, table_width * P may not pass it
+ * (CB_ERR_UNSUPPORTED). A bounded wait that gives up records CB_ERR_TIMEOUT.
  * Partial results meet in the plan's scratch: calls of this function on one plan must not overlap on the GPU; order them
  * on one stream, or give each stream its own plan (graphs that may run at once too). */
 cb_status cb_kv4_chunk_attention(cb_plan* plan, const void* q, const void* cache, int32_t n_pages, int32_t page_size,
@@ -485,13 +486,13 @@ cb_status cb_kv4_chunk_attention(cb_plan* plan, const void* q, const void* cache
  * summed over the query heads h of g and those of the request's last `window` rows t (0: all its rows) that see
  * j. earlier is added for the tokens that were cached before these rows (j < kv_lens[s] - m); NULL: 0. weights,
  * earlier: float32 [n_seqs, hkv, table_width * P]; earlier may be weights (in place), else they must not overlap.
- * Entries from kv_lens[s] on, and those of a request without rows, are left as they are. A row whose lse is
- * -infinity adds nothing, whatever its q is. The order of the sum is fixed, in fp32; the keys are held as in
+ * Entries from kv_lens[s] on, and those of a request without rows, are left as they are. A row whose lse is -infinity
+ * adds nothing, whatever its q is. The order of the sum is fixed, in fp32; the keys are held as in
  * cb_kv4_chunk_attention, each with a power of two of its own (exact for requests of few rows, which run on mma.sync),
- * q to within 2^-39 of the largest magnitude among 128 rows of a request (tokens times heads of g, in order; requests of
- * few rows: as in cb_kv4_chunk_attention). Recorded, and the limits on sizes, as for cb_kv4_chunk_attention (a key of a bad page gets no
- * weight of these rows; nothing is computed for requests of many rows that go past the limit together). No scratch: calls
- * on one plan may overlap. */
+ * q to within 2^-39 of the largest magnitude among 128 rows of a request (tokens times heads of g, in order; requests
+ * of few rows: as in cb_kv4_chunk_attention). Recorded, and the limits on sizes, as for cb_kv4_chunk_attention (a key
+ * of a bad page gets no weight of these rows; nothing is computed for requests of many rows that go past the limit
+ * together). No scratch: calls on one plan may overlap. */
 cb_status cb_kv4_attention_weights(cb_plan* plan, const void* q, const float* lse, const void* cache, int32_t n_pages,
                                    int32_t page_size, const int32_t* table, int32_t table_width,
                                    const int32_t* cu_seqlens, const int32_t* kv_lens, int32_t n_seqs, int32_t n_rows,

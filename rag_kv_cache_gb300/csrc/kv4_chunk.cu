@@ -23,8 +23,8 @@
 //
 // Measured (8 kv heads of 128 dims): 2,048 tokens over 30,720, 32 query heads, 1.05 ms (1.06 TFLOP, 0.53 of the burst rate of a
 // library product, which also has no softmax); 128 over 32,768 111 us; 64 requests of up to 8,453 keys, up to 5
-// tokens of 64 query heads each, 341 us (378 MB, 56 us at the copy rate); 40 requests, 5 with chunks of up to 512
-// tokens, 301 us; three short ones 14 us. What bounds it: a round of 128 keys takes 4,700 cycles with 256 rows, of which the
+// tokens of 64 query heads each, 347 us (378 MB, 56 us at the copy rate); 40 requests, 5 with chunks of up to 512
+// tokens, 307 us; three short ones 14 us. What bounds it: a round of 128 keys takes 4,700 cycles with 256 rows, of which the
 // tensor cores work 2,050, and 3,800 with few rows. No role is busy all the time (softmax 2,200 to 2,800 cycles of a tile's
 // round, widening 1,650 to 2,100, scales 1,600 to 1,800, issuing products 1,300 to 2,300); each waits for another one's
 // latency: two tiles of scores, K and V each is all that tensor memory and shared memory hold. Leaving out the softmax of
@@ -86,8 +86,8 @@ constexpr int kSoftmaxRegs = 152, kWidenRegs = 56, kOtherRegs = 64;
 constexpr float kHeadroom = 6.0f;         // log2 of P at the reference: what lies 2^-31 below it still counts
 constexpr float kRescaleThreshold = 6.0f; // log2 units
 constexpr float kHalfSumLimit = 32768.0f; // half a round whose P sums to more moves the reference (P fits fp16)
-// log2 of a row's factor up to which its scores (at most 2^38 times it) stay below 2^24, where a reference of 24 bits is still a number
-// that differences with it can be taken from in one multiply-add.
+// log2 of a row's factor up to which its scores (at most 2^38 times it) stay below 2^24: there a reference rounded to 24 bits
+// may still be taken off an exact product.
 constexpr int kFactorExponent = -14;
 constexpr int kValueRange = 60;           // powers of two that a round's e_v may lie below one before it
 

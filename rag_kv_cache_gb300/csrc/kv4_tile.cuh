@@ -75,8 +75,8 @@ __device__ __forceinline__ void widen_word(uint32_t w, __half2 scale, uint32_t (
 // The scales of a tile, in place, by one converged warp: bf16 [128 tokens][K NG, V NG] become, for every 8 tokens, fp16 scales
 // of K [8 tokens][NG], then of V [NG][8 tokens]. Tokens from `valid` on, and those of records in `bad`, get 0. e_k and
 // e_v: the tile's exponents; e_v is least_v at least, and kNoExponent where all values are 0. A V scale that is not finite
-// gets 0, and nan_from[its group] the least of what it was and first + its token. Two passes of four turns, 32 tokens each, in few
-// instructions: the roles of a kernel share its instruction cache.
+// gets 0, and nan_from[its group] the least of what it was and first + its token. Two passes of four turns, 32 tokens each, in
+// few instructions: the roles of a kernel share its instruction cache.
 //   mixed: not every row sees every token. Where one's largest scale then lies more than 2^20 below the tile's, it returns
 // true, each token has exponents of its own, and `own` [128 tokens] holds them (global memory).
 constexpr int kNoExponent = -1000;

@@ -9,7 +9,7 @@
 // order; nothing passes between warps. Requests of more rows are left to kv4_weights.cu.
 //
 // Measured: a step of 64 requests of up to 8,449 tokens, 8 query heads on each of 8 kv heads of 128 dims, added to earlier
-// weights, 67.6 us (171 MB, 25 us at the copy rate; 160 on the other kernel); bound by its warps' own latencies as the decode kernel
+// weights, 68 us (171 MB, 25 us at the copy rate; 160 on the other kernel); bound by its warps' own latencies as the decode kernel
 // is (kv4_decode.cu), whose keys' half this is: issue slots 45%, integer pipe 48%.
 #include <math.h>
 
